@@ -591,6 +591,209 @@ nt_status nt_pair_block_backward_nl(const nt_partition* p, const void* s_in, con
                                     int32_t c_z, int32_t hidden, nt_dtype dtype, void* workspace,
                                     size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Attention among the singles of a sample, biased by the pair state, with
+ * what a training step of it needs: norms and rotation of queries and keys,
+ * the gradients of both, and the optimizer's step. Queries belong to the pair
+ * rows and keys and values to the pair columns of a partition, so a square
+ * partition gives self attention within each packed sample and a rectangular
+ * one attention of N_i queries over M_i keys (N_i = 1: one new token over its
+ * kept keys). Arrays of heads are [tokens, heads, head_dim], a token's heads
+ * contiguous; ld is the distance in elements from one token to the next (0
+ * for heads * head_dim), a multiple of 8, so that queries, keys and values
+ * may be parts of one projected array. Gradients of activations have the
+ * storage type here: they are the operands of the projections' gradients,
+ * whose products round them to bf16 in any case; gradients of the norm
+ * weights are fp32. head_dim is a multiple of 8 and at most 128; heads is a
+ * multiple of kv_heads, and query head h reads key head h / (heads /
+ * kv_heads).
+ * ------------------------------------------------------------------------ */
+
+/* Scaling of the rotation's frequencies f_j = base^(-2j / rot_dim) for
+ * positions past the trained length. */
+typedef enum nt_rotary_scaling {
+  NT_ROTARY_NONE = 0,
+  NT_ROTARY_LINEAR = 1, /* f_j / factor */
+  NT_ROTARY_PARTS = 2   /* f_j k_j + f_j / factor (1 - k_j), k_j = clamp((original f_j / 2 pi
+                         * - beta_slow) / (beta_fast - beta_slow), 0, 1): frequencies that
+                         * turn often within the trained length stay, slow ones are
+                         * interpolated */
+} nt_rotary_scaling;
+
+typedef struct nt_rotary {
+  int32_t rot_dim;  /* rotated dimensions R, even, 2 <= R <= 128 */
+  int32_t scaling;  /* nt_rotary_scaling */
+  double base;      /* > 1 */
+  double factor;    /* >= 1 (LINEAR, PARTS) */
+  double original;  /* trained length, > 0 (PARTS) */
+  double beta_fast; /* > beta_slow >= 0 (PARTS) */
+  double beta_slow;
+  double magnitude; /* multiplies cos and sin, > 0 */
+} nt_rotary;
+
+/*
+ * The rotation's table: table [positions, R] fp32, the R / 2 cosines of a
+ * position, then its sines. Angles are formed in fp64 (at position 10^6 an
+ * fp32 angle is off by 0.03) and each value is rounded once.
+ */
+nt_status nt_rotary_table(const nt_rotary* r, float* table, int64_t positions, void* stream);
+
+typedef struct nt_norm_rotary {
+  int32_t heads;       /* of q, >= 1 */
+  int32_t kv_heads;    /* of k, >= 0; 0: no k (its pointers are not read) */
+  int32_t head_dim;    /* D */
+  int32_t rot_dim;     /* R <= D, even; 0: no rotation (table NULL) */
+  int32_t interleaved; /* 0: pairs (j, j + R/2); 1: pairs (2j, 2j + 1) */
+  float eps;
+  int64_t positions;   /* rows of the table */
+  int64_t ld_q, ld_k;
+  int64_t ld_q_out, ld_k_out; /* of q_out, k_out; in the backward of g_q_in, g_k_in */
+} nt_norm_rotary;
+
+/*
+ * Norm of every query and key head and the position rotation, in one pass:
+ *   y = x / sqrt(mean_d x_d^2 + eps) * w     (w NULL: y = x),
+ *   out_a = y_a cos - y_b sin, out_b = y_b cos + y_a sin for the pairs (a, b)
+ * of the first R dimensions, the others as they are. q: [T, heads, D], k:
+ * [T_cols, kv_heads, D]; w_q, w_k: fp32 [D]. The position of a token is its
+ * index within its sample, or positions_q[T], positions_k[T_cols] (int32,
+ * device) where given; tokens whose position the table does not hold come
+ * back as NaN. Statistics, rotation and products are fp32, rounded once.
+ * q_out may be q and k_out k (with the same ld); other overlaps are rejected.
+ */
+nt_status nt_qk_norm_rotary(const nt_partition* p, const nt_norm_rotary* n, const void* q,
+                            const void* k, const float* w_q, const float* w_k, const float* table,
+                            const int32_t* positions_q, const int32_t* positions_k, void* q_out,
+                            void* k_out, nt_dtype dtype, void* stream);
+
+/* Workspace bytes nt_qk_norm_rotary_backward needs. */
+nt_status nt_qk_norm_rotary_backward_workspace_bytes(const nt_partition* p,
+                                                     const nt_norm_rotary* n, nt_dtype dtype,
+                                                     size_t* bytes);
+
+/*
+ * Gradient of nt_qk_norm_rotary: for the outputs' gradients g_q, g_k
+ * (contiguous, `dtype`) and the same q, k, with h the gradient turned back,
+ * r = 1 / sqrt(mean x^2 + eps) and xhat = x r:
+ *   g_w = sum over tokens and heads of h xhat,
+ *   g_x = r (h w - xhat mean_d(h w xhat))         (w NULL: g_x = h).
+ * g_q_in, g_k_in (`dtype`) may be g_q, g_k (contiguous), not q or k. g_w_q,
+ * g_w_k: fp32 [D], written when w_q, w_k are given, summed in a fixed order.
+ * workspace: device, 16-byte aligned.
+ */
+nt_status nt_qk_norm_rotary_backward(const nt_partition* p, const nt_norm_rotary* n,
+                                     const void* q, const void* k, const void* g_q,
+                                     const void* g_k, const float* w_q, const float* w_k,
+                                     const float* table, const int32_t* positions_q,
+                                     const int32_t* positions_k, void* g_q_in, void* g_k_in,
+                                     float* g_w_q, float* g_w_k, nt_dtype dtype, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+
+typedef struct nt_attention {
+  int32_t heads, kv_heads, head_dim;
+  int32_t causal; /* 1: query r sees key c when c <= r + M_i - N_i */
+  float scale;    /* of the products, finite */
+  int64_t ld_q, ld_k, ld_v;
+} nt_attention;
+
+/* Workspace bytes nt_single_attention needs (0 where the keys are not split). */
+nt_status nt_attention_workspace_bytes(const nt_partition* p, const nt_attention* a,
+                                       nt_dtype dtype, size_t* bytes);
+
+/*
+ * Attention of each pair row's query over the sample's pair columns:
+ *   S[h, o_i + r M_i + c] = scale q[eta_i + r, h] . k[mu_i + c, h'] + bias[h, o_i + r M_i + c],
+ *   lse[eta_i + r, h] = log sum_c exp S,   o[eta_i + r, h] = sum_c exp(S - lse) v[mu_i + c, h'].
+ * q: [T, heads, D]; k, v: [T_cols, kv_heads, D]; bias: [heads, cells] or NULL
+ * (a head's cells are contiguous, so that a tile of scores reads whole
+ * lines); o: [T, heads, D] contiguous; lse: fp32 [T, heads]. A bias of -inf
+ * masks its cell; cells past the causal bound are masked whatever their bias
+ * holds. A row that sees nothing has o = 0 and lse = -inf. Scores,
+ * statistics and sums are fp32; with NT_BF16 the probabilities are rounded
+ * to bf16 before their product with v, and o once. A masked key has weight
+ * zero: its v must be finite (0 times infinity is NaN). o must not overlap
+ * the inputs. workspace: device, 16-byte aligned.
+ */
+nt_status nt_single_attention(const nt_partition* p, const nt_attention* a, const void* q,
+                              const void* k, const void* v, const void* bias, void* o, float* lse,
+                              nt_dtype dtype, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
+/* Gradients of one attention; g_bias may be NULL (bias without gradient). */
+typedef struct nt_attention_grads {
+  void* q;    /* [T, heads, D] */
+  void* k;    /* [T_cols, kv_heads, D] */
+  void* v;    /* [T_cols, kv_heads, D] */
+  void* bias; /* [heads, cells] */
+  int64_t ld_q, ld_k, ld_v;
+} nt_attention_grads;
+
+/* Workspace bytes nt_single_attention_backward needs. */
+nt_status nt_attention_backward_workspace_bytes(const nt_partition* p, const nt_attention* a,
+                                                nt_dtype dtype, size_t* bytes);
+
+/*
+ * Gradients of nt_single_attention for g_o = dL/do ([T, heads, D],
+ * contiguous, `dtype`), from the inputs, o and lse of the forward. The
+ * probabilities are recomputed, P = exp(S - lse):
+ *   delta = sum_d g_o o,  dS = P (g_o . v - delta),
+ *   g_v = P^T g_o, g_q = scale dS k, g_k = scale dS^T q, g_bias = dS,
+ * shared key heads summing over their query heads. Masked cells and rows
+ * with lse = -inf give zero. With NT_BF16 P and dS are rounded to bf16 before
+ * their products. Sums run in a fixed order (no atomics). The gradients
+ * must not overlap the inputs or each other. workspace: device, 16-byte
+ * aligned.
+ */
+nt_status nt_single_attention_backward(const nt_partition* p, const nt_attention* a,
+                                       const void* q, const void* k, const void* v,
+                                       const void* bias, const void* o, const float* lse,
+                                       const void* g_o, const nt_attention_grads* g,
+                                       nt_dtype dtype, void* workspace, size_t workspace_bytes,
+                                       void* stream);
+
+/* Elements of a parameter that share one scale of an 8-bit state. */
+#define NT_ADAMW_BLOCK 256
+
+/* One parameter with its gradient and states. */
+typedef struct nt_adamw_tensor {
+  void* param;       /* [n] of the step's dtype */
+  const float* grad; /* [n] */
+  float* master;     /* [n] fp32 copy that is updated in the parameter's place; NULL: none */
+  void* m;           /* [n] fp32, or 8-bit codes */
+  void* v;           /* [n] fp32, or 8-bit codes of its root */
+  float* m_scale;    /* [ceil(n / NT_ADAMW_BLOCK)] (8 bits), else NULL */
+  float* v_scale;
+  int64_t n;
+} nt_adamw_tensor;
+
+typedef struct nt_adamw {
+  double lr, beta1, beta2, eps, weight_decay;
+  int64_t step;              /* 1 for the first */
+  const int64_t* step_device; /* when given, read by the kernels in step's place */
+  const float* lr_device;     /* when given, read by the kernels in lr's place */
+  int32_t state_bits;        /* 32 or 8 */
+} nt_adamw;
+
+/*
+ * One AdamW step over `count` tensors (host array) in one launch for every
+ * 40 of them:
+ *   m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2,
+ *   w = w (1 - lr weight_decay) - lr (m / (1 - beta1^step)) /
+ *       (sqrt(v / (1 - beta2^step)) + eps),
+ * w the master copy where there is one (the parameter receives it rounded),
+ * else the parameter. Everything is fp32 between reading and writing. With
+ * 8-bit states m and sqrt(v) are kept as e4m3 codes (OCP: 448 the largest)
+ * times a scale for each NT_ADAMW_BLOCK elements, the block's largest
+ * magnitude over 448; a positive sqrt(v) keeps at least the least code, so
+ * that no step divides by a moment rounded away. The step itself uses m and
+ * v before that rounding. A state that is not finite is stored as the NaN
+ * code and left out of its block's scale. With step_device and lr_device a
+ * captured graph follows the values they hold at each replay. No two of the
+ * written arrays may overlap.
+ */
+nt_status nt_adamw_step(const nt_adamw_tensor* tensors, int32_t count, const nt_adamw* h,
+                        nt_dtype dtype, void* stream);
+
 /* Thread-local description of the last failure in this thread ("" if none). */
 const char* nt_last_error(void);
 

@@ -34,6 +34,10 @@ backward.py holds the gradients: Equation 5's sample-weighted squared loss
 (Appendix A.1) over the returned singles and pair state, and the chain rule
 through every step of the block, in reverse.
 
+single.py holds attention among the singles of a sample (biased by the pair
+state) with its gradients, the norms and rotation of its queries and keys, and
+the AdamW step.
+
 The block's transition is z + relu(z W1^T) W2^T (a two-layer ReLU MLP without
 normalisation, the transition of the measured workloads). The paper's own
 pre-normalised SwiGLU transition (Eq. 1 with h o LN; Appendix A.1, expansion
@@ -61,4 +65,8 @@ from .backward import (  # noqa: F401
     block_backward, chain_loss, chain_backward, block_nl, block_backward_nl,
     layer_norm_backward, transition_swiglu_backward, block_swiglu_backward, chain_swiglu_loss,
     chain_swiglu_backward,
+)
+from .single import (  # noqa: F401
+    rotary_frequencies, rotary_table, rotation_matrix, positions_of, norm_rotary,
+    norm_rotary_backward, attention, attention_backward, adamw, e4m3_values, block_scales,
 )

@@ -26,7 +26,12 @@ __all__ = ["NtError", "Partition", "nt_partition_sizes", "nt_make_partition",
            "nt_block_workspace_bytes", "nt_pair_block", "nt_pair_block_noalloc",
            "nt_chain_workspace_bytes",
            "nt_pair_chain", "nt_pair_block_ex", "nt_pair_chain_ex", "nt_pair_block_backward_ex",
-           "nt_block_backward_ex_workspace_bytes", "nt_last_error", "nt_version",
+           "nt_block_backward_ex_workspace_bytes", "nt_rotary_table", "nt_qk_norm_rotary",
+           "nt_qk_norm_rotary_backward", "nt_single_attention", "nt_single_attention_backward",
+           "nt_attention_workspace_bytes", "nt_attention_backward_workspace_bytes",
+           "nt_qk_norm_rotary_backward_workspace_bytes",
+           "AdamwTensors", "nt_adamw_states", "nt_adamw_tensors", "nt_adamw_step",
+           "nt_last_error", "nt_version",
            "NT_F32", "NT_BF16"]
 
 
@@ -880,3 +885,11 @@ def nt_pair_block_backward_ex(p: Partition, s_in, z_out, params: dict, g_s_out, 
         _ptr(g_z_out), _ptr(g_s_in), ctypes.byref(gst), c_s, c_z, hidden, _dtype_code(s_in),
         _ptr(workspace), _nbytes(workspace), _stream(stream, dev)))
     return g_s_in, grads
+
+
+# ------------------------------------- single attention, the optimizer's step
+from ._single import (  # noqa: E402,F401
+    AdamwTensors, nt_adamw_states, nt_adamw_step, nt_adamw_tensors,
+    nt_attention_backward_workspace_bytes, nt_attention_workspace_bytes, nt_qk_norm_rotary,
+    nt_qk_norm_rotary_backward, nt_qk_norm_rotary_backward_workspace_bytes, nt_rotary_table,
+    nt_single_attention, nt_single_attention_backward)

@@ -26,8 +26,11 @@ EXPORTS = ("nt_partition_sizes", "nt_make_partition", "nt_partition_sizes_rect",
            "nt_pair_broadcast_backward", "nt_transition_backward_workspace_bytes",
            "nt_pair_transition_backward", "nt_block_backward_workspace_bytes",
            "nt_pair_block_backward", "nt_block_nl_workspace_bytes", "nt_pair_block_nl",
-           "nt_block_backward_nl_workspace_bytes", "nt_pair_block_backward_nl", "nt_last_error",
-           "nt_version")
+           "nt_block_backward_nl_workspace_bytes", "nt_pair_block_backward_nl",
+           "nt_rotary_table", "nt_qk_norm_rotary", "nt_qk_norm_rotary_backward_workspace_bytes",
+           "nt_qk_norm_rotary_backward", "nt_attention_workspace_bytes", "nt_single_attention",
+           "nt_attention_backward_workspace_bytes", "nt_single_attention_backward",
+           "nt_adamw_step", "nt_last_error", "nt_version")
 
 
 class NtPartition(ctypes.Structure):
@@ -64,6 +67,45 @@ class NtBlockParams(ctypes.Structure):
 
 class NtBlockParamGrads(ctypes.Structure):
     _fields_ = [(k, ctypes.c_void_p) for k in PARAM_NAMES]
+
+
+# nt_rotary_scaling
+NT_ROTARY_NONE, NT_ROTARY_LINEAR, NT_ROTARY_PARTS = 0, 1, 2
+NT_ADAMW_BLOCK = 256
+
+
+class NtRotary(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("scaling", ctypes.c_int32)] + \
+        [(k, ctypes.c_double) for k in ("base", "factor", "original", "beta_fast", "beta_slow",
+                                        "magnitude")]
+
+
+class NtNormRotary(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_int32) for k in ("heads", "kv_heads", "head_dim", "rot_dim",
+                                              "interleaved")] + \
+        [("eps", ctypes.c_float)] + \
+        [(k, ctypes.c_int64) for k in ("positions", "ld_q", "ld_k", "ld_q_out", "ld_k_out")]
+
+
+class NtAttention(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_int32) for k in ("heads", "kv_heads", "head_dim", "causal")] + \
+        [("scale", ctypes.c_float)] + [(k, ctypes.c_int64) for k in ("ld_q", "ld_k", "ld_v")]
+
+
+class NtAttentionGrads(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_void_p) for k in ("q", "k", "v", "bias")] + \
+        [(k, ctypes.c_int64) for k in ("ld_q", "ld_k", "ld_v")]
+
+
+class NtAdamwTensor(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_void_p) for k in ("param", "grad", "master", "m", "v", "m_scale",
+                                               "v_scale")] + [("n", ctypes.c_int64)]
+
+
+class NtAdamw(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_double) for k in ("lr", "beta1", "beta2", "eps", "weight_decay")] + \
+        [("step", ctypes.c_int64), ("step_device", ctypes.c_void_p),
+         ("lr_device", ctypes.c_void_p), ("state_bits", ctypes.c_int32)]
 
 
 _lib = None
@@ -132,6 +174,17 @@ def lib() -> ctypes.CDLL:
         "nt_block_backward_nl_workspace_bytes": [part, i32, i32, i32, i32, ctypes.c_int, P(sz)],
         "nt_pair_block_backward_nl": [part, vp, vp, P(NtBlockWeights), vp, vp, vp, P(NtBlockGrads),
                                       i32, i32, i32, i32, ctypes.c_int, vp, sz, vp],
+        "nt_rotary_table": [P(NtRotary), vp, i64, vp],
+        "nt_qk_norm_rotary": [part, P(NtNormRotary)] + [vp] * 9 + [ctypes.c_int, vp],
+        "nt_qk_norm_rotary_backward_workspace_bytes": [part, P(NtNormRotary), ctypes.c_int, P(sz)],
+        "nt_qk_norm_rotary_backward": [part, P(NtNormRotary)] + [vp] * 13 +
+        [ctypes.c_int, vp, sz, vp],
+        "nt_attention_workspace_bytes": [part, P(NtAttention), ctypes.c_int, P(sz)],
+        "nt_single_attention": [part, P(NtAttention)] + [vp] * 6 + [ctypes.c_int, vp, sz, vp],
+        "nt_attention_backward_workspace_bytes": [part, P(NtAttention), ctypes.c_int, P(sz)],
+        "nt_single_attention_backward": [part, P(NtAttention)] + [vp] * 7 +
+        [P(NtAttentionGrads), ctypes.c_int, vp, sz, vp],
+        "nt_adamw_step": [P(NtAdamwTensor), i32, P(NtAdamw), ctypes.c_int, vp],
     }
     for name, args in sig.items():
         fn = getattr(L, name)

@@ -249,4 +249,37 @@ hipError_t launch_transition_backward_generic(const nt_partition& p, const void*
                                               float* g_z, void* H, void* GH, void* Gb, int c_z,
                                               int hidden, nt_dtype dtype, hipStream_t stream);
 
+// ---- Single attention and the optimizer's step (nt_norm_rotary.hip,
+// nt_attention.hip, nt_attention_bwd.hip, nt_adamw.hip). The distances ld of
+// the structs are filled in (no zeros) in nt_attention, nt_attention_grads.
+hipError_t launch_rotary_table(const nt_rotary& r, float* table, int64_t positions,
+                               hipStream_t stream);
+hipError_t launch_norm_rotary(const nt_partition& p, const nt_norm_rotary& n, const void* q,
+                              const void* k, const float* w_q, const float* w_k,
+                              const float* table, const int32_t* pos_q, const int32_t* pos_k,
+                              void* q_out, void* k_out, nt_dtype dtype, hipStream_t stream);
+size_t norm_rotary_backward_ws_bytes(const nt_partition& p, const nt_norm_rotary& n);
+hipError_t launch_norm_rotary_backward(const nt_partition& p, const nt_norm_rotary& n,
+                                       const void* q, const void* k, const void* g_q,
+                                       const void* g_k, const float* w_q, const float* w_k,
+                                       const float* table, const int32_t* pos_q,
+                                       const int32_t* pos_k, void* g_q_in, void* g_k_in,
+                                       float* g_w_q, float* g_w_k, void* ws, nt_dtype dtype,
+                                       hipStream_t stream);
+size_t attention_ws_bytes(const nt_partition& p, const nt_attention& a, nt_dtype dtype);
+hipError_t launch_attention(const nt_partition& p, const nt_attention& a, const void* q,
+                            const void* k, const void* v, const void* bias, void* o, float* lse,
+                            nt_dtype dtype, void* ws, hipStream_t stream);
+size_t attention_backward_ws_bytes(const nt_partition& p, const nt_attention& a, nt_dtype dtype);
+hipError_t launch_attention_backward(const nt_partition& p, const nt_attention& a, const void* q,
+                                     const void* k, const void* v, const void* bias,
+                                     const void* o, const float* lse, const void* g_o,
+                                     const nt_attention_grads& g, nt_dtype dtype, void* ws,
+                                     hipStream_t stream);
+// Workgroups of one launch of the step: a grid holds fewer than 2^32 threads.
+constexpr uint64_t kAdamwMostBlocks = uint64_t(1) << 23;
+constexpr int64_t kAdamwMostElements = int64_t(1) << 35;  // of one tensor (4,096 a workgroup)
+hipError_t launch_adamw(const nt_adamw_tensor* tensors, int32_t count, const nt_adamw& h,
+                        nt_dtype dtype, hipStream_t stream);
+
 }  // namespace nt
