@@ -711,8 +711,9 @@ nt_status nt_attention_workspace_bytes(const nt_partition* p, const nt_attention
  * holds. A row that sees nothing has o = 0 and lse = -inf. Scores,
  * statistics and sums are fp32; with NT_BF16 the probabilities are rounded
  * to bf16 before their product with v, and o once. A masked key has weight
- * zero: its v must be finite (0 times infinity is NaN). o must not overlap
- * the inputs. workspace: device, 16-byte aligned.
+ * zero, but its k and v must be finite (0 times infinity is NaN). o must not
+ * overlap the inputs. NT_ERR_OVERFLOW: T heads / kv_heads or T_cols of 2^30
+ * or more. workspace: device, 16-byte aligned.
  */
 nt_status nt_single_attention(const nt_partition* p, const nt_attention* a, const void* q,
                               const void* k, const void* v, const void* bias, void* o, float* lse,

@@ -137,6 +137,9 @@ nt_status check_attention(const nt_partition* p, const nt_attention* a, nt_dtype
   out->ld_q = ld_or(a->ld_q, (int64_t)a->heads * a->head_dim);
   out->ld_k = ld_or(a->ld_k, (int64_t)a->kv_heads * a->head_dim);
   out->ld_v = ld_or(a->ld_v, (int64_t)a->kv_heads * a->head_dim);
+  if (!nt::attention_fits(*p, *out))
+    return fail(NT_ERR_OVERFLOW, "%lld rows of %d heads exceed one launch", (long long)p->T,
+                (int)a->heads);
   return NT_OK;
 }
 

@@ -22,7 +22,6 @@ constexpr int kAtWaves = 4;
 constexpr int kAtThreads = 64 * kAtWaves;
 constexpr int kAtRows = 32 * kAtWaves;  // virtual rows of a workgroup
 constexpr int kAtKeys = 64;             // keys of a tile
-constexpr float kLog2e = 1.44269504088896340736f;
 
 struct AtArgs {
   const int64_t *eta, *mu, *cell0;
@@ -37,36 +36,16 @@ struct AtArgs {
   float *part_o, *part_ml;
 };
 
-// Four bias values of a row, from column c on; the ones past `m` as zeros. A row
-// begins at any element, so the four are one unaligned load.
-__device__ __forceinline__ void at_bias4(const bf16* p, int64_t c, int64_t m, float* f) {
-  if (c + 4 <= m) {
-    at_bf16x4 v;
-    __builtin_memcpy(&v, p + c, 8);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) f[e] = (float)v[e];
-  } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) f[e] = c + e < m ? (float)p[c + e] : 0.0f;
-  }
-}
-__device__ __forceinline__ void at_bias4(const float* p, int64_t c, int64_t m, float* f) {
-  if (c + 4 <= m) {
-    __builtin_memcpy(f, p + c, 16);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) f[e] = c + e < m ? p[c + e] : 0.0f;
-  }
-}
-
 template <typename T, int DP, bool BIAS, bool CAUSAL>
 __global__ __launch_bounds__(kAtThreads, sizeof(T) == 4 && DP > 64 ? 1 : 2) void k_attention(AtArgs a) {
   constexpr int KS = DP / 16, DT = DP / 32;
-  constexpr int KP = AtPitch<T, DP>::along, VP = AtPitch<T, DP>::across;
+  typedef AtAlong<T, DP> LK;
+  typedef AtAcross<T, DP> LV;
   typedef typename AtFrag<T>::type Frag;
-  __shared__ __align__(16) T lds[2][kAtKeys * (KP + VP)];
+  __shared__ __align__(16) T lds[2][kAtKeys * (LK::pitch + LV::pitch)];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l32 = lane & 31, h = lane >> 5;
-  const int64_t place = at_place(blockIdx.x, (int64_t)gridDim.x);
+  const int64_t place = at_place((int64_t)blockIdx.y * gridDim.x + blockIdx.x,
+                                 (int64_t)gridDim.x * gridDim.y);
   const int split = (int)(place % a.splits);
   const int64_t ph = place / a.splits;
   const int hk = (int)(ph / a.slots);
@@ -110,7 +89,7 @@ __global__ __launch_bounds__(kAtThreads, sizeof(T) == 4 && DP > 64 ? 1 : 2) void
 #pragma unroll
   for (int s = 0; s < KS; ++s) {
     q[s] = Frag{};
-    if (16 * s + 8 * h < a.D && a.scale != 0.0f) q[s] = at_along(qp, s, h);
+    if (16 * s + 8 * h < a.D && a.scale != 0.0f) q[s] = at_row(qp, s, h);
     if (a.scale < 0.0f) q[s] = -q[s];
   }
   const T* kp = static_cast<const T*>(a.k) + a.mu[i] * a.ld_k + (int64_t)hk * a.D;
@@ -126,8 +105,8 @@ __global__ __launch_bounds__(kAtThreads, sizeof(T) == 4 && DP > 64 ? 1 : 2) void
   if (c0 < c1) {
     sk.load(kp + c0 * a.ld_k, a.ld_k, m - c0, a.D);
     sv.load(vp + c0 * a.ld_v, a.ld_v, m - c0, a.D);
-    sk.template put<KP>(lds[0]);
-    sv.template put<VP>(lds[0] + kAtKeys * KP);
+    sk.template put<LK>(lds[0]);
+    sv.template put<LV>(lds[0] + kAtKeys * LK::pitch);
   }
   __syncthreads();
   int buf = 0;
@@ -138,13 +117,13 @@ __global__ __launch_bounds__(kAtThreads, sizeof(T) == 4 && DP > 64 ? 1 : 2) void
       sv.load(vp + (c + kAtKeys) * a.ld_v, a.ld_v, m - c - kAtKeys, a.D);
     }
     const T* lk = lds[buf];
-    const T* lv = lds[buf] + kAtKeys * KP;
+    const T* lv = lds[buf] + kAtKeys * LK::pitch;
     f32x16 s[2];
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
       s[b] = f32x16{};
 #pragma unroll
-      for (int x = 0; x < KS; ++x) s[b] = at_mma(at_along(lk + (32 * b + l32) * KP, x, h), q[x], s[b]);
+      for (int x = 0; x < KS; ++x) s[b] = at_mma(at_along<LK>(lk, 32 * b + l32, x, h), q[x], s[b]);
     }
     if (BIAS) {
 #pragma unroll
@@ -197,11 +176,11 @@ __global__ __launch_bounds__(kAtThreads, sizeof(T) == 4 && DP > 64 ? 1 : 2) void
       at_pack(s[x / 2], 8 * (x % 2), p);
 #pragma unroll
       for (int d = 0; d < DT; ++d)
-        o[d] = at_mma(at_across<VP>(lv, 16 * x, 32 * d), p, o[d]);
+        o[d] = at_mma(at_across<LV>(lv, 16 * x, 32 * d), p, o[d]);
     }
     if (more) {
-      sk.template put<KP>(lds[buf ^ 1]);
-      sv.template put<VP>(lds[buf ^ 1] + kAtKeys * KP);
+      sk.template put<LK>(lds[buf ^ 1]);
+      sv.template put<LV>(lds[buf ^ 1] + kAtKeys * LK::pitch);
     }
     __syncthreads();
   }
@@ -276,8 +255,8 @@ int splits_of(const nt_partition& p, const nt_attention& a) {
 }
 
 template <typename T, int DP>
-hipError_t run(const AtArgs& x, bool causal, int64_t grid, hipStream_t stream) {
-  const unsigned g = (unsigned)grid;
+hipError_t run(const AtArgs& x, bool causal, hipStream_t stream) {
+  const dim3 g((unsigned)(x.slots * x.splits), x.K);
   if (x.bias) {
     if (causal) k_attention<T, DP, true, true><<<g, kAtThreads, 0, stream>>>(x);
     else k_attention<T, DP, true, false><<<g, kAtThreads, 0, stream>>>(x);
@@ -290,12 +269,11 @@ hipError_t run(const AtArgs& x, bool causal, int64_t grid, hipStream_t stream) {
 
 template <typename T>
 hipError_t forward(const nt_partition& p, const nt_attention& a, AtArgs x, hipStream_t stream) {
-  const int64_t grid = x.slots * x.K * x.splits;
   hipError_t e;
-  if (a.head_dim <= 32) e = run<T, 32>(x, a.causal, grid, stream);
-  else if (a.head_dim <= 64) e = run<T, 64>(x, a.causal, grid, stream);
-  else if (a.head_dim <= 96) e = run<T, 96>(x, a.causal, grid, stream);
-  else e = run<T, 128>(x, a.causal, grid, stream);
+  if (a.head_dim <= 32) e = run<T, 32>(x, a.causal, stream);
+  else if (a.head_dim <= 64) e = run<T, 64>(x, a.causal, stream);
+  else if (a.head_dim <= 96) e = run<T, 96>(x, a.causal, stream);
+  else e = run<T, 128>(x, a.causal, stream);
   if (e != hipSuccess || x.splits == 1) return e;
   const int64_t rows = p.T * a.heads, blocks = (rows + 3) / 4;
   k_attention_join<T><<<(unsigned)(blocks < (1 << 20) ? blocks : (1 << 20)), 256, 0, stream>>>(
@@ -304,6 +282,14 @@ hipError_t forward(const nt_partition& p, const nt_attention& a, AtArgs x, hipSt
 }
 
 }  // namespace
+
+// A grid holds fewer than 2^32 threads an axis.
+bool attention_fits(const nt_partition& p, const nt_attention& a) {
+  const int64_t most = (int64_t(1) << 32) / kAtThreads;
+  // the smallest tiles that any kernel here or of the gradients takes
+  return at_slots(p.T, p.B, a.heads / a.kv_heads, 64) * splits_of(p, a) < most &&
+         at_slots(p.T_cols, p.B, 1, 64) < most;
+}
 
 size_t attention_ws_bytes(const nt_partition& p, const nt_attention& a, nt_dtype) {
   const int s = splits_of(p, a);

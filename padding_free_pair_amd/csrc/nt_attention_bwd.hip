@@ -1,182 +1,428 @@
-// Gradients of the attention of pair rows over pair columns.
+// Gradients of the attention of pair rows over pair columns, which recompute
+// the probabilities from the scores and the forward's log sums.
 //
-// One wave for a query and head (its gradient and the bias's), and one for a
-// key and key head, which takes the queries of its group's heads in turn; the
-// lanes hold the head's dimensions, two each.
+// Two kernels, each with its own order of sums and no atomics, so results
+// repeat bit by bit. The first owns 32 virtual rows (queries of one key head,
+// as in the forward) in a wave and walks over the keys: it forms S^T = K Q^T and
+// dP^T = V G^T, and their dS^T is, as it stands, the fragment of
+// g_q^T += K^T dS^T. It also leaves each row's delta for the second, which owns
+// 32 keys in a wave and walks over the virtual rows: S = Q K^T and dP = G V^T
+// give P and dS as fragments of g_v^T += G^T P and g_k^T += Q^T dS; the rows of
+// all query heads of the group pass by, so shared key heads sum in registers.
+// The scores and dP are formed twice (7 products instead of 5); joining the
+// walks would need g_q summed across workgroups.
 #include <math.h>
 
-#include "nt_device.hpp"
+#include "nt_attention_tile.hpp"
 #include "nt_internal.hpp"
 
 namespace nt {
 namespace {
 
-constexpr int kAbThreads = 256;
+constexpr int kAbTile = 64;  // rows of a tile in LDS: keys, or virtual rows
 
-__device__ __forceinline__ float ab_wave_sum(float v) {
-#pragma unroll
-  for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m);
-  return v;
-}
-
-template <typename T> struct AbArgs {
+struct AbArgs {
   const int64_t *eta, *mu, *cell0;
-  const int32_t *rows, *cols, *row_sample;
-  int64_t T_rows, T_cols, cells;
+  const int32_t *rows, *cols;
+  int64_t cells, slots, ld_q, ld_k, ld_v, ld_gq, ld_gk, ld_gv;
   int B, H, K, D, causal;
   float scale;
-  int64_t ld_q, ld_k, ld_v, ld_gq, ld_gk, ld_gv;
-  const T *q, *k, *v, *bias, *o, *g_o;
+  const void *q, *k, *v, *bias, *o, *g_o;
   const float* lse;
-  T *g_q, *g_k, *g_v, *g_bias;
+  void *g_q, *g_k, *g_v, *g_bias;
+  float* delta;  // [T, H]
 };
 
-template <typename T> __device__ __forceinline__ void ab_load(const T* p, int D, float* f) {
-  const int lane = threadIdx.x & 63;
+template <typename T>
+__device__ __forceinline__ float ab_dot(const bf16x8& a, const bf16x8& b) {
+  float s = 0.0f;
 #pragma unroll
-  for (int e = 0; e < 2; ++e) f[e] = lane + 64 * e < D ? to_f32(p[lane + 64 * e]) : 0.0f;
+  for (int j = 0; j < 8; ++j) s += (float)a[j] * (float)b[j];
+  return s;
 }
-template <typename T> __device__ __forceinline__ void ab_store(T* p, int D, const float* f) {
-  const int lane = threadIdx.x & 63;
+template <typename T> __device__ __forceinline__ float ab_dot(const f32x8& a, const f32x8& b) {
+  float s = 0.0f;
 #pragma unroll
-  for (int e = 0; e < 2; ++e)
-    if (lane + 64 * e < D) p[lane + 64 * e] = from_f32<T>(f[e]);
-}
-__device__ __forceinline__ float ab_dot(const float* a, const float* b) {
-  return ab_wave_sum(a[0] * b[0] + a[1] * b[1]);
+  for (int j = 0; j < 8; ++j) s += a[j] * b[j];
+  return s;
 }
 
-template <typename T> __global__ __launch_bounds__(kAbThreads) void k_attention_bwd_q(AbArgs<T> a) {
-  const int lane = threadIdx.x & 63;
-  for (int64_t w = (int64_t)blockIdx.x * (kAbThreads / 64) + (threadIdx.x >> 6);
-       w < a.T_rows * a.H; w += (int64_t)gridDim.x * (kAbThreads / 64)) {
-    const int64_t t = w / a.H;
-    const int h = (int)(w - t * a.H), hk = h / (a.H / a.K);
-    const int i = a.row_sample[t];
-    const int64_t r = t - a.eta[i], m = a.cols[i];
-    const int64_t past = a.causal ? r + 1 + m - a.rows[i] : m;
-    const int64_t cell = (int64_t)h * a.cells + a.cell0[i] + r * m;
-    float q[2], o[2], g[2], acc[2] = {0.0f, 0.0f};
-    ab_load(a.q + t * a.ld_q + h * a.D, a.D, q);
-    ab_load(a.o + w * a.D, a.D, o);
-    ab_load(a.g_o + w * a.D, a.D, g);
-    const float delta = ab_dot(g, o), lse = a.lse[w];
-    for (int64_t c = 0; c < m; ++c) {
-      float ds = 0.0f;
-      if (c < past && lse != -INFINITY) {
-        float k[2], v[2];
-        ab_load(a.k + (a.mu[i] + c) * a.ld_k + hk * a.D, a.D, k);
-        ab_load(a.v + (a.mu[i] + c) * a.ld_v + hk * a.D, a.D, v);
-        float s = ab_dot(q, k) * a.scale;
-        if (a.bias) s += to_f32(a.bias[cell + c]);
-        const float p = expf(s - lse);
-        ds = p > 0.0f ? p * (ab_dot(g, v) - delta) : p;
-        acc[0] += ds * k[0];
-        acc[1] += ds * k[1];
-      }
-      if (a.g_bias && lane == 0) a.g_bias[cell + c] = from_f32<T>(ds);
-    }
-    acc[0] *= a.scale;
-    acc[1] *= a.scale;
-    ab_store(a.g_q + t * a.ld_gq + h * a.D, a.D, acc);
+// g_q of 32 virtual rows a wave, and their delta.
+template <typename T, int DP, int WAVES, bool BIAS>
+__global__ __launch_bounds__(64 * WAVES, sizeof(T) == 4 && DP > 64 ? 1 : 2) void k_attention_bwd_q(
+    AbArgs a) {
+  constexpr int KS = DP / 16, DT = DP / 32, THREADS = 64 * WAVES, ROWS = 32 * WAVES;
+  typedef AtBoth<T, DP> L;
+  constexpr int TILE = kAbTile * L::pitch;
+  typedef typename AtFrag<T>::type Frag;
+  __shared__ __align__(16) T lds[2][2 * TILE];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l32 = lane & 31, h = lane >> 5;
+  const int64_t place = at_place((int64_t)blockIdx.y * gridDim.x + blockIdx.x,
+                                 (int64_t)gridDim.x * gridDim.y);
+  const int hk = (int)(place / a.slots);
+  const int64_t slot = place - hk * a.slots;
+  const int G = a.H / a.K;
+  const int i = at_sample_of(a.eta, a.B, G, ROWS, slot);
+  const int64_t tile = slot - (a.eta[i] * G / ROWS + i);
+  const int64_t n = a.rows[i], m = a.cols[i];
+  if (tile * ROWS >= n * G) return;
+
+  const int64_t vr = tile * ROWS + wave * 32 + l32;
+  const bool live = vr < n * G;
+  const int64_t r = (live ? vr : n * G - 1) / G;
+  const int hq = hk * G + (int)((live ? vr : n * G - 1) % G);
+  const int64_t t = a.eta[i] + r, at = t * a.H + hq;
+  const int64_t seen64 = a.causal ? r + 1 + m - n : m;
+  const int64_t seen = seen64 < 0 ? 0 : seen64 < m ? seen64 : m;
+  int64_t c1 = m;
+  if (a.causal) {
+    const int64_t vlast = tile * ROWS + ROWS - 1;
+    const int64_t rl = (vlast < n * G ? vlast : n * G - 1) / G;
+    c1 = rl + 1 + m - n;
+    c1 = c1 < 0 ? 0 : c1 < m ? c1 : m;
   }
+  const int64_t seen0 = a.causal ? __builtin_amdgcn_readfirstlane((int)seen) : m;
+
+  Frag q[KS], g[KS];
+  const T* qp = static_cast<const T*>(a.q) + t * a.ld_q + (int64_t)hq * a.D;
+  const T* gp = static_cast<const T*>(a.g_o) + at * a.D;
+  const T* op = static_cast<const T*>(a.o) + at * a.D;
+  float delta = 0.0f;
+#pragma unroll
+  for (int s = 0; s < KS; ++s) {
+    q[s] = g[s] = Frag{};
+    if (16 * s + 8 * h < a.D) {
+      q[s] = at_row(qp, s, h);
+      g[s] = at_row(gp, s, h);
+      delta += ab_dot<T>(g[s], at_row(op, s, h));
+    }
+  }
+  delta += __shfl_xor(delta, 32);
+  if (live && h == 0) a.delta[at] = delta;
+  // a row that saw nothing gives nothing
+  const float lse = a.lse[at] == -INFINITY ? INFINITY : a.lse[at];
+  const T* kp = static_cast<const T*>(a.k) + a.mu[i] * a.ld_k + (int64_t)hk * a.D;
+  const T* vp = static_cast<const T*>(a.v) + a.mu[i] * a.ld_v + (int64_t)hk * a.D;
+  const T* bp = BIAS ? static_cast<const T*>(a.bias) + hq * a.cells + a.cell0[i] + r * m : nullptr;
+
+  f32x16 gq[DT];
+#pragma unroll
+  for (int d = 0; d < DT; ++d) gq[d] = f32x16{};
+  const float unit = a.scale * kLog2e, base = lse * kLog2e;
+  AtStage<T, kAbTile, DP, THREADS> sk, sv;
+  if (c1 > 0) {
+    sk.load(kp, a.ld_k, m, a.D);
+    sv.load(vp, a.ld_v, m, a.D);
+    sk.template put<L>(lds[0]);
+    sv.template put<L>(lds[0] + TILE);
+  }
+  __syncthreads();
+  int buf = 0;
+  for (int64_t c = 0; c < c1; c += kAbTile, buf ^= 1) {
+    const bool more = c + kAbTile < c1;
+    if (more) {
+      sk.load(kp + (c + kAbTile) * a.ld_k, a.ld_k, m - c - kAbTile, a.D);
+      sv.load(vp + (c + kAbTile) * a.ld_v, a.ld_v, m - c - kAbTile, a.D);
+    }
+    const T* lk = lds[buf];
+    const T* lv = lds[buf] + TILE;
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      f32x16 s = f32x16{}, dp = f32x16{};
+#pragma unroll
+      for (int x = 0; x < KS; ++x) {
+        s = at_mma(at_along<L>(lk, 32 * b + l32, x, h), q[x], s);
+        dp = at_mma(at_along<L>(lv, 32 * b + l32, x, h), g[x], dp);
+      }
+      if (BIAS) {
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          float f[4];
+          at_bias4(bp, c + 32 * b + 8 * y + 4 * h, m, f);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            s[4 * y + e] = (s[4 * y + e] * a.scale + f[e] - lse) * kLog2e;
+        }
+      } else {
+#pragma unroll
+        for (int x = 0; x < 16; ++x) s[x] = s[x] * unit - base;
+      }
+#pragma unroll
+      for (int x = 0; x < 16; ++x) s[x] = __builtin_amdgcn_exp2f(s[x]) * (dp[x] - delta);
+      if (c + kAbTile > seen0) {
+#pragma unroll
+        for (int x = 0; x < 16; ++x)
+          if (c + 32 * b + 8 * (x / 4) + 4 * h + x % 4 >= seen) s[x] = 0.0f;
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        Frag f;
+        at_pack(s, 8 * x, f);
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+          gq[d] = at_mma(at_across<L>(lk, 32 * b + 16 * x, 32 * d), f, gq[d]);
+      }
+    }
+    if (more) {
+      sk.template put<L>(lds[buf ^ 1]);
+      sv.template put<L>(lds[buf ^ 1] + TILE);
+    }
+    __syncthreads();
+  }
+  if (!live) return;
+  T* out = static_cast<T*>(a.g_q) + t * a.ld_gq + (int64_t)hq * a.D;
+#pragma unroll
+  for (int d = 0; d < DT; ++d)
+#pragma unroll
+    for (int y = 0; y < 4; ++y)
+      if (32 * d + 8 * y + 4 * h < a.D)
+        at_store4(out + 32 * d + 8 * y + 4 * h, gq[d][4 * y] * a.scale, gq[d][4 * y + 1] * a.scale,
+                  gq[d][4 * y + 2] * a.scale, gq[d][4 * y + 3] * a.scale);
 }
 
-template <typename T> __global__ __launch_bounds__(kAbThreads) void k_attention_bwd_k(AbArgs<T> a) {
-  for (int64_t w = (int64_t)blockIdx.x * (kAbThreads / 64) + (threadIdx.x >> 6);
-       w < a.T_cols * a.K; w += (int64_t)gridDim.x * (kAbThreads / 64)) {
-    const int64_t t = w / a.K;
-    const int hk = (int)(w - t * a.K), G = a.H / a.K;
-    const int i = find_segment(a.mu, 0, a.B, t);
-    const int64_t c = t - a.mu[i], m = a.cols[i], n = a.rows[i];
-    float k[2], v[2], gk[2] = {0.0f, 0.0f}, gv[2] = {0.0f, 0.0f};
-    ab_load(a.k + t * a.ld_k + hk * a.D, a.D, k);
-    ab_load(a.v + t * a.ld_v + hk * a.D, a.D, v);
-    int64_t r0 = a.causal ? c - m + n : 0;
-    if (r0 < 0) r0 = 0;
-    for (int h = hk * G; h < (hk + 1) * G; ++h)
-      for (int64_t r = r0; r < n; ++r) {
-        const int64_t at = (a.eta[i] + r) * a.H + h;
-        const float lse = a.lse[at];
-        if (lse == -INFINITY) continue;
-        float q[2], o[2], g[2];
-        ab_load(a.q + (a.eta[i] + r) * a.ld_q + h * a.D, a.D, q);
-        ab_load(a.o + at * a.D, a.D, o);
-        ab_load(a.g_o + at * a.D, a.D, g);
-        float s = ab_dot(q, k) * a.scale;
-        if (a.bias) s += to_f32(a.bias[(int64_t)h * a.cells + a.cell0[i] + r * m + c]);
-        const float p = expf(s - lse);
-        const float ds = p > 0.0f ? p * (ab_dot(g, v) - ab_dot(g, o)) : p;
+// What the second kernel keeps of each virtual row of a tile.
+struct AbRow {
+  float lse, delta;
+  int seen;      // keys that the row sees
+  int64_t cell;  // its first cell of the bias
+};
+
+// g_k and g_v of 32 keys a wave, and the bias's gradient.
+template <typename T, int DP, int WAVES, bool BIAS>
+__global__ __launch_bounds__(64 * WAVES, DP > 64 ? 1 : 2) void k_attention_bwd_k(AbArgs a) {
+  constexpr int KS = DP / 16, DT = DP / 32, THREADS = 64 * WAVES, KEYS = 32 * WAVES;
+  typedef AtBoth<T, DP> L;
+  constexpr int TILE = kAbTile * L::pitch;
+  constexpr int kVec = 16 / sizeof(T), kPieces = kAbTile * DP / kVec / THREADS;
+  typedef typename AtFrag<T>::type Frag;
+  typedef T Vec __attribute__((ext_vector_type(16 / sizeof(T))));
+  __shared__ __align__(16) T lds[2][2 * TILE];
+  __shared__ AbRow meta[2][kAbTile];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l32 = lane & 31, h = lane >> 5;
+  const int64_t place = at_place((int64_t)blockIdx.y * gridDim.x + blockIdx.x,
+                                 (int64_t)gridDim.x * gridDim.y);
+  const int hk = (int)(place / a.slots);
+  const int64_t slot = place - hk * a.slots;
+  const int G = a.H / a.K;
+  const int i = at_sample_of(a.mu, a.B, 1, KEYS, slot);
+  const int64_t tile = slot - (a.mu[i] / KEYS + i);
+  const int64_t n = a.rows[i], m = a.cols[i];
+  if (tile * KEYS >= m) return;
+  const int64_t k0 = tile * KEYS + wave * 32, key = k0 + l32;
+  const bool live = key < m;
+  const int64_t t = a.mu[i] + (live ? key : m - 1);
+
+  Frag k[KS], v[KS];
+  const T* kp = static_cast<const T*>(a.k) + t * a.ld_k + (int64_t)hk * a.D;
+  const T* vp = static_cast<const T*>(a.v) + t * a.ld_v + (int64_t)hk * a.D;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          gk[e] += a.scale * ds * q[e];
-          gv[e] += p * g[e];
+  for (int s = 0; s < KS; ++s) {
+    k[s] = v[s] = Frag{};
+    if (16 * s + 8 * h < a.D) {
+      k[s] = at_row(kp, s, h);
+      v[s] = at_row(vp, s, h);
+    }
+  }
+  f32x16 gk[DT], gv[DT];
+#pragma unroll
+  for (int d = 0; d < DT; ++d) gk[d] = gv[d] = f32x16{};
+  const float unit = a.scale * kLog2e;
+
+  // tiles of virtual rows; the rows before the first that sees a key of this
+  // workgroup are passed over, their cells of the bias's gradient are zero
+  const int64_t all = n * G;
+  int64_t first = 0;
+  if (a.causal) {
+    const int64_t r = tile * KEYS - (m - n);
+    first = r <= 0 ? 0 : r >= n ? all : r * G;
+  }
+  if (BIAS && a.g_bias && live) {
+    for (int64_t x = h; x < first; x += 2)
+      static_cast<T*>(a.g_bias)[(hk * G + x % G) * a.cells + a.cell0[i] + x / G * m + key] =
+          from_f32<T>(0.0f);
+  }
+  const T* qb = static_cast<const T*>(a.q) + a.eta[i] * a.ld_q + (int64_t)hk * G * a.D;
+  const T* gb = static_cast<const T*>(a.g_o) + (a.eta[i] * a.H + (int64_t)hk * G) * a.D;
+  const bool pow2 = (G & (G - 1)) == 0;
+  const int shift = __builtin_ctz(G);
+  Vec sq[kPieces], sg[kPieces];
+  AbRow row;
+  auto fetch = [&](int64_t x0) {  // the tile of virtual rows from x0 on
+#pragma unroll
+    for (int u = 0; u < kPieces; ++u) {
+      const int e = (threadIdx.x + u * THREADS) * kVec, c = e % DP;
+      const int64_t x = x0 + e / DP < all ? x0 + e / DP : all - 1;
+      const uint32_t xr = pow2 ? (uint32_t)(x >> shift) : (uint32_t)((uint64_t)x / G);
+      const int xg = (int)(x - (int64_t)xr * G);
+      sq[u] = sg[u] = Vec{};
+      if (c < a.D) {
+        sq[u] = *reinterpret_cast<const Vec*>(qb + xr * a.ld_q + xg * a.D + c);
+        sg[u] = *reinterpret_cast<const Vec*>(gb + ((int64_t)xr * a.H + xg) * a.D + c);
+      }
+    }
+    if (threadIdx.x < kAbTile) {
+      const int64_t x = x0 + threadIdx.x;
+      const bool in = x < all;
+      const int64_t xr = (in ? x : all - 1) / G;
+      const int xh = hk * G + (int)((in ? x : all - 1) - xr * G);
+      const int64_t xt = (a.eta[i] + xr) * a.H + xh;
+      const float z = a.lse[xt];
+      row.lse = in && z != -INFINITY ? z : INFINITY;
+      row.delta = a.delta[xt];
+      const int64_t s = a.causal ? xr + 1 + m - n : m;
+      row.seen = in ? (int)(s < 0 ? 0 : s < m ? s : m) : 0;
+      row.cell = xh * a.cells + a.cell0[i] + xr * m;
+    }
+  };
+  auto put = [&](int b) {
+#pragma unroll
+    for (int u = 0; u < kPieces; ++u) {
+      const int e = (threadIdx.x + u * THREADS) * kVec, p = L::at(e / DP, e % DP);
+      *reinterpret_cast<Vec*>(lds[b] + p) = sq[u];
+      *reinterpret_cast<Vec*>(lds[b] + TILE + p) = sg[u];
+    }
+    if (threadIdx.x < kAbTile) meta[b][threadIdx.x] = row;
+  };
+  if (first < all) {
+    fetch(first);
+    put(0);
+  }
+  __syncthreads();
+  int buf = 0;
+  for (int64_t x0 = first; x0 < all; x0 += kAbTile, buf ^= 1) {
+    const bool more = x0 + kAbTile < all;
+    if (more) fetch(x0 + kAbTile);
+    const T* lq = lds[buf];
+    const T* lg = lds[buf] + TILE;
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      f32x16 s = f32x16{}, dp = f32x16{};
+#pragma unroll
+      for (int x = 0; x < KS; ++x) {
+        s = at_mma(at_along<L>(lq, 32 * b + l32, x, h), k[x], s);
+        dp = at_mma(at_along<L>(lg, 32 * b + l32, x, h), v[x], dp);
+      }
+#pragma unroll
+      for (int x = 0; x < 16; ++x) {
+        const AbRow& w = meta[buf][32 * b + 8 * (x / 4) + 4 * h + x % 4];
+        float p;
+        if (BIAS) {
+          const float f = live ? to_f32(static_cast<const T*>(a.bias)[w.cell + key]) : 0.0f;
+          p = __builtin_amdgcn_exp2f((s[x] * a.scale + f - w.lse) * kLog2e);
+        } else {
+          p = __builtin_amdgcn_exp2f(s[x] * unit - w.lse * kLog2e);
+        }
+        const bool in = key < w.seen;
+        s[x] = in ? p : 0.0f;
+        dp[x] = in ? p * (dp[x] - w.delta) : 0.0f;
+        if (BIAS && a.g_bias && live && x0 + 32 * b + 8 * (x / 4) + 4 * h + x % 4 < all)
+          static_cast<T*>(a.g_bias)[w.cell + key] = from_f32<T>(dp[x]);
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        Frag fp, fs;
+        at_pack(s, 8 * x, fp);
+        at_pack(dp, 8 * x, fs);
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+          gv[d] = at_mma(at_across<L>(lg, 32 * b + 16 * x, 32 * d), fp, gv[d]);
+          gk[d] = at_mma(at_across<L>(lq, 32 * b + 16 * x, 32 * d), fs, gk[d]);
         }
       }
-    ab_store(a.g_k + t * a.ld_gk + hk * a.D, a.D, gk);
-    ab_store(a.g_v + t * a.ld_gv + hk * a.D, a.D, gv);
+    }
+    if (more) put(buf ^ 1);
+    __syncthreads();
   }
+  if (!live) return;
+  T* ok = static_cast<T*>(a.g_k) + t * a.ld_gk + (int64_t)hk * a.D;
+  T* ov = static_cast<T*>(a.g_v) + t * a.ld_gv + (int64_t)hk * a.D;
+#pragma unroll
+  for (int d = 0; d < DT; ++d)
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+      const int c = 32 * d + 8 * y + 4 * h;
+      if (c < a.D) {
+        at_store4(ok + c, gk[d][4 * y] * a.scale, gk[d][4 * y + 1] * a.scale,
+                  gk[d][4 * y + 2] * a.scale, gk[d][4 * y + 3] * a.scale);
+        at_store4(ov + c, gv[d][4 * y], gv[d][4 * y + 1], gv[d][4 * y + 2], gv[d][4 * y + 3]);
+      }
+    }
+}
+
+template <typename T, int DP, int WAVES, bool BIAS>
+hipError_t run(const nt_partition& p, AbArgs x, hipStream_t stream) {
+  if (p.T) {
+    x.slots = at_slots(p.T, p.B, x.H / x.K, 32 * WAVES);
+    k_attention_bwd_q<T, DP, WAVES, BIAS>
+        <<<dim3((unsigned)x.slots, x.K), 64 * WAVES, 0, stream>>>(x);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (p.T_cols) {
+    x.slots = at_slots(p.T_cols, p.B, 1, 32 * WAVES);
+    k_attention_bwd_k<T, DP, WAVES, BIAS>
+        <<<dim3((unsigned)x.slots, x.K), 64 * WAVES, 0, stream>>>(x);
+  }
+  return hipGetLastError();
+}
+
+template <typename T, int DP>
+hipError_t run(const nt_partition& p, const AbArgs& x, hipStream_t stream) {
+  return x.bias ? run<T, DP, 4, true>(p, x, stream) : run<T, DP, 4, false>(p, x, stream);
 }
 
 template <typename T>
-hipError_t backward(const nt_partition& p, const nt_attention& x, const void* q, const void* k,
-                    const void* v, const void* bias, const void* o, const float* lse,
-                    const void* g_o, const nt_attention_grads& g, hipStream_t stream) {
-  AbArgs<T> a;
-  a.eta = p.single_offsets;
-  a.mu = p.col_offsets;
-  a.cell0 = p.pair_offsets;
-  a.rows = p.lengths;
-  a.cols = p.col_lengths;
-  a.row_sample = p.row_sample;
-  a.T_rows = p.T;
-  a.T_cols = p.T_cols;
-  a.cells = p.cells;
-  a.B = p.B;
-  a.H = x.heads;
-  a.K = x.kv_heads;
-  a.D = x.head_dim;
-  a.causal = x.causal;
-  a.scale = x.scale;
-  a.ld_q = x.ld_q;
-  a.ld_k = x.ld_k;
-  a.ld_v = x.ld_v;
-  a.ld_gq = g.ld_q;
-  a.ld_gk = g.ld_k;
-  a.ld_gv = g.ld_v;
-  a.q = (const T*)q;
-  a.k = (const T*)k;
-  a.v = (const T*)v;
-  a.bias = (const T*)bias;
-  a.o = (const T*)o;
-  a.g_o = (const T*)g_o;
-  a.lse = lse;
-  a.g_q = (T*)g.q;
-  a.g_k = (T*)g.k;
-  a.g_v = (T*)g.v;
-  a.g_bias = (T*)g.bias;
-  auto grid = [](int64_t items) {
-    const int64_t b = (items + kAbThreads / 64 - 1) / (kAbThreads / 64);
-    return (unsigned)(b < (1 << 20) ? b : (1 << 20));
-  };
-  if (p.T) k_attention_bwd_q<T><<<grid(p.T * x.heads), kAbThreads, 0, stream>>>(a);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess || p.T_cols == 0) return e;
-  k_attention_bwd_k<T><<<grid(p.T_cols * x.kv_heads), kAbThreads, 0, stream>>>(a);
-  return hipGetLastError();
+hipError_t backward(const nt_partition& p, const AbArgs& x, hipStream_t stream) {
+  if (x.D <= 32) return run<T, 32>(p, x, stream);
+  if (x.D <= 64) return run<T, 64>(p, x, stream);
+  if (x.D <= 96) return run<T, 96>(p, x, stream);
+  return run<T, 128>(p, x, stream);
 }
 
 }  // namespace
 
-size_t attention_backward_ws_bytes(const nt_partition&, const nt_attention&, nt_dtype) { return 0; }
+size_t attention_backward_ws_bytes(const nt_partition& p, const nt_attention& a, nt_dtype) {
+  return (size_t)p.T * a.heads * sizeof(float);
+}
 
 hipError_t launch_attention_backward(const nt_partition& p, const nt_attention& a, const void* q,
                                      const void* k, const void* v, const void* bias,
                                      const void* o, const float* lse, const void* g_o,
-                                     const nt_attention_grads& g, nt_dtype dtype, void*,
+                                     const nt_attention_grads& g, nt_dtype dtype, void* ws,
                                      hipStream_t stream) {
-  return dtype == NT_BF16 ? backward<bf16>(p, a, q, k, v, bias, o, lse, g_o, g, stream)
-                          : backward<float>(p, a, q, k, v, bias, o, lse, g_o, g, stream);
+  AbArgs x;
+  x.eta = p.single_offsets;
+  x.mu = p.col_offsets;
+  x.cell0 = p.pair_offsets;
+  x.rows = p.lengths;
+  x.cols = p.col_lengths;
+  x.cells = p.cells;
+  x.slots = 0;
+  x.ld_q = a.ld_q;
+  x.ld_k = a.ld_k;
+  x.ld_v = a.ld_v;
+  x.ld_gq = g.ld_q;
+  x.ld_gk = g.ld_k;
+  x.ld_gv = g.ld_v;
+  x.B = p.B;
+  x.H = a.heads;
+  x.K = a.kv_heads;
+  x.D = a.head_dim;
+  x.causal = a.causal;
+  x.scale = a.scale;
+  x.q = q;
+  x.k = k;
+  x.v = v;
+  x.bias = bias;
+  x.o = o;
+  x.g_o = g_o;
+  x.lse = lse;
+  x.g_q = g.q;
+  x.g_k = g.k;
+  x.g_v = g.v;
+  x.g_bias = g.bias;
+  x.delta = static_cast<float*>(ws);
+  return dtype == NT_BF16 ? backward<bf16>(p, x, stream) : backward<float>(p, x, stream);
 }
 
 }  // namespace nt

@@ -16,6 +16,8 @@
 
 namespace nt {
 
+constexpr float kLog2e = 1.44269504088896340736f;
+
 typedef float f32x8 __attribute__((ext_vector_type(8)));
 typedef short at_i16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 at_bf16x4 __attribute__((ext_vector_type(4)));
@@ -34,29 +36,53 @@ __device__ __forceinline__ f32x16 at_mma(const f32x8& a, const f32x8& b, f32x16 
   return c;
 }
 
-// Row pitches in LDS, in elements. Fragments along a row (16 bytes a lane, 16
-// rows at once) want a pitch of an odd number of 16 bytes; fragments across
-// rows want, in bf16, four rows of 64 bytes on different banks (a pitch of 64
-// bytes modulo 256 or an odd multiple), in fp32 rows 4 apart on different
-// halves of the banks.
-template <typename T, int DP> struct AtPitch;
-template <int DP> struct AtPitch<bf16, DP> {
-  static constexpr int along = DP + 8;
-  static constexpr int across = DP % 64 == 0 ? DP + 32 : DP;
+// Where a tile of token rows keeps its elements in LDS, by the fragments that
+// are read from it, without bank conflicts.
+// AtAlong: along rows only. 16 rows are read at once, 16 bytes of each: a pitch
+// of an odd number of 16 bytes.
+template <typename T, int DP> struct AtAlong {
+  static constexpr int pitch = DP + 16 / (int)sizeof(T);
+  static __device__ __forceinline__ int at(int r, int c) { return r * pitch + c; }
 };
-template <int DP> struct AtPitch<float, DP> {
-  static constexpr int along = DP + 4;
-  static constexpr int across = DP + 8;
+// AtAcross: across rows only. bf16: four rows at once, 64 bytes of each: a pitch
+// of 64 bytes modulo 256, or of 192. fp32: rows 4 apart on different halves of
+// the banks.
+template <typename T, int DP> struct AtAcross {
+  static constexpr int pitch = sizeof(T) == 4 ? DP + 8 : DP % 64 == 0 ? DP + 32 : DP;
+  static __device__ __forceinline__ int at(int r, int c) { return r * pitch + c; }
 };
+// AtBoth: both. bf16: rows of 16-byte chunks, chunk c of row r at c ^ f(r);
+// along a row, 16 rows read one chunk each, which f must send to the 16 chunks
+// of 256 bytes; across rows, 4 rows read 4 neighbouring chunks each, which f
+// must send to the 4 different 64-byte pieces: f's high bits are r's low ones.
+// fp32: AtAlong's pitch, which serves the other kind half.
+template <typename T, int DP> struct AtBoth;
+template <int DP> struct AtBoth<bf16, DP> {
+  static constexpr int pitch = DP == 96 ? 128 : DP;
+  static __device__ __forceinline__ int at(int r, int c) {
+    const int f = pitch == 128 ? (r & 3) << 2 | ((r >> 2) & 3)
+                  : pitch == 64 ? ((r >> 1) & 1) << 2 | ((r >> 2) & 3) : (r >> 2) & 3;
+    return r * pitch + (((c >> 3) ^ f) << 3) + (c & 7);
+  }
+};
+template <int DP> struct AtBoth<float, DP> : AtAlong<float, DP> {};
 
-// Fragment of row `row` of a tile, values 16 s + 8 h ..
-__device__ __forceinline__ bf16x8 at_along(const bf16* row, int s, int h) {
+// Values 16 s + 8 h .. of a row in global memory as a fragment.
+__device__ __forceinline__ bf16x8 at_row(const bf16* row, int s, int h) {
   return *reinterpret_cast<const bf16x8*>(row + 16 * s + 8 * h);
 }
-__device__ __forceinline__ f32x8 at_along(const float* row, int s, int h) {
+__device__ __forceinline__ f32x8 at_row(const float* row, int s, int h) {
   const f32x4 a = *reinterpret_cast<const f32x4*>(row + 16 * s + 8 * h);
   const f32x4 b = *reinterpret_cast<const f32x4*>(row + 16 * s + 8 * h + 4);
   return f32x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+}
+
+// Fragment along row r of a tile, values 16 s + 8 h ..
+template <typename L> __device__ __forceinline__ bf16x8 at_along(const bf16* tile, int r, int s, int h) {
+  return *reinterpret_cast<const bf16x8*>(tile + L::at(r, 16 * s + 8 * h));
+}
+template <typename L> __device__ __forceinline__ f32x8 at_along(const float* tile, int r, int s, int h) {
+  return at_row(tile + L::at(r, 0), s, h);
 }
 
 // Four bf16 by the transposing LDS read: within each 16 lanes, lane j's
@@ -69,22 +95,22 @@ __device__ __forceinline__ at_bf16x4 at_read_tr(const bf16* p) {
 
 // Fragment across rows: column c0 + l % 32 of the tile, rows r0 + {4 h + 0 ..
 // 3, 8 + 4 h + 0 .. 3} (the order of a product's results).
-template <int PITCH>
-__device__ __forceinline__ bf16x8 at_across(const bf16* tile, int r0, int c0) {
+template <typename L> __device__ __forceinline__ bf16x8 at_across(const bf16* tile, int r0, int c0) {
   const int lane = threadIdx.x & 63, h = lane >> 5, q = lane & 15, g = lane >> 4;
-  const bf16* p = tile + (r0 + 4 * h + (q >> 2)) * PITCH + c0 + 16 * (g & 1) + 4 * (q & 3);
-  const at_bf16x4 a = at_read_tr(p), b = at_read_tr(p + 8 * PITCH);
+  const int r = r0 + 4 * h + (q >> 2), c = c0 + 16 * (g & 1) + 4 * (q & 3);
+  const at_bf16x4 a = at_read_tr(tile + L::at(r, c));
+  const at_bf16x4 b = at_read_tr(tile + L::at(r + 8, c));
   return bf16x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
 }
-template <int PITCH>
-__device__ __forceinline__ f32x8 at_across(const float* tile, int r0, int c0) {
+template <typename L> __device__ __forceinline__ f32x8 at_across(const float* tile, int r0, int c0) {
   const int lane = threadIdx.x & 63, h = lane >> 5;
-  const float* p = tile + (r0 + 4 * h) * PITCH + c0 + (lane & 31);
+  constexpr int P = L::pitch;
+  const float* p = tile + (r0 + 4 * h) * P + c0 + (lane & 31);
   f32x8 f;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    f[j] = p[j * PITCH];
-    f[4 + j] = p[(8 + j) * PITCH];
+    f[j] = p[j * P];
+    f[4 + j] = p[(8 + j) * P];
   }
   return f;
 }
@@ -107,6 +133,28 @@ __device__ __forceinline__ void at_store4(float* p, float a, float b, float c, f
   *reinterpret_cast<at_f32x4*>(p) = at_f32x4{a, b, c, d};
 }
 
+// Four bias values of a row, from column c on; the ones past `m` as zeros. A row
+// begins at any element, so the four are one unaligned load.
+__device__ __forceinline__ void at_bias4(const bf16* p, int64_t c, int64_t m, float* f) {
+  if (c + 4 <= m) {
+    at_bf16x4 v;
+    __builtin_memcpy(&v, p + c, 8);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f[e] = (float)v[e];
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f[e] = c + e < m ? (float)p[c + e] : 0.0f;
+  }
+}
+__device__ __forceinline__ void at_bias4(const float* p, int64_t c, int64_t m, float* f) {
+  if (c + 4 <= m) {
+    __builtin_memcpy(f, p + c, 16);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f[e] = c + e < m ? p[c + e] : 0.0f;
+  }
+}
+
 // A tile of ROWS token rows of D elements (D <= DP) on its way to LDS: pieces
 // of 16 bytes, one after another over the THREADS threads. Rows past the
 // last one read the last one (their weight is zero).
@@ -127,11 +175,11 @@ template <typename T, int ROWS, int DP, int THREADS> struct AtStage {
       if (c < D) v[u] = *reinterpret_cast<const Vec*>(first + row * ld + c);
     }
   }
-  template <int PITCH> __device__ __forceinline__ void put(T* tile) const {
+  template <typename L> __device__ __forceinline__ void put(T* tile) const {
 #pragma unroll
     for (int u = 0; u < kPieces; ++u) {
       const int at = (threadIdx.x + u * THREADS) * kVec;
-      *reinterpret_cast<Vec*>(tile + (at / DP) * PITCH + at % DP) = v[u];
+      *reinterpret_cast<Vec*>(tile + L::at(at / DP, at % DP)) = v[u];
     }
   }
 };

@@ -266,6 +266,7 @@ hipError_t launch_norm_rotary_backward(const nt_partition& p, const nt_norm_rota
                                        const int32_t* pos_k, void* g_q_in, void* g_k_in,
                                        float* g_w_q, float* g_w_k, void* ws, nt_dtype dtype,
                                        hipStream_t stream);
+bool attention_fits(const nt_partition& p, const nt_attention& a);  // a launch's limits
 size_t attention_ws_bytes(const nt_partition& p, const nt_attention& a, nt_dtype dtype);
 hipError_t launch_attention(const nt_partition& p, const nt_attention& a, const void* q,
                             const void* k, const void* v, const void* bias, void* o, float* lse,
