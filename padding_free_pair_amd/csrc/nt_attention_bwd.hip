@@ -180,25 +180,23 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 4 && DP > 64 ? 1 : 2) void
                   gq[d][4 * y + 2] * a.scale, gq[d][4 * y + 3] * a.scale);
 }
 
-// What the second kernel keeps of each virtual row of a tile.
-struct AbRow {
-  float lse, delta;
-  int seen;      // keys that the row sees
-  int64_t cell;  // its first cell of the bias
-};
-
-// g_k and g_v of 32 keys a wave, and the bias's gradient.
-template <typename T, int DP, int WAVES, bool BIAS>
-__global__ __launch_bounds__(64 * WAVES, DP > 64 ? 1 : 2) void k_attention_bwd_k(AbArgs a) {
-  constexpr int KS = DP / 16, DT = DP / 32, THREADS = 64 * WAVES, KEYS = 32 * WAVES;
+// g_k and g_v of 32 keys a wave, and the bias's gradient. KW waves of a
+// workgroup own different keys; RW waves own the same keys and take different
+// blocks of 32 rows of each tile, and their sums are joined at the end in
+// order, so few keys still fill the card.
+template <typename T, int DP, int KW, int RW, bool BIAS>
+__global__ __launch_bounds__(64 * KW * RW, DP > 64 ? 1 : 2) void k_attention_bwd_k(AbArgs a) {
+  constexpr int KS = DP / 16, DT = DP / 32, THREADS = 64 * KW * RW, KEYS = 32 * KW;
+  constexpr int NB = RW == 1 ? 2 : 1, ROWS = 32 * RW * NB;  // blocks of a wave, rows of a tile
   typedef AtBoth<T, DP> L;
-  constexpr int TILE = kAbTile * L::pitch;
-  constexpr int kVec = 16 / sizeof(T), kPieces = kAbTile * DP / kVec / THREADS;
+  constexpr int TILE = ROWS * L::pitch;
+  constexpr int kLds = 2 * 2 * TILE * (int)sizeof(T), kJoin = (RW - 1) * KW * 2 * DP * 32 * 4;
   typedef typename AtFrag<T>::type Frag;
-  typedef T Vec __attribute__((ext_vector_type(16 / sizeof(T))));
-  __shared__ __align__(16) T lds[2][2 * TILE];
-  __shared__ AbRow meta[2][kAbTile];
+  __shared__ __align__(16) char lds_bytes[kLds > kJoin ? kLds : kJoin];
+  __shared__ __align__(16) float stats[2][2][ROWS];  // [buffer][log sum, delta]
+  T* lds = reinterpret_cast<T*>(lds_bytes);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l32 = lane & 31, h = lane >> 5;
+  const int kw = wave / RW, rw = wave % RW;
   const int64_t place = at_place((int64_t)blockIdx.y * gridDim.x + blockIdx.x,
                                  (int64_t)gridDim.x * gridDim.y);
   const int hk = (int)(place / a.slots);
@@ -208,9 +206,9 @@ __global__ __launch_bounds__(64 * WAVES, DP > 64 ? 1 : 2) void k_attention_bwd_k
   const int64_t tile = slot - (a.mu[i] / KEYS + i);
   const int64_t n = a.rows[i], m = a.cols[i];
   if (tile * KEYS >= m) return;
-  const int64_t k0 = tile * KEYS + wave * 32, key = k0 + l32;
+  const int64_t k0 = tile * KEYS + kw * 32, key = k0 + l32;
   const bool live = key < m;
-  const int64_t t = a.mu[i] + (live ? key : m - 1);
+  const int64_t keyc = live ? key : m - 1, t = a.mu[i] + keyc;
 
   Frag k[KS], v[KS];
   const T* kp = static_cast<const T*>(a.k) + t * a.ld_k + (int64_t)hk * a.D;
@@ -228,95 +226,112 @@ __global__ __launch_bounds__(64 * WAVES, DP > 64 ? 1 : 2) void k_attention_bwd_k
   for (int d = 0; d < DT; ++d) gk[d] = gv[d] = f32x16{};
   const float unit = a.scale * kLog2e;
 
-  // tiles of virtual rows; the rows before the first that sees a key of this
-  // workgroup are passed over, their cells of the bias's gradient are zero
-  const int64_t all = n * G;
+  // Rows from the first that sees a key of this workgroup, for each query head
+  // in turn; the cells of the bias's gradient before it are zero.
+  const int64_t ahead = a.causal ? m - n : 0;  // row r sees keys up to r + ahead
   int64_t first = 0;
   if (a.causal) {
-    const int64_t r = tile * KEYS - (m - n);
-    first = r <= 0 ? 0 : r >= n ? all : r * G;
+    first = tile * KEYS - ahead;
+    first = first < 0 ? 0 : first < n ? first : n;
   }
-  if (BIAS && a.g_bias && live) {
-    for (int64_t x = h; x < first; x += 2)
-      static_cast<T*>(a.g_bias)[(hk * G + x % G) * a.cells + a.cell0[i] + x / G * m + key] =
-          from_f32<T>(0.0f);
-  }
-  const T* qb = static_cast<const T*>(a.q) + a.eta[i] * a.ld_q + (int64_t)hk * G * a.D;
-  const T* gb = static_cast<const T*>(a.g_o) + (a.eta[i] * a.H + (int64_t)hk * G) * a.D;
-  const bool pow2 = (G & (G - 1)) == 0;
-  const int shift = __builtin_ctz(G);
-  Vec sq[kPieces], sg[kPieces];
-  AbRow row;
-  auto fetch = [&](int64_t x0) {  // the tile of virtual rows from x0 on
-#pragma unroll
-    for (int u = 0; u < kPieces; ++u) {
-      const int e = (threadIdx.x + u * THREADS) * kVec, c = e % DP;
-      const int64_t x = x0 + e / DP < all ? x0 + e / DP : all - 1;
-      const uint32_t xr = pow2 ? (uint32_t)(x >> shift) : (uint32_t)((uint64_t)x / G);
-      const int xg = (int)(x - (int64_t)xr * G);
-      sq[u] = sg[u] = Vec{};
-      if (c < a.D) {
-        sq[u] = *reinterpret_cast<const Vec*>(qb + xr * a.ld_q + xg * a.D + c);
-        sg[u] = *reinterpret_cast<const Vec*>(gb + ((int64_t)xr * a.H + xg) * a.D + c);
-      }
+  const T* bias = static_cast<const T*>(a.bias) + a.cell0[i];
+  T* g_bias = static_cast<T*>(a.g_bias) + a.cell0[i];
+  if (BIAS && a.g_bias && live)
+    for (int g = 0; g < G; ++g)
+      for (int64_t r = 2 * rw + h; r < first; r += 2 * RW)
+        g_bias[(int64_t)(hk * G + g) * a.cells + r * m + key] = from_f32<T>(0.0f);
+  const int64_t per_head = (n - first + ROWS - 1) / ROWS, tiles = per_head * G;
+
+  AtStage<T, ROWS, DP, THREADS> sq, sg;
+  float row_lse = 0.0f, row_delta = 0.0f;
+  T b_now[NB][16], b_next[NB][16];  // bias of this lane's key at its rows
+  auto fetch = [&](int64_t j) {
+    const int hq = hk * G + (int)(j / per_head);
+    const int64_t r0 = first + j % per_head * ROWS, t0 = a.eta[i] + r0;
+    sq.load(static_cast<const T*>(a.q) + t0 * a.ld_q + (int64_t)hq * a.D, a.ld_q, n - r0, a.D);
+    sg.load(static_cast<const T*>(a.g_o) + (t0 * a.H + hq) * a.D, (int64_t)a.H * a.D, n - r0, a.D);
+    if (threadIdx.x < ROWS) {
+      const bool in = r0 + threadIdx.x < n;
+      const int64_t at = (t0 + (in ? threadIdx.x : 0)) * a.H + hq;
+      const float z = a.lse[at];
+      // a row that saw nothing, or is none, gives nothing
+      row_lse = in && z != -INFINITY ? (BIAS ? z : z * kLog2e) : INFINITY;
+      row_delta = a.delta[at];
     }
-    if (threadIdx.x < kAbTile) {
-      const int64_t x = x0 + threadIdx.x;
-      const bool in = x < all;
-      const int64_t xr = (in ? x : all - 1) / G;
-      const int xh = hk * G + (int)((in ? x : all - 1) - xr * G);
-      const int64_t xt = (a.eta[i] + xr) * a.H + xh;
-      const float z = a.lse[xt];
-      row.lse = in && z != -INFINITY ? z : INFINITY;
-      row.delta = a.delta[xt];
-      const int64_t s = a.causal ? xr + 1 + m - n : m;
-      row.seen = in ? (int)(s < 0 ? 0 : s < m ? s : m) : 0;
-      row.cell = xh * a.cells + a.cell0[i] + xr * m;
+    if (BIAS) {
+      const T* p = bias + (int64_t)hq * a.cells + r0 * m + keyc;
+      const bool whole = r0 + ROWS <= n;
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int x = 0; x < 16; ++x) {
+          const int64_t r = 32 * (rw * NB + b) + 8 * (x / 4) + 4 * h + x % 4;
+          b_next[b][x] = p[(whole || r < n - r0 ? r : n - 1 - r0) * m];
+        }
     }
   };
-  auto put = [&](int b) {
-#pragma unroll
-    for (int u = 0; u < kPieces; ++u) {
-      const int e = (threadIdx.x + u * THREADS) * kVec, p = L::at(e / DP, e % DP);
-      *reinterpret_cast<Vec*>(lds[b] + p) = sq[u];
-      *reinterpret_cast<Vec*>(lds[b] + TILE + p) = sg[u];
+  auto put = [&](int buf) {
+    sq.template put<L>(lds + buf * 2 * TILE);
+    sg.template put<L>(lds + buf * 2 * TILE + TILE);
+    if (threadIdx.x < ROWS) {
+      stats[buf][0][threadIdx.x] = row_lse;
+      stats[buf][1][threadIdx.x] = row_delta;
     }
-    if (threadIdx.x < kAbTile) meta[b][threadIdx.x] = row;
   };
-  if (first < all) {
-    fetch(first);
+  if (tiles > 0) {
+    fetch(0);
     put(0);
   }
   __syncthreads();
   int buf = 0;
-  for (int64_t x0 = first; x0 < all; x0 += kAbTile, buf ^= 1) {
-    const bool more = x0 + kAbTile < all;
-    if (more) fetch(x0 + kAbTile);
-    const T* lq = lds[buf];
-    const T* lg = lds[buf] + TILE;
+  for (int64_t j = 0; j < tiles; ++j, buf ^= 1) {
+    const bool more = j + 1 < tiles;
+    const int hq = hk * G + (int)(j / per_head);
+    const int64_t r0 = first + j % per_head * ROWS;
+    if (BIAS) {
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int x = 0; x < 16; ++x) b_now[b][x] = b_next[b][x];
+    }
+    if (more) fetch(j + 1);
+    const T* lq = lds + buf * 2 * TILE;
+    const T* lg = lq + TILE;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const int rb = 32 * (rw * NB + b);  // first row of the block in the tile
       f32x16 s = f32x16{}, dp = f32x16{};
 #pragma unroll
       for (int x = 0; x < KS; ++x) {
-        s = at_mma(at_along<L>(lq, 32 * b + l32, x, h), k[x], s);
-        dp = at_mma(at_along<L>(lg, 32 * b + l32, x, h), v[x], dp);
+        s = at_mma(at_along<L>(lq, rb + l32, x, h), k[x], s);
+        dp = at_mma(at_along<L>(lg, rb + l32, x, h), v[x], dp);
       }
 #pragma unroll
-      for (int x = 0; x < 16; ++x) {
-        const AbRow& w = meta[buf][32 * b + 8 * (x / 4) + 4 * h + x % 4];
-        float p;
-        if (BIAS) {
-          const float f = live ? to_f32(static_cast<const T*>(a.bias)[w.cell + key]) : 0.0f;
-          p = __builtin_amdgcn_exp2f((s[x] * a.scale + f - w.lse) * kLog2e);
-        } else {
-          p = __builtin_amdgcn_exp2f(s[x] * unit - w.lse * kLog2e);
+      for (int y = 0; y < 4; ++y) {
+        const f32x4 z = *reinterpret_cast<const f32x4*>(&stats[buf][0][rb + 8 * y + 4 * h]);
+        const f32x4 d = *reinterpret_cast<const f32x4*>(&stats[buf][1][rb + 8 * y + 4 * h]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int x = 4 * y + e;
+          const float p = __builtin_amdgcn_exp2f(
+              BIAS ? (s[x] * a.scale + to_f32(b_now[b][x]) - z[e]) * kLog2e : s[x] * unit - z[e]);
+          s[x] = p;
+          dp[x] = p * (dp[x] - d[e]);
         }
-        const bool in = key < w.seen;
-        s[x] = in ? p : 0.0f;
-        dp[x] = in ? p * (dp[x] - w.delta) : 0.0f;
-        if (BIAS && a.g_bias && live && x0 + 32 * b + 8 * (x / 4) + 4 * h + x % 4 < all)
-          static_cast<T*>(a.g_bias)[w.cell + key] = from_f32<T>(dp[x]);
+      }
+      if (a.causal && k0 + 31 > r0 + rb + ahead) {
+#pragma unroll
+        for (int x = 0; x < 16; ++x)
+          if (key > r0 + rb + ahead + 8 * (x / 4) + 4 * h + x % 4) s[x] = dp[x] = 0.0f;
+      }
+      if (BIAS && a.g_bias && live) {
+        T* p = g_bias + (int64_t)hq * a.cells + (r0 + rb) * m + key;
+        const int64_t left = n - r0 - rb;
+#pragma unroll
+        for (int x = 0; x < 16; ++x) {
+          const int64_t r = 8 * (x / 4) + 4 * h + x % 4;
+          if (r < left) p[r * m] = from_f32<T>(dp[x]);
+        }
       }
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
@@ -325,13 +340,38 @@ __global__ __launch_bounds__(64 * WAVES, DP > 64 ? 1 : 2) void k_attention_bwd_k
         at_pack(dp, 8 * x, fs);
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
-          gv[d] = at_mma(at_across<L>(lg, 32 * b + 16 * x, 32 * d), fp, gv[d]);
-          gk[d] = at_mma(at_across<L>(lq, 32 * b + 16 * x, 32 * d), fs, gk[d]);
+          gv[d] = at_mma(at_across<L>(lg, rb + 16 * x, 32 * d), fp, gv[d]);
+          gk[d] = at_mma(at_across<L>(lq, rb + 16 * x, 32 * d), fs, gk[d]);
         }
       }
     }
     if (more) put(buf ^ 1);
     __syncthreads();
+  }
+  if (RW > 1) {  // the waves of the same keys, in order
+    float* join = reinterpret_cast<float*>(lds_bytes);
+    if (rw > 0) {
+      float* p = join + ((rw - 1) * KW + kw) * 2 * DT * 16 * 64 + lane;
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int x = 0; x < 16; ++x) {
+          p[(32 * d + x) * 64] = gk[d][x];
+          p[(32 * d + 16 + x) * 64] = gv[d][x];
+        }
+    }
+    __syncthreads();
+    if (rw > 0) return;
+    for (int w = 1; w < RW; ++w) {
+      const float* p = join + ((w - 1) * KW + kw) * 2 * DT * 16 * 64 + lane;
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int x = 0; x < 16; ++x) {
+          gk[d][x] += p[(32 * d + x) * 64];
+          gv[d][x] += p[(32 * d + 16 + x) * 64];
+        }
+    }
   }
   if (!live) return;
   T* ok = static_cast<T*>(a.g_k) + t * a.ld_gk + (int64_t)hk * a.D;
@@ -349,26 +389,31 @@ __global__ __launch_bounds__(64 * WAVES, DP > 64 ? 1 : 2) void k_attention_bwd_k
     }
 }
 
-template <typename T, int DP, int WAVES, bool BIAS>
+template <typename T, int DP, int KW, int RW, bool BIAS>
+hipError_t run_k(const nt_partition& p, AbArgs x, hipStream_t stream) {
+  x.slots = at_slots(p.T_cols, p.B, 1, 32 * KW);
+  k_attention_bwd_k<T, DP, KW, RW, BIAS>
+      <<<dim3((unsigned)x.slots, x.K), 64 * KW * RW, 0, stream>>>(x);
+  return hipGetLastError();
+}
+
+template <typename T, int DP, bool BIAS>
 hipError_t run(const nt_partition& p, AbArgs x, hipStream_t stream) {
   if (p.T) {
-    x.slots = at_slots(p.T, p.B, x.H / x.K, 32 * WAVES);
-    k_attention_bwd_q<T, DP, WAVES, BIAS>
-        <<<dim3((unsigned)x.slots, x.K), 64 * WAVES, 0, stream>>>(x);
+    x.slots = at_slots(p.T, p.B, x.H / x.K, 128);
+    k_attention_bwd_q<T, DP, 4, BIAS><<<dim3((unsigned)x.slots, x.K), 256, 0, stream>>>(x);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  if (p.T_cols) {
-    x.slots = at_slots(p.T_cols, p.B, 1, 32 * WAVES);
-    k_attention_bwd_k<T, DP, WAVES, BIAS>
-        <<<dim3((unsigned)x.slots, x.K), 64 * WAVES, 0, stream>>>(x);
-  }
-  return hipGetLastError();
+  if (!p.T_cols) return hipSuccess;
+  const int64_t groups = at_slots(p.T_cols, p.B, 1, 128) * x.K;
+  if (groups >= 2048) return run_k<T, DP, 4, 1, BIAS>(p, x, stream);
+  return run_k<T, DP, 2, 2, BIAS>(p, x, stream);
 }
 
 template <typename T, int DP>
 hipError_t run(const nt_partition& p, const AbArgs& x, hipStream_t stream) {
-  return x.bias ? run<T, DP, 4, true>(p, x, stream) : run<T, DP, 4, false>(p, x, stream);
+  return x.bias ? run<T, DP, true>(p, x, stream) : run<T, DP, false>(p, x, stream);
 }
 
 template <typename T>
