@@ -600,12 +600,12 @@ nt_status nt_pair_block_backward_nl(const nt_partition* p, const void* s_in, con
  * one attention of N_i queries over M_i keys (N_i = 1: one new token over its
  * kept keys). Arrays of heads are [tokens, heads, head_dim], a token's heads
  * contiguous; ld is the distance in elements from one token to the next (0
- * for heads * head_dim), a multiple of 8, so that queries, keys and values
+ * for heads * head_dim), a multiple of 8 and at most 2^22, so that queries, keys and values
  * may be parts of one projected array. Gradients of activations have the
  * storage type here: they are the operands of the projections' gradients,
  * whose products round them to bf16 in any case; gradients of the norm
- * weights are fp32. head_dim is a multiple of 8 and at most 128; heads is a
- * multiple of kv_heads, and query head h reads key head h / (heads /
+ * weights are fp32. head_dim is a multiple of 8 and at most 128, heads at most
+ * 4096 and a multiple of kv_heads, and query head h reads key head h / (heads /
  * kv_heads).
  * ------------------------------------------------------------------------ */
 
@@ -712,8 +712,8 @@ nt_status nt_attention_workspace_bytes(const nt_partition* p, const nt_attention
  * statistics and sums are fp32; with NT_BF16 the probabilities are rounded
  * to bf16 before their product with v, and o once. A masked key has weight
  * zero, but its k and v must be finite (0 times infinity is NaN). o must not
- * overlap the inputs. NT_ERR_OVERFLOW: T heads / kv_heads or T_cols of 2^30
- * or more. workspace: device, 16-byte aligned.
+ * overlap the inputs. NT_ERR_OVERFLOW: (T heads / 64 + B kv_heads) or
+ * (T_cols kv_heads / 64 + B kv_heads) of 2^24 or more in one launch. workspace: device, 16-byte aligned.
  */
 nt_status nt_single_attention(const nt_partition* p, const nt_attention* a, const void* q,
                               const void* k, const void* v, const void* bias, void* o, float* lse,
@@ -741,7 +741,8 @@ nt_status nt_attention_backward_workspace_bytes(const nt_partition* p, const nt_
  *   g_v = P^T g_o, g_q = scale dS k, g_k = scale dS^T q, g_bias = dS,
  * shared key heads summing over their query heads. Masked cells and rows
  * with lse = -inf give zero. With NT_BF16 P and dS are rounded to bf16 before
- * their products. Sums run in a fixed order (no atomics). The gradients
+ * their products. Sums run in a fixed order (no atomics). NT_ERR_OVERFLOW as
+ * the forward's, and with a bias T_cols of 2^27 or more. The gradients
  * must not overlap the inputs or each other. workspace: device, 16-byte
  * aligned.
  */

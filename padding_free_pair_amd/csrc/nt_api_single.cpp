@@ -17,8 +17,8 @@ namespace {
 using namespace nt::host;
 
 constexpr int kMaxHeadDim = 128;
-constexpr int kMaxHeads = 16384;
-constexpr int64_t kMaxLd = int64_t(1) << 28;
+constexpr int kMaxHeads = 4096;
+constexpr int64_t kMaxLd = int64_t(1) << 22;  // byte distances within a tile fit 32 bits
 
 // An array of token rows: `width` elements every `ld`.
 struct Rows {
@@ -46,8 +46,8 @@ bool rows_overlap(const Rows& a, const Rows& b, size_t es) {
 
 nt_status check_rows(const Rows& a, size_t es) {
   if (a.ld < a.width || a.ld % 8 != 0 || a.ld > kMaxLd)
-    return fail(NT_ERR_INVALID, "ld of %s = %lld must be a multiple of 8, at least %lld", a.name,
-                (long long)a.ld, (long long)a.width);
+    return fail(NT_ERR_INVALID, "ld of %s = %lld must be a multiple of 8 in [%lld, %lld]", a.name,
+                (long long)a.ld, (long long)a.width, (long long)kMaxLd);
   return check_array(a.name, a.ptr, span(a, es));
 }
 
@@ -348,6 +348,10 @@ nt_status nt_single_attention_backward(const nt_partition* p, const nt_attention
   const uint64_t lse_bytes = (uint64_t)p->T * x.heads * sizeof(float);
   if (bias) NT_TRY(check_array("bias", bias, bias_bytes));
   if (y.bias) NT_TRY(check_array("g_bias", y.bias, bias_bytes));
+  if (bias && p->T_cols >= int64_t(1) << 27)
+    return fail(NT_ERR_OVERFLOW, "T_cols = %lld with a bias must be below 2^27",
+                (long long)p->T_cols);
+  if (y.bias && !bias) return fail(NT_ERR_NULL, "g_bias without a bias");
   NT_TRY(check_array("lse", lse, lse_bytes));
   const size_t need = nt::attention_backward_ws_bytes(*p, x, dtype);
   NT_TRY(check_workspace(workspace, workspace_bytes, need));

@@ -44,12 +44,13 @@ __global__ __launch_bounds__(kAtThreads, sizeof(T) == 4 && DP > 64 ? 1 : 2) void
   typedef typename AtFrag<T>::type Frag;
   __shared__ __align__(16) T lds[2][kAtKeys * (LK::pitch + LV::pitch)];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l32 = lane & 31, h = lane >> 5;
-  const int64_t place = at_place((int64_t)blockIdx.y * gridDim.x + blockIdx.x,
-                                 (int64_t)gridDim.x * gridDim.y);
-  const int split = (int)(place % a.splits);
-  const int64_t ph = place / a.splits;
-  const int hk = (int)(ph / a.slots);
-  const int64_t slot = ph - hk * a.slots;
+  // Key heads fastest: with 8 of them (or 4, 16 ..) an XCD, which takes every
+  // eighth workgroup, stays with its own heads' keys, and all heads advance
+  // together. Tiles in reverse, so that a causal sample's longest rows begin
+  // first and the short ones fill the end.
+  const int hk = blockIdx.x % a.K;
+  const int split = blockIdx.x / a.K % a.splits;
+  const int64_t slot = a.slots - 1 - blockIdx.x / a.K / a.splits;
   const int G = a.H / a.K;
   const int i = at_sample_of(a.eta, a.B, G, kAtRows, slot);
   const int64_t tile = slot - (a.eta[i] * G / kAtRows + i);
@@ -75,11 +76,12 @@ __global__ __launch_bounds__(kAtThreads, sizeof(T) == 4 && DP > 64 ? 1 : 2) void
   int64_t c0 = 0;
   if (a.splits > 1) {
     const int64_t per = ((c1 + a.splits - 1) / a.splits + kAtKeys - 1) / kAtKeys * kAtKeys;
-    c0 = split * per;
+    c0 = split * per < c1 ? split * per : c1;
     c1 = c0 + per < c1 ? c0 + per : c1;
   }
+  const int keys = (int)m, end = (int)c1, last = (int)seen;
   // the fewest keys that a row of this wave sees: no masks below it
-  const int64_t seen0 = __builtin_amdgcn_readfirstlane((int)seen);
+  const int seen0 = __builtin_amdgcn_readfirstlane(last);
 
   // queries as fragments; the scale's sign goes with them
   Frag q[KS];
@@ -101,20 +103,24 @@ __global__ __launch_bounds__(kAtThreads, sizeof(T) == 4 && DP > 64 ? 1 : 2) void
   for (int d = 0; d < DT; ++d) o[d] = f32x16{};
   float most = -INFINITY, sum = 0.0f;  // of this row; sum: this half's keys
   const float unit = BIAS ? 1.0f : scale * kLog2e;  // a score's unit in powers of two
-  AtStage<T, kAtKeys, DP, kAtThreads> sk, sv;
+  AtStage<T, kAtKeys, DP, kAtThreads> sk(a.ld_k), sv(a.ld_v);
+  kp += c0 * a.ld_k;
+  vp += c0 * a.ld_v;
   if (c0 < c1) {
-    sk.load(kp + c0 * a.ld_k, a.ld_k, m - c0, a.D);
-    sv.load(vp + c0 * a.ld_v, a.ld_v, m - c0, a.D);
+    sk.load(kp, a.ld_k, keys - (int)c0, a.D);
+    sv.load(vp, a.ld_v, keys - (int)c0, a.D);
     sk.template put<LK>(lds[0]);
     sv.template put<LV>(lds[0] + kAtKeys * LK::pitch);
   }
   __syncthreads();
   int buf = 0;
-  for (int64_t c = c0; c < c1; c += kAtKeys, buf ^= 1) {
-    const bool more = c + kAtKeys < c1;
+  for (int c = (int)c0; c < end; c += kAtKeys, buf ^= 1) {
+    const bool more = c + kAtKeys < end;
     if (more) {
-      sk.load(kp + (c + kAtKeys) * a.ld_k, a.ld_k, m - c - kAtKeys, a.D);
-      sv.load(vp + (c + kAtKeys) * a.ld_v, a.ld_v, m - c - kAtKeys, a.D);
+      kp += kAtKeys * a.ld_k;
+      vp += kAtKeys * a.ld_v;
+      sk.load(kp, a.ld_k, keys - c - kAtKeys, a.D);
+      sv.load(vp, a.ld_v, keys - c - kAtKeys, a.D);
     }
     const T* lk = lds[buf];
     const T* lv = lds[buf] + kAtKeys * LK::pitch;
@@ -131,28 +137,31 @@ __global__ __launch_bounds__(kAtThreads, sizeof(T) == 4 && DP > 64 ? 1 : 2) void
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
           float f[4];
-          at_bias4(bp, c + 32 * b + 8 * g + 4 * h, m, f);
+          at_bias4(bp, c + 32 * b + 8 * g + 4 * h, keys, f);
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[b][4 * g + e] = s[b][4 * g + e] * scale + f[e];
         }
     }
-    if (c + kAtKeys > (CAUSAL ? seen0 : m)) {
+    if (c + kAtKeys > (CAUSAL ? seen0 : keys)) {
+      at_rare();
+      const int left = last - c - 4 * h;
 #pragma unroll
       for (int b = 0; b < 2; ++b)
 #pragma unroll
         for (int x = 0; x < 16; ++x)
-          if (c + 32 * b + 8 * (x / 4) + 4 * h + x % 4 >= seen) s[b][x] = -INFINITY;
+          if (32 * b + 8 * (x / 4) + x % 4 >= left) s[b][x] = -INFINITY;
     }
     float top = s[0][0];
 #pragma unroll
     for (int b = 0; b < 2; ++b)
 #pragma unroll
       for (int x = 0; x < 16; ++x) top = fmaxf(top, s[b][x]);
-    top = fmaxf(top, __shfl_xor(top, 32));
+    top = at_halves_max(top);
     if (__any(top > most)) {
+      at_rare();
       const float now = fmaxf(most, top);
       const float keep = now == -INFINITY ? 1.0f
-                         : BIAS ? exp2f((most - now) * kLog2e) : exp2f((most - now) * unit);
+                                          : __builtin_amdgcn_exp2f((most - now) * (BIAS ? kLog2e : unit));
       most = now;
       sum *= keep;
 #pragma unroll
@@ -256,7 +265,7 @@ int splits_of(const nt_partition& p, const nt_attention& a) {
 
 template <typename T, int DP>
 hipError_t run(const AtArgs& x, bool causal, hipStream_t stream) {
-  const dim3 g((unsigned)(x.slots * x.splits), x.K);
+  const unsigned g = (unsigned)(x.slots * x.splits * x.K);
   if (x.bias) {
     if (causal) k_attention<T, DP, true, true><<<g, kAtThreads, 0, stream>>>(x);
     else k_attention<T, DP, true, false><<<g, kAtThreads, 0, stream>>>(x);
@@ -287,8 +296,8 @@ hipError_t forward(const nt_partition& p, const nt_attention& a, AtArgs x, hipSt
 bool attention_fits(const nt_partition& p, const nt_attention& a) {
   const int64_t most = (int64_t(1) << 32) / kAtThreads;
   // the smallest tiles that any kernel here or of the gradients takes
-  return at_slots(p.T, p.B, a.heads / a.kv_heads, 64) * splits_of(p, a) < most &&
-         at_slots(p.T_cols, p.B, 1, 64) < most;
+  return at_slots(p.T, p.B, a.heads / a.kv_heads, 64) * splits_of(p, a) * a.kv_heads < most &&
+         at_slots(p.T_cols, p.B, 1, 64) * a.kv_heads < most;
 }
 
 size_t attention_ws_bytes(const nt_partition& p, const nt_attention& a, nt_dtype) {

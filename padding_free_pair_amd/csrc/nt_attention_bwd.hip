@@ -57,10 +57,9 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 4 && DP > 64 ? 1 : 2) void
   typedef typename AtFrag<T>::type Frag;
   __shared__ __align__(16) T lds[2][2 * TILE];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l32 = lane & 31, h = lane >> 5;
-  const int64_t place = at_place((int64_t)blockIdx.y * gridDim.x + blockIdx.x,
-                                 (int64_t)gridDim.x * gridDim.y);
-  const int hk = (int)(place / a.slots);
-  const int64_t slot = place - hk * a.slots;
+  // as in the forward: key heads fastest, a causal sample's longest rows first
+  const int hk = blockIdx.x % a.K;
+  const int64_t slot = a.slots - 1 - blockIdx.x / a.K;
   const int G = a.H / a.K;
   const int i = at_sample_of(a.eta, a.B, G, ROWS, slot);
   const int64_t tile = slot - (a.eta[i] * G / ROWS + i);
@@ -81,7 +80,8 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 4 && DP > 64 ? 1 : 2) void
     c1 = rl + 1 + m - n;
     c1 = c1 < 0 ? 0 : c1 < m ? c1 : m;
   }
-  const int64_t seen0 = a.causal ? __builtin_amdgcn_readfirstlane((int)seen) : m;
+  const int keys = (int)m, end = (int)c1, last = (int)seen;
+  const int seen0 = a.causal ? __builtin_amdgcn_readfirstlane(last) : keys;
 
   Frag q[KS], g[KS];
   const T* qp = static_cast<const T*>(a.q) + t * a.ld_q + (int64_t)hq * a.D;
@@ -109,20 +109,22 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 4 && DP > 64 ? 1 : 2) void
 #pragma unroll
   for (int d = 0; d < DT; ++d) gq[d] = f32x16{};
   const float unit = a.scale * kLog2e, base = lse * kLog2e;
-  AtStage<T, kAbTile, DP, THREADS> sk, sv;
-  if (c1 > 0) {
-    sk.load(kp, a.ld_k, m, a.D);
-    sv.load(vp, a.ld_v, m, a.D);
+  AtStage<T, kAbTile, DP, THREADS> sk(a.ld_k), sv(a.ld_v);
+  if (end > 0) {
+    sk.load(kp, a.ld_k, keys, a.D);
+    sv.load(vp, a.ld_v, keys, a.D);
     sk.template put<L>(lds[0]);
     sv.template put<L>(lds[0] + TILE);
   }
   __syncthreads();
   int buf = 0;
-  for (int64_t c = 0; c < c1; c += kAbTile, buf ^= 1) {
-    const bool more = c + kAbTile < c1;
+  for (int c = 0; c < end; c += kAbTile, buf ^= 1) {
+    const bool more = c + kAbTile < end;
     if (more) {
-      sk.load(kp + (c + kAbTile) * a.ld_k, a.ld_k, m - c - kAbTile, a.D);
-      sv.load(vp + (c + kAbTile) * a.ld_v, a.ld_v, m - c - kAbTile, a.D);
+      kp += kAbTile * a.ld_k;
+      vp += kAbTile * a.ld_v;
+      sk.load(kp, a.ld_k, keys - c - kAbTile, a.D);
+      sv.load(vp, a.ld_v, keys - c - kAbTile, a.D);
     }
     const T* lk = lds[buf];
     const T* lv = lds[buf] + TILE;
@@ -138,7 +140,7 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 4 && DP > 64 ? 1 : 2) void
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
           float f[4];
-          at_bias4(bp, c + 32 * b + 8 * y + 4 * h, m, f);
+          at_bias4(bp, c + 32 * b + 8 * y + 4 * h, keys, f);
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             s[4 * y + e] = (s[4 * y + e] * a.scale + f[e] - lse) * kLog2e;
@@ -150,9 +152,11 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 4 && DP > 64 ? 1 : 2) void
 #pragma unroll
       for (int x = 0; x < 16; ++x) s[x] = __builtin_amdgcn_exp2f(s[x]) * (dp[x] - delta);
       if (c + kAbTile > seen0) {
+        at_rare();
+        const int left = last - c - 4 * h;
 #pragma unroll
         for (int x = 0; x < 16; ++x)
-          if (c + 32 * b + 8 * (x / 4) + 4 * h + x % 4 >= seen) s[x] = 0.0f;
+          if (32 * b + 8 * (x / 4) + x % 4 >= left) s[x] = 0.0f;
       }
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
@@ -197,10 +201,9 @@ __global__ __launch_bounds__(64 * KW * RW, DP > 64 ? 1 : 2) void k_attention_bwd
   T* lds = reinterpret_cast<T*>(lds_bytes);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l32 = lane & 31, h = lane >> 5;
   const int kw = wave / RW, rw = wave % RW;
-  const int64_t place = at_place((int64_t)blockIdx.y * gridDim.x + blockIdx.x,
-                                 (int64_t)gridDim.x * gridDim.y);
-  const int hk = (int)(place / a.slots);
-  const int64_t slot = place - hk * a.slots;
+  // a causal sample's first keys, which the most rows see, begin first
+  const int hk = blockIdx.x % a.K;
+  const int64_t slot = blockIdx.x / a.K;
   const int G = a.H / a.K;
   const int i = at_sample_of(a.mu, a.B, 1, KEYS, slot);
   const int64_t tile = slot - (a.mu[i] / KEYS + i);
@@ -240,18 +243,28 @@ __global__ __launch_bounds__(64 * KW * RW, DP > 64 ? 1 : 2) void k_attention_bwd
     for (int g = 0; g < G; ++g)
       for (int64_t r = 2 * rw + h; r < first; r += 2 * RW)
         g_bias[(int64_t)(hk * G + g) * a.cells + r * m + key] = from_f32<T>(0.0f);
-  const int64_t per_head = (n - first + ROWS - 1) / ROWS, tiles = per_head * G;
+  const int rows = (int)n, per_head = (int)((n - first + ROWS - 1) / ROWS), tiles = per_head * G;
 
-  AtStage<T, ROWS, DP, THREADS> sq, sg;
+  AtStage<T, ROWS, DP, THREADS> sq(a.ld_q), sg((int64_t)a.H * a.D);
   float row_lse = 0.0f, row_delta = 0.0f;
-  T b_now[NB][16], b_next[NB][16];  // bias of this lane's key at its rows
-  auto fetch = [&](int64_t j) {
-    const int hq = hk * G + (int)(j / per_head);
-    const int64_t r0 = first + j % per_head * ROWS, t0 = a.eta[i] + r0;
-    sq.load(static_cast<const T*>(a.q) + t0 * a.ld_q + (int64_t)hq * a.D, a.ld_q, n - r0, a.D);
-    sg.load(static_cast<const T*>(a.g_o) + (t0 * a.H + hq) * a.D, (int64_t)a.H * a.D, n - r0, a.D);
+  // Bias of this lane's key at its rows. Rows are m elements apart from a uniform
+  // base; a lane's distance from it, of its key and its half's four rows, is
+  // one register (T_cols < 2^27 with a bias).
+  T b_now[NB][16], b_next[NB][16];
+  const uint32_t b_off = (uint32_t)((4 * h * (uint32_t)m + (uint32_t)keyc) * sizeof(T));
+  int next_h = hk * G, next_r = (int)first;  // head and first row of the tile to fetch
+  auto fetch = [&]() {
+    const int hq = next_h, r0 = next_r;
+    next_r += ROWS;
+    if (next_r >= rows) {
+      next_r = (int)first;
+      ++next_h;
+    }
+    const int64_t t0 = a.eta[i] + r0;
+    sq.load(static_cast<const T*>(a.q) + t0 * a.ld_q + (int64_t)hq * a.D, a.ld_q, rows - r0, a.D);
+    sg.load(static_cast<const T*>(a.g_o) + (t0 * a.H + hq) * a.D, (int64_t)a.H * a.D, rows - r0, a.D);
     if (threadIdx.x < ROWS) {
-      const bool in = r0 + threadIdx.x < n;
+      const bool in = r0 + (int)threadIdx.x < rows;
       const int64_t at = (t0 + (in ? threadIdx.x : 0)) * a.H + hq;
       const float z = a.lse[at];
       // a row that saw nothing, or is none, gives nothing
@@ -259,15 +272,24 @@ __global__ __launch_bounds__(64 * KW * RW, DP > 64 ? 1 : 2) void k_attention_bwd
       row_delta = a.delta[at];
     }
     if (BIAS) {
-      const T* p = bias + (int64_t)hq * a.cells + r0 * m + keyc;
-      const bool whole = r0 + ROWS <= n;
+      const T* p = bias + (int64_t)hq * a.cells + r0 * m;
+      if (r0 + ROWS <= rows) {
 #pragma unroll
-      for (int b = 0; b < NB; ++b)
+        for (int b = 0; b < NB; ++b)
 #pragma unroll
-        for (int x = 0; x < 16; ++x) {
-          const int64_t r = 32 * (rw * NB + b) + 8 * (x / 4) + 4 * h + x % 4;
-          b_next[b][x] = p[(whole || r < n - r0 ? r : n - 1 - r0) * m];
-        }
+          for (int x = 0; x < 16; ++x) {
+            const T* pr = p + (32 * (rw * NB + b) + 8 * (x / 4) + x % 4) * m;
+            b_next[b][x] = *reinterpret_cast<const T*>(reinterpret_cast<const char*>(pr) + b_off);
+          }
+      } else {
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int x = 0; x < 16; ++x) {
+            const int r = 32 * (rw * NB + b) + 8 * (x / 4) + 4 * h + x % 4;
+            b_next[b][x] = p[(r < rows - r0 ? r : rows - r0 - 1) * m + keyc];
+          }
+      }
     }
   };
   auto put = [&](int buf) {
@@ -279,22 +301,20 @@ __global__ __launch_bounds__(64 * KW * RW, DP > 64 ? 1 : 2) void k_attention_bwd
     }
   };
   if (tiles > 0) {
-    fetch(0);
+    fetch();
     put(0);
   }
   __syncthreads();
   int buf = 0;
-  for (int64_t j = 0; j < tiles; ++j, buf ^= 1) {
+  for (int j = 0, hq = hk * G, r0 = (int)first; j < tiles; ++j, buf ^= 1) {
     const bool more = j + 1 < tiles;
-    const int hq = hk * G + (int)(j / per_head);
-    const int64_t r0 = first + j % per_head * ROWS;
     if (BIAS) {
 #pragma unroll
       for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int x = 0; x < 16; ++x) b_now[b][x] = b_next[b][x];
     }
-    if (more) fetch(j + 1);
+    if (more) fetch();
     const T* lq = lds + buf * 2 * TILE;
     const T* lg = lq + TILE;
 #pragma unroll
@@ -320,17 +340,27 @@ __global__ __launch_bounds__(64 * KW * RW, DP > 64 ? 1 : 2) void k_attention_bwd
         }
       }
       if (a.causal && k0 + 31 > r0 + rb + ahead) {
+        at_rare();
+        const int past = (int)(key - ahead) - r0 - rb - 4 * h;  // rows before it do not see the key
 #pragma unroll
         for (int x = 0; x < 16; ++x)
-          if (key > r0 + rb + ahead + 8 * (x / 4) + 4 * h + x % 4) s[x] = dp[x] = 0.0f;
+          if (8 * (x / 4) + x % 4 < past) s[x] = dp[x] = 0.0f;
       }
       if (BIAS && a.g_bias && live) {
-        T* p = g_bias + (int64_t)hq * a.cells + (r0 + rb) * m + key;
-        const int64_t left = n - r0 - rb;
+        T* p = g_bias + (int64_t)hq * a.cells + (int64_t)(r0 + rb) * m;
+        const int left = rows - r0 - rb;
+        if (left >= 32) {
 #pragma unroll
-        for (int x = 0; x < 16; ++x) {
-          const int64_t r = 8 * (x / 4) + 4 * h + x % 4;
-          if (r < left) p[r * m] = from_f32<T>(dp[x]);
+          for (int x = 0; x < 16; ++x)
+            *reinterpret_cast<T*>(reinterpret_cast<char*>(p + (8 * (x / 4) + x % 4) * m) + b_off) =
+                from_f32<T>(dp[x]);
+        } else {
+          at_rare();
+#pragma unroll
+          for (int x = 0; x < 16; ++x) {
+            const int r = 8 * (x / 4) + 4 * h + x % 4;
+            if (r < left) p[r * m + key] = from_f32<T>(dp[x]);
+          }
         }
       }
 #pragma unroll
@@ -347,6 +377,11 @@ __global__ __launch_bounds__(64 * KW * RW, DP > 64 ? 1 : 2) void k_attention_bwd
     }
     if (more) put(buf ^ 1);
     __syncthreads();
+    r0 += ROWS;
+    if (r0 >= rows) {
+      r0 = (int)first;
+      ++hq;
+    }
   }
   if (RW > 1) {  // the waves of the same keys, in order
     float* join = reinterpret_cast<float*>(lds_bytes);
@@ -393,7 +428,7 @@ template <typename T, int DP, int KW, int RW, bool BIAS>
 hipError_t run_k(const nt_partition& p, AbArgs x, hipStream_t stream) {
   x.slots = at_slots(p.T_cols, p.B, 1, 32 * KW);
   k_attention_bwd_k<T, DP, KW, RW, BIAS>
-      <<<dim3((unsigned)x.slots, x.K), 64 * KW * RW, 0, stream>>>(x);
+      <<<(unsigned)(x.slots * x.K), 64 * KW * RW, 0, stream>>>(x);
   return hipGetLastError();
 }
 
@@ -401,7 +436,7 @@ template <typename T, int DP, bool BIAS>
 hipError_t run(const nt_partition& p, AbArgs x, hipStream_t stream) {
   if (p.T) {
     x.slots = at_slots(p.T, p.B, x.H / x.K, 128);
-    k_attention_bwd_q<T, DP, 4, BIAS><<<dim3((unsigned)x.slots, x.K), 256, 0, stream>>>(x);
+    k_attention_bwd_q<T, DP, 4, BIAS><<<(unsigned)(x.slots * x.K), 256, 0, stream>>>(x);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }

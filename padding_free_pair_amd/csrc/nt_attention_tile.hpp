@@ -156,33 +156,56 @@ __device__ __forceinline__ void at_bias4(const float* p, int64_t c, int64_t m, f
 }
 
 // A tile of ROWS token rows of D elements (D <= DP) on its way to LDS: pieces
-// of 16 bytes, one after another over the THREADS threads. Rows past the
-// last one read the last one (their weight is zero).
+// of 16 bytes, one after another over the THREADS threads. The distances of a
+// thread's pieces from the tile's first row stay the same from tile to tile
+// (ld <= 2^22 keeps them in 32 bits), so a load is a uniform base and one
+// register. Rows past the last one read the last one (their weight is zero).
 template <typename T, int ROWS, int DP, int THREADS> struct AtStage {
   static constexpr int kVec = 16 / sizeof(T);
   static constexpr int kPieces = ROWS * DP / kVec / THREADS;
   static_assert(ROWS * DP % (kVec * THREADS) == 0, "whole pieces");
   typedef T Vec __attribute__((ext_vector_type(16 / sizeof(T))));
   Vec v[kPieces];
-  // first: the tile's first row; rows: how many there are from it on (>= 1)
-  __device__ __forceinline__ void load(const T* first, int64_t ld, int64_t rows, int D) {
+  uint32_t off[kPieces];
+  static __device__ __forceinline__ int row(int u) { return (threadIdx.x + u * THREADS) * kVec / DP; }
+  static __device__ __forceinline__ int col(int u) { return (threadIdx.x + u * THREADS) * kVec % DP; }
+  __device__ __forceinline__ AtStage(int64_t ld) {
 #pragma unroll
-    for (int u = 0; u < kPieces; ++u) {
-      const int at = (threadIdx.x + u * THREADS) * kVec;
-      const int r = at / DP, c = at % DP;
-      const int64_t row = r < rows ? r : rows - 1;
-      v[u] = Vec{};
-      if (c < D) v[u] = *reinterpret_cast<const Vec*>(first + row * ld + c);
+    for (int u = 0; u < kPieces; ++u)
+      off[u] = (uint32_t)((row(u) * (uint32_t)ld + col(u)) * sizeof(T));
+  }
+  // first: the tile's first row; rows: how many there are from it on (>= 1)
+  __device__ __forceinline__ void load(const T* first, int64_t ld, int rows, int D) {
+    const char* base = reinterpret_cast<const char*>(first);
+    if (rows >= ROWS && D == DP) {
+#pragma unroll
+      for (int u = 0; u < kPieces; ++u) v[u] = *reinterpret_cast<const Vec*>(base + off[u]);
+    } else {
+#pragma unroll
+      for (int u = 0; u < kPieces; ++u) {
+        const int r = row(u) < rows ? row(u) : rows - 1, c = col(u);
+        v[u] = Vec{};
+        if (c < D) v[u] = *reinterpret_cast<const Vec*>(first + r * ld + c);
+      }
     }
   }
   template <typename L> __device__ __forceinline__ void put(T* tile) const {
 #pragma unroll
-    for (int u = 0; u < kPieces; ++u) {
-      const int at = (threadIdx.x + u * THREADS) * kVec;
-      *reinterpret_cast<Vec*>(tile + L::at(at / DP, at % DP)) = v[u];
-    }
+    for (int u = 0; u < kPieces; ++u)
+      *reinterpret_cast<Vec*>(tile + L::at(row(u), col(u))) = v[u];
   }
 };
+
+// Keeps the compiler from turning a branch that few tiles take into selects
+// that every tile pays for.
+__device__ __forceinline__ void at_rare() { asm volatile("" ::: "memory"); }
+
+// The larger of a lane's value and its partner's in the other half.
+__device__ __forceinline__ float at_halves_max(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, x),
+                                                  __builtin_bit_cast(uint32_t, x), false, false);
+  return fmaxf(__builtin_bit_cast(float, (uint32_t)r[0]), __builtin_bit_cast(float, (uint32_t)r[1]));
+}
 
 // Tiles of `tile` rows of ragged samples without a list of them: sample i
 // owns the slots [off_i mult / tile + i, off_{i+1} mult / tile + i + 1), at
@@ -206,14 +229,6 @@ __device__ __forceinline__ int at_sample_of(const int64_t* off, int B, int mult,
 }
 inline int64_t at_slots(int64_t total, int B, int mult, int tile) {
   return total * mult / tile + B;
-}
-
-// Workgroup b of n in an order in which each XCD (b mod 8 holds workgroups
-// round robin) takes a run of consecutive places: those share keys and values
-// in its L2.
-__device__ __forceinline__ int64_t at_place(int64_t b, int64_t n) {
-  const int64_t per = n / 8, rest = n % 8, x = b % 8;
-  return x * per + (x < rest ? x : rest) + b / 8;
 }
 
 }  // namespace nt
