@@ -12,6 +12,7 @@
 // The scores and dP are formed twice (7 products instead of 5); joining the
 // walks would need g_q summed across workgroups.
 #include <math.h>
+#include <stdlib.h>
 
 #include "nt_attention_tile.hpp"
 #include "nt_internal.hpp"
@@ -442,6 +443,14 @@ hipError_t run(const nt_partition& p, AbArgs x, hipStream_t stream) {
   }
   if (!p.T_cols) return hipSuccess;
   const int64_t groups = at_slots(p.T_cols, p.B, 1, 128) * x.K;
+  if (const char* ev = getenv("NT_BK")) {
+    const int c = atoi(ev);
+    if (c == 41) return run_k<T, DP, 4, 1, BIAS>(p, x, stream);
+    if (c == 22) return run_k<T, DP, 2, 2, BIAS>(p, x, stream);
+    if (c == 21) return run_k<T, DP, 2, 1, BIAS>(p, x, stream);
+    if (c == 12) return run_k<T, DP, 1, 2, BIAS>(p, x, stream);
+    if constexpr (sizeof(T) == 2) { if (c == 14) return run_k<bf16, DP, 1, 4, BIAS>(p, x, stream); }
+  }
   if (groups >= 2048) return run_k<T, DP, 4, 1, BIAS>(p, x, stream);
   return run_k<T, DP, 2, 2, BIAS>(p, x, stream);
 }
