@@ -40,11 +40,6 @@ template <typename T> struct NrSide {
 };
 
 template <typename T> __device__ __forceinline__ void nr_load(const T* p, float* f);
-template <> __device__ __forceinline__ void nr_load<bf16>(const bf16* p, float* f) {
-  const bf16x8 v = *reinterpret_cast<const bf16x8*>(p);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = (float)v[i];
-}
 template <> __device__ __forceinline__ void nr_load<float>(const float* p, float* f) {
   const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 4);
 #pragma unroll
@@ -85,39 +80,71 @@ __device__ __forceinline__ int nr_partner(int e, int R, bool interleaved) {
 
 // cos and signed sin of the lane's dimensions at a token: out_e = y_e c_e +
 // y_partner s_e. A position that the table does not hold gives NaN.
+template <int PAIRS>
 __device__ __forceinline__ void nr_angles(const float* table, int64_t at, int64_t positions, int R,
-                                          bool interleaved, int e0, float* c, float* s) {
+                                          int e0, float* c, float* s) {
   const bool inside = at >= 0 && at < positions;
   const float* row = table + (inside ? at : 0) * R;
+  if (PAIRS == kPairsInLine) {  // eight angles in a row, and half a head is whole lanes
+    if (e0 < R) {
+      const bool first = e0 < R / 2;
+      const float* p = row + (first ? e0 : e0 - R / 2);
+      nr_load<float>(p, c);
+      nr_load<float>(p + R / 2, s);
 #pragma unroll
-  for (int i = 0; i < kNrVec; ++i) {
-    const int e = e0 + i;
-    c[i] = 1.0f;
-    s[i] = 0.0f;
-    if (e < R) {
-      const int j = interleaved ? e >> 1 : (e < R / 2 ? e : e - R / 2);
-      const bool first = interleaved ? !(e & 1) : e < R / 2;
-      c[i] = row[j];
-      s[i] = first ? -row[R / 2 + j] : row[R / 2 + j];
+      for (int i = 0; i < kNrVec; ++i) s[i] = first ? -s[i] : s[i];
     }
-    if (!inside) c[i] = __builtin_nanf("");
-  }
-}
-
-// Values of the partners of the lane's dimensions of one head.
-template <typename T, int PAIRS>
-__device__ __forceinline__ void nr_partners(const T* head, const float* own, int e0, int R,
-                                            float* f) {
-  if (PAIRS == kPairsInLane) {
+  } else if (PAIRS == kPairsInLane && R % 8 == 0) {  // four angles in a row
+    if (e0 < R) {
+      const f32x4 u = *reinterpret_cast<const f32x4*>(row + e0 / 2);
+      const f32x4 v = *reinterpret_cast<const f32x4*>(row + R / 2 + e0 / 2);
 #pragma unroll
-    for (int i = 0; i < kNrVec; ++i) f[i] = own[i ^ 1];
-  } else if (PAIRS == kPairsInLine) {
-    nr_load<T>(head + nr_partner(e0, R, false), f);
+      for (int i = 0; i < kNrVec; ++i) {
+        c[i] = u[i / 2];
+        s[i] = i & 1 ? v[i / 2] : -v[i / 2];
+      }
+    }
   } else {
 #pragma unroll
-    for (int i = 0; i < kNrVec; ++i) f[i] = to_f32(head[nr_partner(e0 + i, R, false)]);
+    for (int i = 0; i < kNrVec; ++i) {
+      const int e = e0 + i;
+      if (e < R) {
+        const int j = PAIRS == kPairsInLane ? e >> 1 : (e < R / 2 ? e : e - R / 2);
+        const bool first = PAIRS == kPairsInLane ? !(e & 1) : e < R / 2;
+        c[i] = row[j];
+        s[i] = first ? -row[R / 2 + j] : row[R / 2 + j];
+      }
+    }
   }
+  if (!inside)
+#pragma unroll
+    for (int i = 0; i < kNrVec; ++i) c[i] = __builtin_nanf("");
 }
+
+// The lane's part of a head as it is stored, and its partners' part.
+template <typename T, int PAIRS> struct NrHead {
+  T own[kNrVec], other[kNrVec];
+  __device__ __forceinline__ void load(const T* head, int e0, int R, bool partners) {
+    typedef T Vec __attribute__((ext_vector_type(16 / sizeof(T))));
+    constexpr int n = 16 / sizeof(T);
+#pragma unroll
+    for (int i = 0; i < kNrVec; i += n)
+      *reinterpret_cast<Vec*>(own + i) = *reinterpret_cast<const Vec*>(head + e0 + i);
+    if (PAIRS == kPairsInLane || !partners) return;
+    if (PAIRS == kPairsInLine) {
+      const int p = nr_partner(e0, R, false);
+#pragma unroll
+      for (int i = 0; i < kNrVec; i += n)
+        *reinterpret_cast<Vec*>(other + i) = *reinterpret_cast<const Vec*>(head + p + i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kNrVec; ++i) other[i] = head[nr_partner(e0 + i, R, false)];
+    }
+  }
+  __device__ __forceinline__ float partner(int i) const {
+    return to_f32(PAIRS == kPairsInLane ? own[i ^ 1] : other[i]);
+  }
+};
 
 template <typename T>
 __device__ __forceinline__ int64_t nr_position(const NrSide<T>& a, int64_t t, int B) {
@@ -126,7 +153,9 @@ __device__ __forceinline__ int64_t nr_position(const NrSide<T>& a, int64_t t, in
   return t - a.offsets[i];
 }
 
-// grid: x over groups of tokens, y over the head chunks of q, then of k.
+// grid: x over groups of tokens, y over the head chunks of q, then of k. The
+// next heads are loaded before the present ones are stored (which may be in
+// the same array, at heads already read).
 template <typename T, int PAIRS>
 __global__ __launch_bounds__(kNrThreads) void k_norm_rotary(NrSide<T> q, NrSide<T> k,
                                                             const float* table, int64_t positions,
@@ -138,53 +167,56 @@ __global__ __launch_bounds__(kNrThreads) void k_norm_rotary(NrSide<T> q, NrSide<
   const int groups = kNrThreads / lanes;
   const int e0 = (threadIdx.x % lanes) * kNrVec;
   const bool live = e0 < D;
+  const int ec = live ? e0 : 0;  // lanes past the head read its first dimensions
   const int h0 = chunk * a.per_chunk;
   const int h1 = h0 + a.per_chunk < a.heads ? h0 + a.per_chunk : a.heads;
   float w[kNrVec], wp[kNrVec];
 #pragma unroll
   for (int i = 0; i < kNrVec; ++i) {
-    w[i] = a.w && live ? a.w[e0 + i] : 1.0f;
-    wp[i] = a.w && live ? a.w[nr_partner(e0 + i, R, PAIRS == kPairsInLane)] : 1.0f;
+    w[i] = a.w ? a.w[ec + i] : 1.0f;
+    wp[i] = a.w ? a.w[nr_partner(ec + i, R, PAIRS == kPairsInLane)] : 1.0f;
   }
   // whole groups leave together
   for (int64_t t = (int64_t)blockIdx.x * groups + threadIdx.x / lanes; t < a.tokens;
        t += (int64_t)gridDim.x * groups) {
+    const T* x = a.x + t * a.ld;
+    T* y = a.y + t * a.ld_y;
+    NrHead<T, PAIRS> now[kNrHeadsAtOnce], next[kNrHeadsAtOnce];
+#pragma unroll
+    for (int u = 0; u < kNrHeadsAtOnce; ++u)
+      next[u].load(x + (h0 + u < h1 ? h0 + u : h0) * D, ec, R, R > 0);
     float c[kNrVec], s[kNrVec];
 #pragma unroll
     for (int i = 0; i < kNrVec; ++i) {
       c[i] = 1.0f;
       s[i] = 0.0f;
     }
-    if (R && live)
-      nr_angles(table, nr_position(a, t, B), positions, R, PAIRS == kPairsInLane, e0, c, s);
-    const T* x = a.x + t * a.ld;
-    T* y = a.y + t * a.ld_y;
+    if (R) nr_angles<PAIRS>(table, nr_position(a, t, B), positions, R, ec, c, s);
     for (int h = h0; h < h1; h += kNrHeadsAtOnce) {
-      float v[kNrHeadsAtOnce][kNrVec], f[kNrHeadsAtOnce][kNrVec];
-      // the heads' loads first: their stores may write the same array
 #pragma unroll
-      for (int u = 0; u < kNrHeadsAtOnce; ++u) {
-        const int hu = h + u < h1 ? h + u : h;
+      for (int u = 0; u < kNrHeadsAtOnce; ++u) now[u] = next[u];
+      if (h + kNrHeadsAtOnce < h1) {
 #pragma unroll
-        for (int i = 0; i < kNrVec; ++i) v[u][i] = f[u][i] = 0.0f;
-        if (live) {
-          nr_load<T>(x + hu * D + e0, v[u]);
-          nr_partners<T, PAIRS>(x + hu * D, v[u], e0, R, f[u]);
+        for (int u = 0; u < kNrHeadsAtOnce; ++u) {
+          const int hu = h + kNrHeadsAtOnce + u;
+          next[u].load(x + (hu < h1 ? hu : h1 - 1) * D, ec, R, R > 0);
         }
       }
 #pragma unroll
       for (int u = 0; u < kNrHeadsAtOnce; ++u) {
-        float r = 1.0f;
+        float r = 1.0f, v[kNrVec];
         if (a.w) {
           float sum = 0.0f;
 #pragma unroll
-          for (int i = 0; i < kNrVec; ++i) sum += v[u][i] * v[u][i];
-          r = 1.0f / sqrtf(nr_group_sum(sum, lanes) / (float)D + eps);
+          for (int i = 0; i < kNrVec; ++i) sum += to_f32(now[u].own[i]) * to_f32(now[u].own[i]);
+          r = 1.0f / sqrtf(nr_group_sum(live ? sum : 0.0f, lanes) / (float)D + eps);
         }
 #pragma unroll
-        for (int i = 0; i < kNrVec; ++i)
-          v[u][i] = v[u][i] * r * w[i] * c[i] + f[u][i] * r * wp[i] * s[i];
-        if (live && h + u < h1) nr_store<T>(y + (h + u) * D + e0, v[u]);
+        for (int i = 0; i < kNrVec; ++i) {
+          v[i] = to_f32(now[u].own[i]) * r * w[i] * c[i];
+          if (R) v[i] += now[u].partner(i) * r * wp[i] * s[i];
+        }
+        if (live && h + u < h1) nr_store<T>(y + (h + u) * D + e0, v);
       }
     }
   }
@@ -198,102 +230,124 @@ __global__ __launch_bounds__(kNrThreads) void k_norm_rotary_bwd(NrSide<T> q, NrS
                                                                 const float* table,
                                                                 int64_t positions, int B, int D,
                                                                 int R, int lanes, float eps) {
-  __shared__ float sums[kNrThreads * kNrVec];
+  __shared__ float sums[kNrThreads / 64][16 * kNrVec];
   const bool is_q = (int)blockIdx.y < q.chunks;
   const NrSide<T>& a = is_q ? q : k;
   const int chunk = is_q ? blockIdx.y : blockIdx.y - q.chunks;
   const int groups = kNrThreads / lanes;
   const int e0 = (threadIdx.x % lanes) * kNrVec;
   const bool live = e0 < D;
+  const int ec = live ? e0 : 0;
   const int h0 = chunk * a.per_chunk;
   const int h1 = h0 + a.per_chunk < a.heads ? h0 + a.per_chunk : a.heads;
   float w[kNrVec], gw[kNrVec];
 #pragma unroll
   for (int i = 0; i < kNrVec; ++i) {
-    w[i] = a.w && live ? a.w[e0 + i] : 1.0f;
+    w[i] = a.w ? a.w[ec + i] : 1.0f;
     gw[i] = 0.0f;
   }
   for (int64_t t = (int64_t)blockIdx.x * groups + threadIdx.x / lanes; t < a.tokens;
        t += (int64_t)gridDim.x * groups) {
+    const T* x = a.x + t * a.ld;
+    const T* g = a.g + t * (int64_t)a.heads * D;
+    T* y = a.y + t * a.ld_y;
+    NrHead<T, PAIRS> gn[kNrHeadsAtOnce], gc[kNrHeadsAtOnce];
+    NrHead<T, kPairsInLane> xn[kNrHeadsAtOnce], xc[kNrHeadsAtOnce];
+#pragma unroll
+    for (int u = 0; u < kNrHeadsAtOnce; ++u) {
+      const int hu = h0 + u < h1 ? h0 + u : h0;
+      gn[u].load(g + hu * D, ec, R, R > 0);
+      if (a.w) xn[u].load(x + hu * D, ec, R, false);
+    }
     float c[kNrVec], s[kNrVec];
 #pragma unroll
     for (int i = 0; i < kNrVec; ++i) {
       c[i] = 1.0f;
       s[i] = 0.0f;
     }
-    if (R && live)
-      nr_angles(table, nr_position(a, t, B), positions, R, PAIRS == kPairsInLane, e0, c, s);
-    const T* x = a.x + t * a.ld;
-    const T* g = a.g + t * (int64_t)a.heads * D;
-    T* y = a.y + t * a.ld_y;
+    if (R) nr_angles<PAIRS>(table, nr_position(a, t, B), positions, R, ec, c, s);
     for (int h = h0; h < h1; h += kNrHeadsAtOnce) {
-      float v[kNrHeadsAtOnce][kNrVec], d[kNrHeadsAtOnce][kNrVec], f[kNrHeadsAtOnce][kNrVec];
 #pragma unroll
       for (int u = 0; u < kNrHeadsAtOnce; ++u) {
-        const int hu = h + u < h1 ? h + u : h;
+        gc[u] = gn[u];
+        xc[u] = xn[u];
+      }
+      if (h + kNrHeadsAtOnce < h1) {
 #pragma unroll
-        for (int i = 0; i < kNrVec; ++i) v[u][i] = d[u][i] = f[u][i] = 0.0f;
-        if (live) {
-          if (a.w) nr_load<T>(x + hu * D + e0, v[u]);
-          nr_load<T>(g + hu * D + e0, d[u]);
-          nr_partners<T, PAIRS>(g + hu * D, d[u], e0, R, f[u]);
+        for (int u = 0; u < kNrHeadsAtOnce; ++u) {
+          const int hu = h + kNrHeadsAtOnce + u < h1 ? h + kNrHeadsAtOnce + u : h1 - 1;
+          gn[u].load(g + hu * D, ec, R, R > 0);
+          if (a.w) xn[u].load(x + hu * D, ec, R, false);
         }
       }
 #pragma unroll
       for (int u = 0; u < kNrHeadsAtOnce; ++u) {
         const bool mine = live && h + u < h1;
+        float d[kNrVec];
 #pragma unroll
-        for (int i = 0; i < kNrVec; ++i) d[u][i] = d[u][i] * c[i] - f[u][i] * s[i];
+        for (int i = 0; i < kNrVec; ++i) {
+          d[i] = to_f32(gc[u].own[i]) * c[i];
+          if (R) d[i] -= gc[u].partner(i) * s[i];
+        }
         if (a.w) {
-          float sum = 0.0f, dot = 0.0f;
-#pragma unroll
-          for (int i = 0; i < kNrVec; ++i) sum += v[u][i] * v[u][i];
-          const float r = 1.0f / sqrtf(nr_group_sum(sum, lanes) / (float)D + eps);
+          float sum = 0.0f, dot = 0.0f, v[kNrVec];
 #pragma unroll
           for (int i = 0; i < kNrVec; ++i) {
-            v[u][i] *= r;  // xhat
-            if (mine) gw[i] += d[u][i] * v[u][i];
-            d[u][i] *= w[i];
-            dot += live ? d[u][i] * v[u][i] : 0.0f;
+            v[i] = to_f32(xc[u].own[i]);
+            sum += v[i] * v[i];
+            dot += d[i] * w[i] * v[i];
           }
-          dot = nr_group_sum(dot, lanes) / (float)D;
+          sum = nr_group_sum(live ? sum : 0.0f, lanes);
+          dot = nr_group_sum(live ? dot : 0.0f, lanes);
+          const float r = 1.0f / sqrtf(sum / (float)D + eps);
+          dot = dot * r / (float)D;  // mean of h w xhat
 #pragma unroll
-          for (int i = 0; i < kNrVec; ++i) d[u][i] = r * (d[u][i] - v[u][i] * dot);
+          for (int i = 0; i < kNrVec; ++i) {
+            v[i] *= r;  // xhat
+            if (mine) gw[i] += d[i] * v[i];
+            d[i] = r * (d[i] * w[i] - v[i] * dot);
+          }
         }
-        if (mine) nr_store<T>(y + (h + u) * D + e0, d[u]);
+        if (mine) nr_store<T>(y + (h + u) * D + e0, d);
       }
     }
   }
   if (!a.w) return;
+  // the wave's groups by lane exchanges, then the waves in order
 #pragma unroll
-  for (int i = 0; i < kNrVec; ++i) sums[threadIdx.x * kNrVec + i] = gw[i];
+  for (int i = 0; i < kNrVec; ++i) {
+    for (int m = lanes; m < 64; m <<= 1) gw[i] += __shfl_xor(gw[i], m);
+    if ((threadIdx.x & 63) < lanes && live) sums[threadIdx.x >> 6][e0 + i] = gw[i];
+  }
   __syncthreads();
-  // dimension e of group n is sums[n lanes 8 + e]: added in group order
   for (int e = threadIdx.x; e < D; e += kNrThreads) {
     float sum = 0.0f;
-    for (int n = 0; n < groups; ++n) sum += sums[n * lanes * kNrVec + e];
+    for (int n = 0; n < kNrThreads / 64; ++n) sum += sums[n][e];
     a.part[((int64_t)chunk * gridDim.x + blockIdx.x) * D + e] = sum;
   }
 }
 
 // Weight gradients: the partial sums added in a fixed order in fp64 (there
-// are up to 4,096 of them). Block y: q or k; 16 dimensions a block.
+// are up to a few thousand of them). Block y: q or k; 4 dimensions a block,
+// so 64 threads share the rows of each.
 __global__ __launch_bounds__(256) void k_norm_weight_sum(const float* part_q, const float* part_k,
                                                          int rows_q, int rows_k, float* g_q,
                                                          float* g_k, int D) {
-  __shared__ double sums[256];
+  __shared__ double sums[4][4];
   const float* part = blockIdx.y ? part_k : part_q;
   const int rows = blockIdx.y ? rows_k : rows_q;
   float* g = blockIdx.y ? g_k : g_q;
-  const int col = threadIdx.x & 15, e = blockIdx.x * 16 + col;
+  if (!g) return;
+  const int e = blockIdx.x * 4 + (threadIdx.x & 3);
   double sum = 0.0;
-  if (g && e < D)
-    for (int r = threadIdx.x >> 4; r < rows; r += 16) sum += (double)part[(int64_t)r * D + e];
-  sums[threadIdx.x] = sum;
+#pragma unroll 8
+  for (int r = threadIdx.x >> 2; r < rows; r += 64) sum += (double)part[(int64_t)r * D + e];
+  for (int m = 4; m < 64; m <<= 1) sum += __shfl_xor(sum, m);
+  if ((threadIdx.x & 63) < 4) sums[threadIdx.x >> 6][threadIdx.x & 3] = sum;
   __syncthreads();
-  if (threadIdx.x >= 16 || !g || e >= D) return;
-  for (int r = 1; r < 16; ++r) sum += sums[r * 16 + col];
-  g[e] = (float)sum;
+  if (threadIdx.x < 4)
+    g[e] = (float)(sums[0][threadIdx.x] + sums[1][threadIdx.x] + sums[2][threadIdx.x] +
+                   sums[3][threadIdx.x]);
 }
 
 __global__ __launch_bounds__(256) void k_rotary_table(float* table, int64_t positions, int R,
@@ -421,7 +475,7 @@ hipError_t backward(const nt_partition& p, const nt_norm_rotary& n, const void* 
     if (e != hipSuccess) return e;
   }
   if (!w_q && !w_k) return hipSuccess;
-  k_norm_weight_sum<<<dim3((n.head_dim + 15) / 16, 2), 256, 0, stream>>>(
+  k_norm_weight_sum<<<dim3(n.head_dim / 4, 2), 256, 0, stream>>>(
       a.part, b.part, (int)(a.chunks * bx), (int)(b.chunks * bx), w_q ? g_w_q : nullptr,
       w_k ? g_w_k : nullptr, n.head_dim);
   return hipGetLastError();
