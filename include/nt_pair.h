@@ -742,7 +742,7 @@ nt_status nt_attention_backward_workspace_bytes(const nt_partition* p, const nt_
  * shared key heads summing over their query heads. Masked cells and rows
  * with lse = -inf give zero. With NT_BF16 P and dS are rounded to bf16 before
  * their products. Sums run in a fixed order (no atomics). NT_ERR_OVERFLOW as
- * the forward's, and with a bias T_cols of 2^27 or more. The gradients
+ * the forward's, and with a bias T_cols of 2^23 or more. The gradients
  * must not overlap the inputs or each other. workspace: device, 16-byte
  * aligned.
  */

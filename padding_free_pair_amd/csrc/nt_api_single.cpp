@@ -348,8 +348,8 @@ nt_status nt_single_attention_backward(const nt_partition* p, const nt_attention
   const uint64_t lse_bytes = (uint64_t)p->T * x.heads * sizeof(float);
   if (bias) NT_TRY(check_array("bias", bias, bias_bytes));
   if (y.bias) NT_TRY(check_array("g_bias", y.bias, bias_bytes));
-  if (bias && p->T_cols >= int64_t(1) << 27)
-    return fail(NT_ERR_OVERFLOW, "T_cols = %lld with a bias must be below 2^27",
+  if (bias && p->T_cols >= int64_t(1) << 23)
+    return fail(NT_ERR_OVERFLOW, "T_cols = %lld with a bias must be below 2^23",
                 (long long)p->T_cols);
   if (y.bias && !bias) return fail(NT_ERR_NULL, "g_bias without a bias");
   NT_TRY(check_array("lse", lse, lse_bytes));

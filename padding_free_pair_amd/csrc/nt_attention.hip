@@ -5,11 +5,14 @@
 // head, (row, head of the group) with the head fastest, so shared key heads
 // fill the rows of a tile and are read once for their group. It forms the
 // scores transposed, S^T = K Q^T: a lane then holds one row's scores for 32 of
-// a tile's 64 keys, its softmax is within the lane and its partner in the
+// a tile's keys, its softmax is within the lane and its partner in the
 // other half, and the probabilities are, as they stand, the fragments of the
-// second product O^T = V^T P^T: they never leave the registers. Four waves
-// share each tile of keys and values in LDS; the next tile's loads are in
-// flight meanwhile, into the other of two buffers.
+// second product O^T = V^T P^T: they never leave the registers. The waves of a
+// workgroup share each tile of keys and values in LDS, which loads write
+// directly, one or two tiles ahead. QW waves own
+// different rows; KW waves own the same rows and take different blocks of 32
+// keys of each tile, each with its own running maximum, and are joined at the
+// end: few or short samples then still fill the card.
 #include <math.h>
 
 #include "nt_attention_tile.hpp"
@@ -18,10 +21,7 @@
 namespace nt {
 namespace {
 
-constexpr int kAtWaves = 4;
-constexpr int kAtThreads = 64 * kAtWaves;
-constexpr int kAtRows = 32 * kAtWaves;  // virtual rows of a workgroup
-constexpr int kAtKeys = 64;             // keys of a tile
+constexpr int kAtThreads = 256;
 
 struct AtArgs {
   const int64_t *eta, *mu, *cell0;
@@ -36,14 +36,30 @@ struct AtArgs {
   float *part_o, *part_ml;
 };
 
-template <typename T, int DP, bool BIAS, bool CAUSAL>
-__global__ __launch_bounds__(kAtThreads, sizeof(T) == 4 && DP > 64 ? 1 : 2) void k_attention(AtArgs a) {
+template <typename T, int DP, int QW, int KW, int NB, bool BIAS, bool CAUSAL>
+__global__ __launch_bounds__(kAtThreads, sizeof(T) == 4 && DP > 64 ? 1 : 2) void k_attention(
+    AtArgs a) {
+  static_assert(64 * QW * KW == kAtThreads, "four waves");
   constexpr int KS = DP / 16, DT = DP / 32;
-  typedef AtAlong<T, DP> LK;
-  typedef AtAcross<T, DP> LV;
+  constexpr int ROWS = 32 * QW, KEYS = 32 * KW * NB;  // of a workgroup; of a tile
   typedef typename AtFrag<T>::type Frag;
-  __shared__ __align__(16) T lds[2][kAtKeys * (LK::pitch + LV::pitch)];
+  typedef AtLoad<T, KEYS, DP, kAtThreads> Load;
+  constexpr int TILE = KEYS * AtTile<T, DP>::pitch, kPair = 2 * TILE * (int)sizeof(T);
+  // Tiles in flight: two where three pairs of tiles leave room for a second
+  // workgroup on the CU (160 KB), else one.
+  constexpr int AHEAD = 3 * kPair <= 80 * 1024 ? 2 : 1, BUFS = AHEAD + 1;
+  constexpr int kLds = BUFS * kPair, kJoin = (KW - 1) * QW * (DP / 2 + 2) * 64 * 4;
+  // Operations behind a tile's own loads when it is needed: the next tile's
+  // loads, and the bias of whole tiles, which is loaded two tiles ahead of its
+  // use (a tile that ends within its block may take fewer loads than four a
+  // block, and is not counted).
+  constexpr int TAIL = (AHEAD - 1) * (2 * Load::kPieces + (BIAS ? 4 * NB : 0));
+  constexpr int BEHIND = (AHEAD - 1) * (2 * Load::kPieces + (BIAS ? 8 * NB : 0));
+  __shared__ __align__(16) char lds_bytes[kLds > kJoin ? kLds : kJoin];
+  const T* lds = reinterpret_cast<const T*>(lds_bytes);
+  const uint32_t lds_at = at_lds(lds_bytes);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l32 = lane & 31, h = lane >> 5;
+  const int qw = wave / KW, kw = wave % KW;
   // Key heads fastest: with 8 of them (or 4, 16 ..) an XCD, which takes every
   // eighth workgroup, stays with its own heads' keys, and all heads advance
   // together. Tiles in reverse, so that a causal sample's longest rows begin
@@ -52,13 +68,13 @@ __global__ __launch_bounds__(kAtThreads, sizeof(T) == 4 && DP > 64 ? 1 : 2) void
   const int split = blockIdx.x / a.K % a.splits;
   const int64_t slot = a.slots - 1 - blockIdx.x / a.K / a.splits;
   const int G = a.H / a.K;
-  const int i = at_sample_of(a.eta, a.B, G, kAtRows, slot);
-  const int64_t tile = slot - (a.eta[i] * G / kAtRows + i);
+  const int i = at_sample_of(a.eta, a.B, G, ROWS, slot);
+  const int64_t tile = slot - (a.eta[i] * G / ROWS + i);
   const int64_t n = a.rows[i], m = a.cols[i];
-  if (tile * kAtRows >= n * G) return;
+  if (tile * ROWS >= n * G) return;
 
   // this lane's row
-  const int64_t vr = tile * kAtRows + wave * 32 + l32;
+  const int64_t vr = tile * ROWS + qw * 32 + l32;
   const bool live = vr < n * G;
   const int64_t r = (live ? vr : n * G - 1) / G;
   const int hq = hk * G + (int)((live ? vr : n * G - 1) % G);
@@ -68,18 +84,18 @@ __global__ __launch_bounds__(kAtThreads, sizeof(T) == 4 && DP > 64 ? 1 : 2) void
   // keys of this split, up to the last that a row of the workgroup sees
   int64_t c1 = m;
   if (CAUSAL) {
-    const int64_t vlast = tile * kAtRows + kAtRows - 1;
+    const int64_t vlast = tile * ROWS + ROWS - 1;
     const int64_t rl = (vlast < n * G ? vlast : n * G - 1) / G;
     c1 = rl + 1 + m - n;
     c1 = c1 < 0 ? 0 : c1 < m ? c1 : m;
   }
   int64_t c0 = 0;
   if (a.splits > 1) {
-    const int64_t per = ((c1 + a.splits - 1) / a.splits + kAtKeys - 1) / kAtKeys * kAtKeys;
+    const int64_t per = ((c1 + a.splits - 1) / a.splits + KEYS - 1) / KEYS * KEYS;
     c0 = split * per < c1 ? split * per : c1;
     c1 = c0 + per < c1 ? c0 + per : c1;
   }
-  const int keys = (int)m, end = (int)c1, last = (int)seen;
+  const int keys = (int)m, last = (int)seen;
   // the fewest keys that a row of this wave sees: no masks below it
   const int seen0 = __builtin_amdgcn_readfirstlane(last);
 
@@ -103,57 +119,61 @@ __global__ __launch_bounds__(kAtThreads, sizeof(T) == 4 && DP > 64 ? 1 : 2) void
   for (int d = 0; d < DT; ++d) o[d] = f32x16{};
   float most = -INFINITY, sum = 0.0f;  // of this row; sum: this half's keys
   const float unit = BIAS ? 1.0f : scale * kLog2e;  // a score's unit in powers of two
-  AtStage<T, kAtKeys, DP, kAtThreads> sk(a.ld_k), sv(a.ld_v);
+  const Load load_k(a.ld_k), load_v(a.ld_v);
+  AtBias<T, NB> bias_even, bias_odd;
+  const int mine = 32 * kw * NB;  // this wave's first key in a tile
+  const int tiles = (int)((c1 - c0 + KEYS - 1) / KEYS);
   kp += c0 * a.ld_k;
   vp += c0 * a.ld_v;
-  if (c0 < c1) {
-    sk.load(kp, a.ld_k, keys - (int)c0, a.D);
-    sv.load(vp, a.ld_v, keys - (int)c0, a.D);
-    sk.template put<LK>(lds[0]);
-    sv.template put<LV>(lds[0] + kAtKeys * LK::pitch);
-  }
-  __syncthreads();
-  int buf = 0;
-  for (int c = (int)c0; c < end; c += kAtKeys, buf ^= 1) {
-    const bool more = c + kAtKeys < end;
-    if (more) {
-      kp += kAtKeys * a.ld_k;
-      vp += kAtKeys * a.ld_v;
-      sk.load(kp, a.ld_k, keys - c - kAtKeys, a.D);
-      sv.load(vp, a.ld_v, keys - c - kAtKeys, a.D);
-    }
-    const T* lk = lds[buf];
-    const T* lv = lds[buf] + kAtKeys * LK::pitch;
-    f32x16 s[2];
+  int left = keys - (int)c0, to = 0;  // keys from the tile to load on; its buffer
+  auto start = [&]() {
+    load_k.start(kp, a.ld_k, left, a.D, lds_at + to * kPair);
+    load_v.start(vp, a.ld_v, left, a.D, lds_at + to * kPair + kPair / 2);
+    kp += KEYS * a.ld_k;
+    vp += KEYS * a.ld_v;
+    left -= KEYS;
+    to = to + 1 == BUFS ? 0 : to + 1;
+  };
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
+  for (int j = 0; j < AHEAD; ++j)
+    if (j < tiles) start();
+  if (BIAS && tiles > 0) bias_even.load(bp, (int)c0 + mine, keys, h);
+  if (BIAS && tiles > 1) bias_odd.load(bp, (int)c0 + KEYS + mine, keys, h);
+  int buf = 0, c = (int)c0;
+  auto step = [&](int j, AtBias<T, NB>& bias) {
+    if (j + AHEAD < tiles) at_arrive<BEHIND>();
+    else if (j + AHEAD - 1 < tiles) at_arrive<TAIL>();
+    else at_arrive<0>();
+    if (j + AHEAD < tiles) start();
+    const T* lk = lds + buf * 2 * TILE;
+    const T* lv = lk + TILE;
+    f32x16 s[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
       s[b] = f32x16{};
 #pragma unroll
-      for (int x = 0; x < KS; ++x) s[b] = at_mma(at_along<LK>(lk, 32 * b + l32, x, h), q[x], s[b]);
+      for (int x = 0; x < KS; ++x)
+        s[b] = at_mma(at_along<DP>(lk, mine + 32 * b + l32, x, h), q[x], s[b]);
     }
     if (BIAS) {
 #pragma unroll
-      for (int b = 0; b < 2; ++b)
+      for (int b = 0; b < NB; ++b)
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          float f[4];
-          at_bias4(bp, c + 32 * b + 8 * g + 4 * h, keys, f);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[b][4 * g + e] = s[b][4 * g + e] * scale + f[e];
-        }
+        for (int x = 0; x < 16; ++x) s[b][x] = s[b][x] * scale + to_f32((T)bias.v[b][x / 4][x % 4]);
+      if (j + 2 < tiles) bias.load(bp, c + 2 * KEYS + mine, keys, h);
     }
-    if (c + kAtKeys > (CAUSAL ? seen0 : keys)) {
+    if (c + KEYS > (CAUSAL ? seen0 : keys)) {
       at_rare();
-      const int left = last - c - 4 * h;
+      const int left = last - c - mine - 4 * h;
 #pragma unroll
-      for (int b = 0; b < 2; ++b)
+      for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int x = 0; x < 16; ++x)
           if (32 * b + 8 * (x / 4) + x % 4 >= left) s[b][x] = -INFINITY;
     }
     float top = s[0][0];
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
+    for (int b = 0; b < NB; ++b)
 #pragma unroll
       for (int x = 0; x < 16; ++x) top = fmaxf(top, s[b][x]);
     top = at_halves_max(top);
@@ -171,7 +191,7 @@ __global__ __launch_bounds__(kAtThreads, sizeof(T) == 4 && DP > 64 ? 1 : 2) void
     }
     const float base = most == -INFINITY ? 0.0f : most;
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
+    for (int b = 0; b < NB; ++b)
 #pragma unroll
       for (int x = 0; x < 16; ++x) {
         const float p = BIAS ? __builtin_amdgcn_exp2f((s[b][x] - base) * kLog2e)
@@ -180,20 +200,63 @@ __global__ __launch_bounds__(kAtThreads, sizeof(T) == 4 && DP > 64 ? 1 : 2) void
         sum += p;
       }
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
+    for (int x = 0; x < 2 * NB; ++x) {
       Frag p;
       at_pack(s[x / 2], 8 * (x % 2), p);
 #pragma unroll
       for (int d = 0; d < DT; ++d)
-        o[d] = at_mma(at_across<LV>(lv, 16 * x, 32 * d), p, o[d]);
+        o[d] = at_mma(at_across<DP>(lv, mine + 16 * x, 32 * d), p, o[d]);
     }
-    if (more) {
-      sk.template put<LK>(lds[buf ^ 1]);
-      sv.template put<LV>(lds[buf ^ 1] + kAtKeys * LK::pitch);
+    c += KEYS;
+    buf = buf + 1 == BUFS ? 0 : buf + 1;
+  };
+  if constexpr (BIAS) {
+    for (int j = 0; j < tiles; j += 2) {
+      step(j, bias_even);
+      if (j + 1 < tiles) step(j + 1, bias_odd);
     }
-    __syncthreads();
+  } else {
+    for (int j = 0; j < tiles; ++j) step(j, bias_even);
   }
   sum += __shfl_xor(sum, 32);
+  if (KW > 1) {  // the waves of the same rows, in order, at their common maximum
+    __syncthreads();
+    float* join = reinterpret_cast<float*>(lds_bytes);
+    constexpr int kPart = (16 * DT + 2) * 64;
+    if (kw > 0) {
+      float* p = join + ((kw - 1) * QW + qw) * kPart + lane;
+      p[0] = most;
+      p[64] = sum;
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int x = 0; x < 16; ++x) p[(2 + 16 * d + x) * 64] = o[d][x];
+    }
+    __syncthreads();
+    if (kw > 0) return;
+    const float step = BIAS ? kLog2e : unit;
+    float now = most;
+#pragma unroll
+    for (int w = 1; w < KW; ++w) now = fmaxf(now, join[((w - 1) * QW + qw) * kPart + lane]);
+    const float base = now == -INFINITY ? 0.0f : now;
+    float keep = __builtin_amdgcn_exp2f((most - base) * step);
+    sum *= keep;
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+      for (int x = 0; x < 16; ++x) o[d][x] *= keep;
+#pragma unroll
+    for (int w = 1; w < KW; ++w) {
+      const float* p = join + ((w - 1) * QW + qw) * kPart + lane;
+      keep = __builtin_amdgcn_exp2f((p[0] - base) * step);
+      sum += p[64] * keep;
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int x = 0; x < 16; ++x) o[d][x] += p[(2 + 16 * d + x) * 64] * keep;
+    }
+    most = now;
+  }
   if (!live) return;
   const int64_t at = t * a.H + hq;
   if (a.splits > 1) {
@@ -224,7 +287,8 @@ __global__ __launch_bounds__(kAtThreads, sizeof(T) == 4 && DP > 64 ? 1 : 2) void
   if (h == 0) a.lse[at] = (BIAS ? most : most * scale) + logf(sum);
 }
 
-// Joins the splits of a row: one wave for each, a dimension or two a lane.
+// Joins the splits of a row: a wave for each. The lanes first hold the splits'
+// maxima and sums (at most 64), then the dimensions, two each.
 template <typename T>
 __global__ __launch_bounds__(256) void k_attention_join(const float* part_o, const float* part_ml,
                                                         int splits, int64_t rows, int D, T* o,
@@ -232,57 +296,90 @@ __global__ __launch_bounds__(256) void k_attention_join(const float* part_o, con
   const int lane = threadIdx.x & 63;
   for (int64_t at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); at < rows;
        at += (int64_t)gridDim.x * 4) {
-    float most = -INFINITY, sum = 0.0f, acc[2] = {0.0f, 0.0f};
-    for (int s = 0; s < splits; ++s) most = fmaxf(most, part_ml[(s * rows + at) * 2]);
-    const float base = most == -INFINITY ? 0.0f : most;
-    for (int s = 0; s < splits; ++s) {
-      const float* ml = part_ml + (s * rows + at) * 2;
-      const float w = expf(ml[0] - base);
-      sum += w * ml[1];
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-        if (lane + 64 * e < D) acc[e] += w * part_o[(s * rows + at) * D + lane + 64 * e];
+    float most = -INFINITY, sum = 0.0f;
+    if (lane < splits) {
+      most = part_ml[(lane * rows + at) * 2];
+      sum = part_ml[(lane * rows + at) * 2 + 1];
     }
+    float top = most;
+#pragma unroll
+    for (int x = 1; x < 64; x <<= 1) top = fmaxf(top, __shfl_xor(top, x));
+    const float w = lane < splits ? expf(most - (top == -INFINITY ? 0.0f : top)) : 0.0f;
+    sum *= w;
+#pragma unroll
+    for (int x = 1; x < 64; x <<= 1) sum += __shfl_xor(sum, x);
+    float acc[2] = {0.0f, 0.0f};
+    const int d0 = lane < D ? lane : 0, d1 = lane + 64 < D ? lane + 64 : 0;
+    for (int s = 0; s < splits; s += 8) {  // eight loads at a time
+      float v[8][2];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const float* p = part_o + ((s + u < splits ? s + u : s) * rows + at) * D;
+        v[u][0] = p[d0];
+        v[u][1] = p[d1];
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        if (s + u < splits) {
+          const float ws = __shfl(w, s + u);
+          acc[0] += ws * v[u][0];
+          acc[1] += ws * v[u][1];
+        }
+      }
+    }
+    const float inv = sum > 0.0f ? 1.0f / sum : 1.0f;
 #pragma unroll
     for (int e = 0; e < 2; ++e)
-      if (lane + 64 * e < D)
-        o[at * D + lane + 64 * e] = from_f32<T>(sum > 0.0f ? acc[e] / sum : 0.0f);
-    if (lane == 0) lse[at] = most + logf(sum);
+      if (lane + 64 * e < D) o[at * D + lane + 64 * e] = from_f32<T>(acc[e] * inv);
+    if (lane == 0) lse[at] = top + logf(sum);
   }
 }
 
-// In how many parts the keys are split: one, unless the rows alone leave the
-// card idle and there are keys to share out.
-int splits_of(const nt_partition& p, const nt_attention& a) {
-  if (p.T == 0 || p.B == 0) return 1;
-  const int64_t groups = at_slots(p.T, p.B, a.heads / a.kv_heads, kAtRows) * a.kv_heads;
+// How the waves of a workgroup are shared out, and in how many parts the keys
+// are split over workgroups.
+struct AtPlan {
+  int qw, splits;
+};
+AtPlan plan_of(const nt_partition& p, const nt_attention& a) {
+  if (p.T == 0 || p.B == 0) return {4, 1};
+  const int G = a.heads / a.kv_heads;
+  auto groups = [&](int qw) { return at_slots(p.T, p.B, G, 32 * qw) * a.kv_heads; };
+  const int qw = groups(4) >= 1024 ? 4 : 2;
   const int64_t keys = p.T_cols / p.B;
-  if (groups >= 512 || keys < 512) return 1;
-  int64_t s = 2048 / groups;
-  if (s > keys / 128) s = keys / 128;
-  return (int)(s < 1 ? 1 : s > 64 ? 64 : s);
+  int64_t s = 1;
+  if (groups(qw) < 512 && keys >= 512) {
+    s = 2048 / groups(qw);
+    if (s > keys / 128) s = keys / 128;
+  }
+  return {qw, (int)(s < 1 ? 1 : s > 64 ? 64 : s)};
 }
 
-template <typename T, int DP>
+template <typename T, int DP, int QW, int KW, int NB>
 hipError_t run(const AtArgs& x, bool causal, hipStream_t stream) {
   const unsigned g = (unsigned)(x.slots * x.splits * x.K);
   if (x.bias) {
-    if (causal) k_attention<T, DP, true, true><<<g, kAtThreads, 0, stream>>>(x);
-    else k_attention<T, DP, true, false><<<g, kAtThreads, 0, stream>>>(x);
+    if (causal) k_attention<T, DP, QW, KW, NB, true, true><<<g, kAtThreads, 0, stream>>>(x);
+    else k_attention<T, DP, QW, KW, NB, true, false><<<g, kAtThreads, 0, stream>>>(x);
   } else {
-    if (causal) k_attention<T, DP, false, true><<<g, kAtThreads, 0, stream>>>(x);
-    else k_attention<T, DP, false, false><<<g, kAtThreads, 0, stream>>>(x);
+    if (causal) k_attention<T, DP, QW, KW, NB, false, true><<<g, kAtThreads, 0, stream>>>(x);
+    else k_attention<T, DP, QW, KW, NB, false, false><<<g, kAtThreads, 0, stream>>>(x);
   }
   return hipGetLastError();
 }
+template <typename T, int DP>
+hipError_t run(const AtArgs& x, int qw, bool causal, hipStream_t stream) {
+  if (qw == 4) return run<T, DP, 4, 1, 2>(x, causal, stream);
+  return run<T, DP, 2, 2, 1>(x, causal, stream);
+}
 
 template <typename T>
-hipError_t forward(const nt_partition& p, const nt_attention& a, AtArgs x, hipStream_t stream) {
+hipError_t forward(const nt_partition& p, const nt_attention& a, const AtArgs& x, int qw,
+                   hipStream_t stream) {
   hipError_t e;
-  if (a.head_dim <= 32) e = run<T, 32>(x, a.causal, stream);
-  else if (a.head_dim <= 64) e = run<T, 64>(x, a.causal, stream);
-  else if (a.head_dim <= 96) e = run<T, 96>(x, a.causal, stream);
-  else e = run<T, 128>(x, a.causal, stream);
+  if (a.head_dim <= 32) e = run<T, 32>(x, qw, a.causal, stream);
+  else if (a.head_dim <= 64) e = run<T, 64>(x, qw, a.causal, stream);
+  else if (a.head_dim <= 96) e = run<T, 96>(x, qw, a.causal, stream);
+  else e = run<T, 128>(x, qw, a.causal, stream);
   if (e != hipSuccess || x.splits == 1) return e;
   const int64_t rows = p.T * a.heads, blocks = (rows + 3) / 4;
   k_attention_join<T><<<(unsigned)(blocks < (1 << 20) ? blocks : (1 << 20)), 256, 0, stream>>>(
@@ -296,12 +393,12 @@ hipError_t forward(const nt_partition& p, const nt_attention& a, AtArgs x, hipSt
 bool attention_fits(const nt_partition& p, const nt_attention& a) {
   const int64_t most = (int64_t(1) << 32) / kAtThreads;
   // the smallest tiles that any kernel here or of the gradients takes
-  return at_slots(p.T, p.B, a.heads / a.kv_heads, 64) * splits_of(p, a) * a.kv_heads < most &&
-         at_slots(p.T_cols, p.B, 1, 64) * a.kv_heads < most;
+  return at_slots(p.T, p.B, a.heads / a.kv_heads, 32) * plan_of(p, a).splits * a.kv_heads < most &&
+         at_slots(p.T_cols, p.B, 1, 32) * a.kv_heads < most;
 }
 
 size_t attention_ws_bytes(const nt_partition& p, const nt_attention& a, nt_dtype) {
-  const int s = splits_of(p, a);
+  const int s = plan_of(p, a).splits;
   if (s == 1) return 0;
   return (size_t)s * p.T * a.heads * (a.head_dim + 2) * sizeof(float);
 }
@@ -317,7 +414,6 @@ hipError_t launch_attention(const nt_partition& p, const nt_attention& a, const 
   x.rows = p.lengths;
   x.cols = p.col_lengths;
   x.cells = p.cells;
-  x.slots = at_slots(p.T, p.B, a.heads / a.kv_heads, kAtRows);
   x.ld_q = a.ld_q;
   x.ld_k = a.ld_k;
   x.ld_v = a.ld_v;
@@ -326,7 +422,9 @@ hipError_t launch_attention(const nt_partition& p, const nt_attention& a, const 
   x.H = a.heads;
   x.K = a.kv_heads;
   x.D = a.head_dim;
-  x.splits = splits_of(p, a);
+  const AtPlan plan = plan_of(p, a);
+  x.slots = at_slots(p.T, p.B, a.heads / a.kv_heads, 32 * plan.qw);
+  x.splits = plan.splits;
   x.scale = a.scale;
   x.q = q;
   x.k = k;
@@ -336,7 +434,8 @@ hipError_t launch_attention(const nt_partition& p, const nt_attention& a, const 
   x.lse = lse;
   x.part_o = static_cast<float*>(ws);
   x.part_ml = x.part_o + (int64_t)x.splits * x.part_rows * a.head_dim;
-  return dtype == NT_BF16 ? forward<bf16>(p, a, x, stream) : forward<float>(p, a, x, stream);
+  return dtype == NT_BF16 ? forward<bf16>(p, a, x, plan.qw, stream)
+                          : forward<float>(p, a, x, plan.qw, stream);
 }
 
 }  // namespace nt

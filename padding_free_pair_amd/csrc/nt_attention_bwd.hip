@@ -5,14 +5,14 @@
 // repeat bit by bit. The first owns 32 virtual rows (queries of one key head,
 // as in the forward) in a wave and walks over the keys: it forms S^T = K Q^T and
 // dP^T = V G^T, and their dS^T is, as it stands, the fragment of
-// g_q^T += K^T dS^T. It also leaves each row's delta for the second, which owns
-// 32 keys in a wave and walks over the virtual rows: S = Q K^T and dP = G V^T
-// give P and dS as fragments of g_v^T += G^T P and g_k^T += Q^T dS; the rows of
-// all query heads of the group pass by, so shared key heads sum in registers.
-// The scores and dP are formed twice (7 products instead of 5); joining the
-// walks would need g_q summed across workgroups.
+// g_q^T += K^T dS^T. It also leaves each row's log sum and delta, prepared and
+// row by row for each head, to the second, which owns 32 keys in a wave and
+// walks over the rows of each query head of the group in turn: S = Q K^T and
+// dP = G V^T give P and dS as fragments of g_v^T += G^T P and g_k^T += Q^T dS,
+// and shared key heads sum in registers. The scores and dP are formed twice (7
+// products instead of 5); joining the walks would need g_q summed across
+// workgroups.
 #include <math.h>
-#include <stdlib.h>
 
 #include "nt_attention_tile.hpp"
 #include "nt_internal.hpp"
@@ -20,44 +20,54 @@
 namespace nt {
 namespace {
 
-constexpr int kAbTile = 64;  // rows of a tile in LDS: keys, or virtual rows
-
 struct AbArgs {
   const int64_t *eta, *mu, *cell0;
   const int32_t *rows, *cols;
-  int64_t cells, slots, ld_q, ld_k, ld_v, ld_gq, ld_gk, ld_gv;
+  int64_t T, cells, slots, ld_q, ld_k, ld_v, ld_gq, ld_gk, ld_gv;
   int B, H, K, D, causal;
   float scale;
   const void *q, *k, *v, *bias, *o, *g_o;
   const float* lse;
   void *g_q, *g_k, *g_v, *g_bias;
-  float* delta;  // [T, H]
+  float *logs, *delta;  // [H, T]
 };
 
-template <typename T>
+// Tiles in flight: two where that leaves room for a second workgroup on the CU.
+constexpr int ab_ahead(int pair_bytes) { return 3 * pair_bytes <= 80 * 1024 ? 2 : 1; }
+
 __device__ __forceinline__ float ab_dot(const bf16x8& a, const bf16x8& b) {
   float s = 0.0f;
 #pragma unroll
   for (int j = 0; j < 8; ++j) s += (float)a[j] * (float)b[j];
   return s;
 }
-template <typename T> __device__ __forceinline__ float ab_dot(const f32x8& a, const f32x8& b) {
+__device__ __forceinline__ float ab_dot(const f32x8& a, const f32x8& b) {
   float s = 0.0f;
 #pragma unroll
   for (int j = 0; j < 8; ++j) s += a[j] * b[j];
   return s;
 }
 
-// g_q of 32 virtual rows a wave, and their delta.
-template <typename T, int DP, int WAVES, bool BIAS>
-__global__ __launch_bounds__(64 * WAVES, sizeof(T) == 4 && DP > 64 ? 1 : 2) void k_attention_bwd_q(
+// g_q of 32 virtual rows a wave, and their statistics. As in the forward, QW
+// waves own different rows, and KW waves the same rows and different keys.
+template <typename T, int DP, int QW, int KW, int NB, bool BIAS>
+__global__ __launch_bounds__(64 * QW * KW, sizeof(T) == 4 && DP > 64 ? 1 : 2) void k_attention_bwd_q(
     AbArgs a) {
-  constexpr int KS = DP / 16, DT = DP / 32, THREADS = 64 * WAVES, ROWS = 32 * WAVES;
-  typedef AtBoth<T, DP> L;
-  constexpr int TILE = kAbTile * L::pitch;
+  constexpr int KS = DP / 16, DT = DP / 32, THREADS = 64 * QW * KW;
+  constexpr int ROWS = 32 * QW, KEYS = 32 * KW * NB;
   typedef typename AtFrag<T>::type Frag;
-  __shared__ __align__(16) T lds[2][2 * TILE];
+  typedef AtLoad<T, KEYS, DP, THREADS> Load;
+  constexpr int TILE = KEYS * AtTile<T, DP>::pitch, kPair = 2 * TILE * (int)sizeof(T);
+  constexpr int AHEAD = ab_ahead(kPair), BUFS = AHEAD + 1;
+  // as in the forward
+  constexpr int TAIL = (AHEAD - 1) * (2 * Load::kPieces + (BIAS ? 4 * NB : 0));
+  constexpr int BEHIND = (AHEAD - 1) * (2 * Load::kPieces + (BIAS ? 8 * NB : 0));
+  constexpr int kLds = BUFS * kPair, kJoin = (KW - 1) * QW * DP / 2 * 64 * 4;
+  __shared__ __align__(16) char lds_bytes[kLds > kJoin ? kLds : kJoin];
+  const T* lds = reinterpret_cast<const T*>(lds_bytes);
+  const uint32_t lds_at = at_lds(lds_bytes);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l32 = lane & 31, h = lane >> 5;
+  const int qw = wave / KW, kw = wave % KW;
   // as in the forward: key heads fastest, a causal sample's longest rows first
   const int hk = blockIdx.x % a.K;
   const int64_t slot = a.slots - 1 - blockIdx.x / a.K;
@@ -67,7 +77,7 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 4 && DP > 64 ? 1 : 2) void
   const int64_t n = a.rows[i], m = a.cols[i];
   if (tile * ROWS >= n * G) return;
 
-  const int64_t vr = tile * ROWS + wave * 32 + l32;
+  const int64_t vr = tile * ROWS + qw * 32 + l32;
   const bool live = vr < n * G;
   const int64_t r = (live ? vr : n * G - 1) / G;
   const int hq = hk * G + (int)((live ? vr : n * G - 1) % G);
@@ -81,7 +91,7 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 4 && DP > 64 ? 1 : 2) void
     c1 = rl + 1 + m - n;
     c1 = c1 < 0 ? 0 : c1 < m ? c1 : m;
   }
-  const int keys = (int)m, end = (int)c1, last = (int)seen;
+  const int keys = (int)m, last = (int)seen;
   const int seen0 = a.causal ? __builtin_amdgcn_readfirstlane(last) : keys;
 
   Frag q[KS], g[KS];
@@ -95,84 +105,118 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 4 && DP > 64 ? 1 : 2) void
     if (16 * s + 8 * h < a.D) {
       q[s] = at_row(qp, s, h);
       g[s] = at_row(gp, s, h);
-      delta += ab_dot<T>(g[s], at_row(op, s, h));
+      delta += ab_dot(g[s], at_row(op, s, h));
     }
   }
   delta += __shfl_xor(delta, 32);
-  if (live && h == 0) a.delta[at] = delta;
   // a row that saw nothing gives nothing
   const float lse = a.lse[at] == -INFINITY ? INFINITY : a.lse[at];
+  const float base = lse * kLog2e;
+  if (live && h == 0 && kw == 0) {
+    a.logs[hq * a.T + t] = BIAS ? lse : base;
+    a.delta[hq * a.T + t] = delta;
+  }
   const T* kp = static_cast<const T*>(a.k) + a.mu[i] * a.ld_k + (int64_t)hk * a.D;
   const T* vp = static_cast<const T*>(a.v) + a.mu[i] * a.ld_v + (int64_t)hk * a.D;
-  const T* bp = BIAS ? static_cast<const T*>(a.bias) + hq * a.cells + a.cell0[i] + r * m : nullptr;
+  const T* bp = static_cast<const T*>(a.bias) + hq * a.cells + a.cell0[i] + r * m;
 
   f32x16 gq[DT];
 #pragma unroll
   for (int d = 0; d < DT; ++d) gq[d] = f32x16{};
-  const float unit = a.scale * kLog2e, base = lse * kLog2e;
-  AtStage<T, kAbTile, DP, THREADS> sk(a.ld_k), sv(a.ld_v);
-  if (end > 0) {
-    sk.load(kp, a.ld_k, keys, a.D);
-    sv.load(vp, a.ld_v, keys, a.D);
-    sk.template put<L>(lds[0]);
-    sv.template put<L>(lds[0] + TILE);
-  }
-  __syncthreads();
-  int buf = 0;
-  for (int c = 0; c < end; c += kAbTile, buf ^= 1) {
-    const bool more = c + kAbTile < end;
-    if (more) {
-      kp += kAbTile * a.ld_k;
-      vp += kAbTile * a.ld_v;
-      sk.load(kp, a.ld_k, keys - c - kAbTile, a.D);
-      sv.load(vp, a.ld_v, keys - c - kAbTile, a.D);
-    }
-    const T* lk = lds[buf];
-    const T* lv = lds[buf] + TILE;
+  const float unit = a.scale * kLog2e;
+  const Load load_k(a.ld_k), load_v(a.ld_v);
+  AtBias<T, NB> bias_even, bias_odd;
+  const int mine = 32 * kw * NB;  // this wave's first key in a tile
+  const int tiles = (int)((c1 + KEYS - 1) / KEYS);
+  int left = keys, to = 0;  // keys from the tile to load on; its buffer
+  auto start = [&]() {
+    load_k.start(kp, a.ld_k, left, a.D, lds_at + to * kPair);
+    load_v.start(vp, a.ld_v, left, a.D, lds_at + to * kPair + kPair / 2);
+    kp += KEYS * a.ld_k;
+    vp += KEYS * a.ld_v;
+    left -= KEYS;
+    to = to + 1 == BUFS ? 0 : to + 1;
+  };
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      f32x16 s = f32x16{}, dp = f32x16{};
+  for (int j = 0; j < AHEAD; ++j)
+    if (j < tiles) start();
+  if (BIAS && tiles > 0) bias_even.load(bp, mine, keys, h);
+  if (BIAS && tiles > 1) bias_odd.load(bp, KEYS + mine, keys, h);
+  int buf = 0, c = 0;
+  auto step = [&](int j, AtBias<T, NB>& bias) {
+    if (j + AHEAD < tiles) at_arrive<BEHIND>();
+    else if (j + AHEAD - 1 < tiles) at_arrive<TAIL>();
+    else at_arrive<0>();
+    if (j + AHEAD < tiles) start();
+    const T* lk = lds + buf * 2 * TILE;
+    const T* lv = lk + TILE;
+    f32x16 s[NB], dp[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      s[b] = dp[b] = f32x16{};
 #pragma unroll
       for (int x = 0; x < KS; ++x) {
-        s = at_mma(at_along<L>(lk, 32 * b + l32, x, h), q[x], s);
-        dp = at_mma(at_along<L>(lv, 32 * b + l32, x, h), g[x], dp);
+        s[b] = at_mma(at_along<DP>(lk, mine + 32 * b + l32, x, h), q[x], s[b]);
+        dp[b] = at_mma(at_along<DP>(lv, mine + 32 * b + l32, x, h), g[x], dp[b]);
       }
-      if (BIAS) {
+    }
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          float f[4];
-          at_bias4(bp, c + 32 * b + 8 * y + 4 * h, keys, f);
+    for (int b = 0; b < NB; ++b)
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            s[4 * y + e] = (s[4 * y + e] * a.scale + f[e] - lse) * kLog2e;
-        }
-      } else {
-#pragma unroll
-        for (int x = 0; x < 16; ++x) s[x] = s[x] * unit - base;
+      for (int x = 0; x < 16; ++x) {
+        s[b][x] = BIAS ? (s[b][x] * a.scale + to_f32((T)bias.v[b][x / 4][x % 4]) - lse) * kLog2e
+                       : s[b][x] * unit - base;
+        s[b][x] = __builtin_amdgcn_exp2f(s[b][x]) * (dp[b][x] - delta);
       }
+    if (BIAS && j + 2 < tiles) bias.load(bp, c + 2 * KEYS + mine, keys, h);
+    if (c + KEYS > seen0) {
+      at_rare();
+      const int end = last - c - mine - 4 * h;
 #pragma unroll
-      for (int x = 0; x < 16; ++x) s[x] = __builtin_amdgcn_exp2f(s[x]) * (dp[x] - delta);
-      if (c + kAbTile > seen0) {
-        at_rare();
-        const int left = last - c - 4 * h;
+      for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int x = 0; x < 16; ++x)
-          if (32 * b + 8 * (x / 4) + x % 4 >= left) s[x] = 0.0f;
-      }
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        Frag f;
-        at_pack(s, 8 * x, f);
-#pragma unroll
-        for (int d = 0; d < DT; ++d)
-          gq[d] = at_mma(at_across<L>(lk, 32 * b + 16 * x, 32 * d), f, gq[d]);
-      }
+          if (32 * b + 8 * (x / 4) + x % 4 >= end) s[b][x] = 0.0f;
     }
-    if (more) {
-      sk.template put<L>(lds[buf ^ 1]);
-      sv.template put<L>(lds[buf ^ 1] + TILE);
+#pragma unroll
+    for (int x = 0; x < 2 * NB; ++x) {
+      Frag f;
+      at_pack(s[x / 2], 8 * (x % 2), f);
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+        gq[d] = at_mma(at_across<DP>(lk, mine + 16 * x, 32 * d), f, gq[d]);
+    }
+    c += KEYS;
+    buf = buf + 1 == BUFS ? 0 : buf + 1;
+  };
+  if constexpr (BIAS) {
+    for (int j = 0; j < tiles; j += 2) {
+      step(j, bias_even);
+      if (j + 1 < tiles) step(j + 1, bias_odd);
+    }
+  } else {
+    for (int j = 0; j < tiles; ++j) step(j, bias_even);
+  }
+  if (KW > 1) {  // the waves of the same rows, in order
+    __syncthreads();
+    float* join = reinterpret_cast<float*>(lds_bytes);
+    if (kw > 0) {
+      float* p = join + ((kw - 1) * QW + qw) * DT * 16 * 64 + lane;
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int x = 0; x < 16; ++x) p[(16 * d + x) * 64] = gq[d][x];
     }
     __syncthreads();
+    if (kw > 0) return;
+#pragma unroll
+    for (int w = 1; w < KW; ++w) {
+      const float* p = join + ((w - 1) * QW + qw) * DT * 16 * 64 + lane;
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int x = 0; x < 16; ++x) gq[d][x] += p[(16 * d + x) * 64];
+    }
   }
   if (!live) return;
   T* out = static_cast<T*>(a.g_q) + t * a.ld_gq + (int64_t)hq * a.D;
@@ -185,21 +229,29 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 4 && DP > 64 ? 1 : 2) void
                   gq[d][4 * y + 2] * a.scale, gq[d][4 * y + 3] * a.scale);
 }
 
-// g_k and g_v of 32 keys a wave, and the bias's gradient. KW waves of a
+// g_k and g_v of 32 keys a wave, and the bias's gradient dS: a store covers 64
+// bytes of two rows. (From the first kernel, whose lanes hold four cells each of
+// 32 rows, the stores took 14 us instead of 5 on 21.5 million cells.) KW waves of a
 // workgroup own different keys; RW waves own the same keys and take different
 // blocks of 32 rows of each tile, and their sums are joined at the end in
 // order, so few keys still fill the card.
-template <typename T, int DP, int KW, int RW, bool BIAS>
-__global__ __launch_bounds__(64 * KW * RW, DP > 64 ? 1 : 2) void k_attention_bwd_k(AbArgs a) {
+template <typename T, int DP, int KW, int RW, int NB, bool BIAS>
+__global__ __launch_bounds__(64 * KW * RW, DP > 64 || (sizeof(T) == 4 && RW == 4) ? 1 : 2) void k_attention_bwd_k(AbArgs a) {
   constexpr int KS = DP / 16, DT = DP / 32, THREADS = 64 * KW * RW, KEYS = 32 * KW;
-  constexpr int NB = RW == 1 ? 2 : 1, ROWS = 32 * RW * NB;  // blocks of a wave, rows of a tile
-  typedef AtBoth<T, DP> L;
-  constexpr int TILE = ROWS * L::pitch;
-  constexpr int kLds = 2 * 2 * TILE * (int)sizeof(T), kJoin = (RW - 1) * KW * 2 * DP * 32 * 4;
+  constexpr int ROWS = 32 * RW * NB;  // of a tile: NB blocks of a wave
   typedef typename AtFrag<T>::type Frag;
+  typedef AtLoad<T, ROWS, DP, THREADS> Load;
+  constexpr int TILE = ROWS * AtTile<T, DP>::pitch, kPair = 2 * TILE * (int)sizeof(T);
+  constexpr int AHEAD = ab_ahead(kPair), BUFS = AHEAD + 1;
+  // behind a tile's loads: the next tile's, its bias and the next one's
+  constexpr int BEHIND = (AHEAD - 1) * (2 * Load::kPieces + NB + (BIAS ? 32 * NB : 0));
+  constexpr int kLds = BUFS * kPair, kJoin = (RW - 1) * KW * 2 * DP * 32 * 4;
   __shared__ __align__(16) char lds_bytes[kLds > kJoin ? kLds : kJoin];
-  __shared__ __align__(16) float stats[2][2][ROWS];  // [buffer][log sum, delta]
-  T* lds = reinterpret_cast<T*>(lds_bytes);
+  // each wave's own rows: log sums, then deltas
+  __shared__ __align__(16) float stats[BUFS][KW * RW][2][32 * NB];
+  const T* lds = reinterpret_cast<const T*>(lds_bytes);
+  const uint32_t lds_at = at_lds(lds_bytes);
+  const uint32_t stats_at = at_lds(stats);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l32 = lane & 31, h = lane >> 5;
   const int kw = wave / RW, rw = wave % RW;
   // a causal sample's first keys, which the most rows see, begin first
@@ -244,147 +296,175 @@ __global__ __launch_bounds__(64 * KW * RW, DP > 64 ? 1 : 2) void k_attention_bwd
     for (int g = 0; g < G; ++g)
       for (int64_t r = 2 * rw + h; r < first; r += 2 * RW)
         g_bias[(int64_t)(hk * G + g) * a.cells + r * m + key] = from_f32<T>(0.0f);
-  const int rows = (int)n, per_head = (int)((n - first + ROWS - 1) / ROWS), tiles = per_head * G;
+  const int rows = (int)n, from = (int)first;
+  const int tiles = (int)((n - first + ROWS - 1) / ROWS) * G;
 
-  AtStage<T, ROWS, DP, THREADS> sq(a.ld_q), sg((int64_t)a.H * a.D);
-  float row_lse = 0.0f, row_delta = 0.0f;
-  // Bias of this lane's key at its rows. Rows are m elements apart from a uniform
-  // base; a lane's distance from it, of its key and its half's four rows, is
-  // one register (T_cols < 2^27 with a bias).
-  T b_now[NB][16], b_next[NB][16];
-  const uint32_t b_off = (uint32_t)((4 * h * (uint32_t)m + (uint32_t)keyc) * sizeof(T));
-  int next_h = hk * G, next_r = (int)first;  // head and first row of the tile to fetch
-  auto fetch = [&]() {
-    const int hq = next_h, r0 = next_r;
-    next_r += ROWS;
-    if (next_r >= rows) {
-      next_r = (int)first;
-      ++next_h;
+  // The loads run ahead of the products: their own head and row.
+  const Load load_q(a.ld_q), load_g((int64_t)a.H * a.D);
+  int load_h = hk * G, load_r = from, to = 0;
+  auto start = [&]() {
+    const int left = rows - load_r;
+    const int64_t t0 = a.eta[i] + load_r;
+    load_q.start(static_cast<const T*>(a.q) + t0 * a.ld_q + (int64_t)load_h * a.D, a.ld_q, left,
+                 a.D, lds_at + to * kPair);
+    load_g.start(static_cast<const T*>(a.g_o) + (t0 * a.H + load_h) * a.D, (int64_t)a.H * a.D,
+                 left, a.D, lds_at + to * kPair + kPair / 2);
+    const float* p = a.logs + load_h * a.T + t0;
+    const float* d = a.delta + load_h * a.T + t0;
+    const uint32_t stats_to = stats_at + (to * KW * RW + wave) * 2 * 32 * NB * 4;
+    if (NB == 1) {  // a half of the wave each
+      const int x = 32 * rw + l32, y = x < left ? x : left - 1;
+      at_load_lds<4>((h ? d : p) + y, stats_to);
+    } else {
+      const int x = 64 * rw + lane, y = x < left ? x : left - 1;
+      at_load_lds<4>(p + y, stats_to);
+      at_load_lds<4>(d + y, stats_to + 32 * NB * 4);
     }
-    const int64_t t0 = a.eta[i] + r0;
-    sq.load(static_cast<const T*>(a.q) + t0 * a.ld_q + (int64_t)hq * a.D, a.ld_q, rows - r0, a.D);
-    sg.load(static_cast<const T*>(a.g_o) + (t0 * a.H + hq) * a.D, (int64_t)a.H * a.D, rows - r0, a.D);
-    if (threadIdx.x < ROWS) {
-      const bool in = r0 + (int)threadIdx.x < rows;
-      const int64_t at = (t0 + (in ? threadIdx.x : 0)) * a.H + hq;
-      const float z = a.lse[at];
-      // a row that saw nothing, or is none, gives nothing
-      row_lse = in && z != -INFINITY ? (BIAS ? z : z * kLog2e) : INFINITY;
-      row_delta = a.delta[at];
-    }
-    if (BIAS) {
-      const T* p = bias + (int64_t)hq * a.cells + r0 * m;
-      if (r0 + ROWS <= rows) {
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-          for (int x = 0; x < 16; ++x) {
-            const T* pr = p + (32 * (rw * NB + b) + 8 * (x / 4) + x % 4) * m;
-            b_next[b][x] = *reinterpret_cast<const T*>(reinterpret_cast<const char*>(pr) + b_off);
-          }
-      } else {
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-          for (int x = 0; x < 16; ++x) {
-            const int r = 32 * (rw * NB + b) + 8 * (x / 4) + 4 * h + x % 4;
-            b_next[b][x] = p[(r < rows - r0 ? r : rows - r0 - 1) * m + keyc];
-          }
-      }
+    to = to + 1 == BUFS ? 0 : to + 1;
+    load_r += ROWS;
+    if (load_r >= rows) {
+      load_r = from;
+      ++load_h;
     }
   };
-  auto put = [&](int buf) {
-    sq.template put<L>(lds + buf * 2 * TILE);
-    sg.template put<L>(lds + buf * 2 * TILE + TILE);
-    if (threadIdx.x < ROWS) {
-      stats[buf][0][threadIdx.x] = row_lse;
-      stats[buf][1][threadIdx.x] = row_delta;
+  // Bias of this lane's key at its rows of a tile: rows are m elements apart
+  // from a uniform base, the lane's key and its half's four rows are one
+  // register's distance (T_cols < 2^23 with a bias).
+  struct Bias {
+    T v[NB][16];
+  } bias_even, bias_odd;
+  const uint32_t row_bytes = (uint32_t)(m * sizeof(T));
+  const uint32_t b_off = 4 * h * row_bytes + (uint32_t)(keyc * sizeof(T));
+  int bias_h = hk * G, bias_r = from;  // of the tile whose bias is loaded next
+  auto load_bias = [&](Bias& b) {
+    const T* p = bias + (int64_t)bias_h * a.cells + (int64_t)bias_r * m;
+    const int left = rows - bias_r;
+    bias_r += ROWS;
+    if (bias_r >= rows) {
+      bias_r = from;
+      ++bias_h;
+    }
+    if (left >= ROWS) {
+      const AtBuffer buffer(p);
+#pragma unroll
+      for (int u = 0; u < NB; ++u)
+#pragma unroll
+        for (int x = 0; x < 16; ++x)
+          b.v[u][x] = buffer.load<T>(b_off, (32 * (rw * NB + u) + 8 * (x / 4) + x % 4) * row_bytes);
+    } else {
+      const int64_t step = at_opaque(m);
+#pragma unroll
+      for (int u = 0; u < NB; ++u)
+#pragma unroll
+        for (int x = 0; x < 16; ++x) {
+          const int r = 32 * (rw * NB + u) + 8 * (x / 4) + 4 * h + x % 4;
+          b.v[u][x] = p[(r < left ? r : left - 1) * step + keyc];
+        }
     }
   };
-  if (tiles > 0) {
-    fetch();
-    put(0);
-  }
-  __syncthreads();
-  int buf = 0;
-  for (int j = 0, hq = hk * G, r0 = (int)first; j < tiles; ++j, buf ^= 1) {
-    const bool more = j + 1 < tiles;
-    if (BIAS) {
 #pragma unroll
-      for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int x = 0; x < 16; ++x) b_now[b][x] = b_next[b][x];
-    }
-    if (more) fetch();
+  for (int j = 0; j < AHEAD; ++j)
+    if (j < tiles) start();
+  if (BIAS && tiles > 0) load_bias(bias_even);
+  if (BIAS && tiles > 1) load_bias(bias_odd);
+  int buf = 0, hq = hk * G, r0 = from;
+  auto step = [&](int j, Bias& b) {
+    if (j + AHEAD - 1 < tiles) at_arrive<BEHIND>();
+    else at_arrive<0>();
+    if (j + AHEAD < tiles) start();
     const T* lq = lds + buf * 2 * TILE;
     const T* lg = lq + TILE;
+    const int mine = 32 * rw * NB;  // this wave's first row in the tile
+    f32x16 s[NB], dp[NB];
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      const int rb = 32 * (rw * NB + b);  // first row of the block in the tile
-      f32x16 s = f32x16{}, dp = f32x16{};
+    for (int u = 0; u < NB; ++u) {
+      s[u] = dp[u] = f32x16{};
 #pragma unroll
       for (int x = 0; x < KS; ++x) {
-        s = at_mma(at_along<L>(lq, rb + l32, x, h), k[x], s);
-        dp = at_mma(at_along<L>(lg, rb + l32, x, h), v[x], dp);
+        s[u] = at_mma(at_along<DP>(lq, mine + 32 * u + l32, x, h), k[x], s[u]);
+        dp[u] = at_mma(at_along<DP>(lg, mine + 32 * u + l32, x, h), v[x], dp[u]);
       }
+    }
+#pragma unroll
+    for (int u = 0; u < NB; ++u)
 #pragma unroll
       for (int y = 0; y < 4; ++y) {
-        const f32x4 z = *reinterpret_cast<const f32x4*>(&stats[buf][0][rb + 8 * y + 4 * h]);
-        const f32x4 d = *reinterpret_cast<const f32x4*>(&stats[buf][1][rb + 8 * y + 4 * h]);
+        const int w = 32 * u + 8 * y + 4 * h;
+        const f32x4 z = *reinterpret_cast<const f32x4*>(&stats[buf][wave][0][w]);
+        const f32x4 d = *reinterpret_cast<const f32x4*>(&stats[buf][wave][1][w]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int x = 4 * y + e;
           const float p = __builtin_amdgcn_exp2f(
-              BIAS ? (s[x] * a.scale + to_f32(b_now[b][x]) - z[e]) * kLog2e : s[x] * unit - z[e]);
-          s[x] = p;
-          dp[x] = p * (dp[x] - d[e]);
+              BIAS ? (s[u][x] * a.scale + to_f32(b.v[u][x]) - z[e]) * kLog2e
+                   : s[u][x] * unit - z[e]);
+          s[u][x] = p;
+          dp[u][x] = p * (dp[u][x] - d[e]);
         }
       }
-      if (a.causal && k0 + 31 > r0 + rb + ahead) {
-        at_rare();
-        const int past = (int)(key - ahead) - r0 - rb - 4 * h;  // rows before it do not see the key
+    // rows of this tile from this wave's first on, and the first that sees its keys
+    const int left = rows - r0 - mine;
+    if (left < 32 * NB || (a.causal && k0 + 31 > r0 + mine + ahead)) {
+      at_rare();
+      const int past = a.causal ? (int)(key - ahead) - r0 - mine - 4 * h : 0;
+      const int end = left - 4 * h;
 #pragma unroll
-        for (int x = 0; x < 16; ++x)
-          if (8 * (x / 4) + x % 4 < past) s[x] = dp[x] = 0.0f;
-      }
-      if (BIAS && a.g_bias && live) {
-        T* p = g_bias + (int64_t)hq * a.cells + (int64_t)(r0 + rb) * m;
-        const int left = rows - r0 - rb;
-        if (left >= 32) {
+      for (int u = 0; u < NB; ++u)
+#pragma unroll
+        for (int x = 0; x < 16; ++x) {
+          const int w = 32 * u + 8 * (x / 4) + x % 4;
+          if (w < past || w >= end) s[u][x] = dp[u][x] = 0.0f;
+        }
+    }
+    if (BIAS && j + 2 < tiles) load_bias(b);
+    if (BIAS && a.g_bias && live) {
+      T* p = g_bias + (int64_t)hq * a.cells + (int64_t)(r0 + mine) * m;
+      if (left >= 32 * NB) {
+        const AtBuffer buffer(p);
+#pragma unroll
+        for (int u = 0; u < NB; ++u)
 #pragma unroll
           for (int x = 0; x < 16; ++x)
-            *reinterpret_cast<T*>(reinterpret_cast<char*>(p + (8 * (x / 4) + x % 4) * m) + b_off) =
-                from_f32<T>(dp[x]);
-        } else {
-          at_rare();
+            buffer.store<T>(from_f32<T>(dp[u][x]), b_off, (32 * u + 8 * (x / 4) + x % 4) * row_bytes);
+      } else {
+        const int64_t step = at_opaque(m);
+#pragma unroll
+        for (int u = 0; u < NB; ++u)
 #pragma unroll
           for (int x = 0; x < 16; ++x) {
-            const int r = 8 * (x / 4) + 4 * h + x % 4;
-            if (r < left) p[r * m + key] = from_f32<T>(dp[x]);
+            const int r = 32 * u + 8 * (x / 4) + 4 * h + x % 4;
+            if (r < left) p[r * step + key] = from_f32<T>(dp[u][x]);
           }
-        }
-      }
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        Frag fp, fs;
-        at_pack(s, 8 * x, fp);
-        at_pack(dp, 8 * x, fs);
-#pragma unroll
-        for (int d = 0; d < DT; ++d) {
-          gv[d] = at_mma(at_across<L>(lg, rb + 16 * x, 32 * d), fp, gv[d]);
-          gk[d] = at_mma(at_across<L>(lq, rb + 16 * x, 32 * d), fs, gk[d]);
-        }
       }
     }
-    if (more) put(buf ^ 1);
-    __syncthreads();
+#pragma unroll
+    for (int x = 0; x < 2 * NB; ++x) {
+      Frag fp, fs;
+      at_pack(s[x / 2], 8 * (x % 2), fp);
+      at_pack(dp[x / 2], 8 * (x % 2), fs);
+#pragma unroll
+      for (int d = 0; d < DT; ++d) {
+        gv[d] = at_mma(at_across<DP>(lg, mine + 16 * x, 32 * d), fp, gv[d]);
+        gk[d] = at_mma(at_across<DP>(lq, mine + 16 * x, 32 * d), fs, gk[d]);
+      }
+    }
+    buf = buf + 1 == BUFS ? 0 : buf + 1;
     r0 += ROWS;
     if (r0 >= rows) {
-      r0 = (int)first;
+      r0 = from;
       ++hq;
     }
+  };
+  if constexpr (BIAS) {
+    for (int j = 0; j < tiles; j += 2) {
+      step(j, bias_even);
+      if (j + 1 < tiles) step(j + 1, bias_odd);
+    }
+  } else {
+    for (int j = 0; j < tiles; ++j) step(j, bias_even);
   }
   if (RW > 1) {  // the waves of the same keys, in order
+    __syncthreads();
     float* join = reinterpret_cast<float*>(lds_bytes);
     if (rw > 0) {
       float* p = join + ((rw - 1) * KW + kw) * 2 * DT * 16 * 64 + lane;
@@ -398,6 +478,7 @@ __global__ __launch_bounds__(64 * KW * RW, DP > 64 ? 1 : 2) void k_attention_bwd
     }
     __syncthreads();
     if (rw > 0) return;
+#pragma unroll
     for (int w = 1; w < RW; ++w) {
       const float* p = join + ((w - 1) * KW + kw) * 2 * DT * 16 * 64 + lane;
 #pragma unroll
@@ -425,34 +506,47 @@ __global__ __launch_bounds__(64 * KW * RW, DP > 64 ? 1 : 2) void k_attention_bwd
     }
 }
 
-template <typename T, int DP, int KW, int RW, bool BIAS>
+template <typename T, int DP, int QW, int KW, int NB, bool BIAS>
+hipError_t run_q(const nt_partition& p, AbArgs x, hipStream_t stream) {
+  x.slots = at_slots(p.T, p.B, x.H / x.K, 32 * QW);
+  k_attention_bwd_q<T, DP, QW, KW, NB, BIAS>
+      <<<(unsigned)(x.slots * x.K), 64 * QW * KW, 0, stream>>>(x);
+  return hipGetLastError();
+}
+template <typename T, int DP, int KW, int RW, int NB, bool BIAS>
 hipError_t run_k(const nt_partition& p, AbArgs x, hipStream_t stream) {
   x.slots = at_slots(p.T_cols, p.B, 1, 32 * KW);
-  k_attention_bwd_k<T, DP, KW, RW, BIAS>
+  k_attention_bwd_k<T, DP, KW, RW, NB, BIAS>
       <<<(unsigned)(x.slots * x.K), 64 * KW * RW, 0, stream>>>(x);
   return hipGetLastError();
 }
 
+// Waves share a tile of 128 rows (keys) where that makes eight workgroups a CU,
+// and two of them each 64 otherwise; fewer than one and a half workgroups of 64
+// keys a CU are split once more. Gradients of eight samples of 2,048 (D 64, 16
+// heads, 2,048 workgroups): 243 us against 260 with two waves for the queries,
+// 388 against 438 for the keys; of lengths 1024, 768, 384, 96 with a bias (D 32,
+// 12 heads, 252): 35 against 31, and 55 against 38; of 2,000 rows with 4 key
+// heads (D 128), keys: 126 with two waves, 79 with one.
 template <typename T, int DP, bool BIAS>
 hipError_t run(const nt_partition& p, AbArgs x, hipStream_t stream) {
+  // (two blocks of 32 at a time; a bias or fp32 fragments would not leave it the registers)
+  constexpr bool can_share = sizeof(T) == 2 && !BIAS;
   if (p.T) {
-    x.slots = at_slots(p.T, p.B, x.H / x.K, 128);
-    k_attention_bwd_q<T, DP, 4, BIAS><<<(unsigned)(x.slots * x.K), 256, 0, stream>>>(x);
-    const hipError_t e = hipGetLastError();
+    bool many = false;
+    if constexpr (can_share) many = at_slots(p.T, p.B, x.H / x.K, 128) * x.K >= 2048;
+    hipError_t e = hipSuccess;
+    if constexpr (can_share)
+      if (many) e = run_q<T, DP, 4, 1, 2, BIAS>(p, x, stream);
+    if (!many) e = run_q<T, DP, 2, 2, 1, BIAS>(p, x, stream);
     if (e != hipSuccess) return e;
   }
   if (!p.T_cols) return hipSuccess;
-  const int64_t groups = at_slots(p.T_cols, p.B, 1, 128) * x.K;
-  if (const char* ev = getenv("NT_BK")) {
-    const int c = atoi(ev);
-    if (c == 41) return run_k<T, DP, 4, 1, BIAS>(p, x, stream);
-    if (c == 22) return run_k<T, DP, 2, 2, BIAS>(p, x, stream);
-    if (c == 21) return run_k<T, DP, 2, 1, BIAS>(p, x, stream);
-    if (c == 12) return run_k<T, DP, 1, 2, BIAS>(p, x, stream);
-    if constexpr (sizeof(T) == 2) { if (c == 14) return run_k<bf16, DP, 1, 4, BIAS>(p, x, stream); }
-  }
-  if (groups >= 2048) return run_k<T, DP, 4, 1, BIAS>(p, x, stream);
-  return run_k<T, DP, 2, 2, BIAS>(p, x, stream);
+  if constexpr (can_share)
+    if (at_slots(p.T_cols, p.B, 1, 128) * x.K >= 2048) return run_k<T, DP, 4, 1, 2, BIAS>(p, x, stream);
+  if constexpr (sizeof(T) == 2 || DP <= 64)  // its tiles of 128 rows would not fit LDS
+    if (at_slots(p.T_cols, p.B, 1, 64) * x.K < 384) return run_k<T, DP, 1, 4, 1, BIAS>(p, x, stream);
+  return run_k<T, DP, 2, 2, 1, BIAS>(p, x, stream);
 }
 
 template <typename T, int DP>
@@ -471,7 +565,7 @@ hipError_t backward(const nt_partition& p, const AbArgs& x, hipStream_t stream) 
 }  // namespace
 
 size_t attention_backward_ws_bytes(const nt_partition& p, const nt_attention& a, nt_dtype) {
-  return (size_t)p.T * a.heads * sizeof(float);
+  return (size_t)p.T * a.heads * 2 * sizeof(float);
 }
 
 hipError_t launch_attention_backward(const nt_partition& p, const nt_attention& a, const void* q,
@@ -485,6 +579,7 @@ hipError_t launch_attention_backward(const nt_partition& p, const nt_attention& 
   x.cell0 = p.pair_offsets;
   x.rows = p.lengths;
   x.cols = p.col_lengths;
+  x.T = p.T;
   x.cells = p.cells;
   x.slots = 0;
   x.ld_q = a.ld_q;
@@ -510,7 +605,8 @@ hipError_t launch_attention_backward(const nt_partition& p, const nt_attention& 
   x.g_k = g.k;
   x.g_v = g.v;
   x.g_bias = g.bias;
-  x.delta = static_cast<float*>(ws);
+  x.logs = static_cast<float*>(ws);
+  x.delta = x.logs + p.T * a.heads;
   return dtype == NT_BF16 ? backward<bf16>(p, x, stream) : backward<float>(p, x, stream);
 }
 

@@ -36,36 +36,27 @@ __device__ __forceinline__ f32x16 at_mma(const f32x8& a, const f32x8& b, f32x16 
   return c;
 }
 
-// Where a tile of token rows keeps its elements in LDS, by the fragments that
-// are read from it, without bank conflicts.
-// AtAlong: along rows only. 16 rows are read at once, 16 bytes of each: a pitch
-// of an odd number of 16 bytes.
-template <typename T, int DP> struct AtAlong {
-  static constexpr int pitch = DP + 16 / (int)sizeof(T);
-  static __device__ __forceinline__ int at(int r, int c) { return r * pitch + c; }
-};
-// AtAcross: across rows only. bf16: four rows at once, 64 bytes of each: a pitch
-// of 64 bytes modulo 256, or of 192. fp32: rows 4 apart on different halves of
-// the banks.
-template <typename T, int DP> struct AtAcross {
-  static constexpr int pitch = sizeof(T) == 4 ? DP + 8 : DP % 64 == 0 ? DP + 32 : DP;
-  static __device__ __forceinline__ int at(int r, int c) { return r * pitch + c; }
-};
-// AtBoth: both. bf16: rows of 16-byte chunks, chunk c of row r at c ^ f(r);
-// along a row, 16 rows read one chunk each, which f must send to the 16 chunks
-// of 256 bytes; across rows, 4 rows read 4 neighbouring chunks each, which f
-// must send to the 4 different 64-byte pieces: f's high bits are r's low ones.
-// fp32: AtAlong's pitch, which serves the other kind half.
-template <typename T, int DP> struct AtBoth;
-template <int DP> struct AtBoth<bf16, DP> {
-  static constexpr int pitch = DP == 96 ? 128 : DP;
+// Where a tile of token rows keeps its elements in LDS: rows of 16-byte chunks
+// without padding (so that loads can write them as they come), chunk c of row
+// r at c ^ f(r). Fragments along rows read one chunk of 16 rows at once, which f
+// must send to the 16 chunks of 256 bytes. Fragments across rows read, in bf16,
+// 4 neighbouring chunks of 4 rows at once, which f must send to the 4 different
+// 64-byte pieces: f's high bits are r's low ones. In fp32 they read 8 chunks of
+// two rows 4 apart, which f sends to the two halves where a row has 16 chunks.
+template <typename T, int DP> struct AtTile {
+  static constexpr int vec = 16 / (int)sizeof(T);       // elements of a chunk
+  static constexpr int pitch = DP == 96 ? 128 : DP;     // elements of a row
+  static constexpr int chunks = pitch / vec;            // of a row
+  static __device__ __forceinline__ int turn(int r) {   // f
+    if (sizeof(T) == 2)
+      return chunks == 16 ? (r & 3) << 2 | ((r >> 2) & 3)
+             : chunks == 8 ? ((r >> 1) & 1) << 2 | ((r >> 2) & 3) : (r >> 2) & 3;
+    return chunks == 8 ? (r >> 1) & 7 : ((r >> 2) & 1) << 3 | ((r >> 3) & 1) << 2 | (r & 3);
+  }
   static __device__ __forceinline__ int at(int r, int c) {
-    const int f = pitch == 128 ? (r & 3) << 2 | ((r >> 2) & 3)
-                  : pitch == 64 ? ((r >> 1) & 1) << 2 | ((r >> 2) & 3) : (r >> 2) & 3;
-    return r * pitch + (((c >> 3) ^ f) << 3) + (c & 7);
+    return r * pitch + ((c / vec) ^ turn(r)) * vec + c % vec;
   }
 };
-template <int DP> struct AtBoth<float, DP> : AtAlong<float, DP> {};
 
 // Values 16 s + 8 h .. of a row in global memory as a fragment.
 __device__ __forceinline__ bf16x8 at_row(const bf16* row, int s, int h) {
@@ -78,11 +69,14 @@ __device__ __forceinline__ f32x8 at_row(const float* row, int s, int h) {
 }
 
 // Fragment along row r of a tile, values 16 s + 8 h ..
-template <typename L> __device__ __forceinline__ bf16x8 at_along(const bf16* tile, int r, int s, int h) {
-  return *reinterpret_cast<const bf16x8*>(tile + L::at(r, 16 * s + 8 * h));
+template <int DP> __device__ __forceinline__ bf16x8 at_along(const bf16* tile, int r, int s, int h) {
+  return *reinterpret_cast<const bf16x8*>(tile + AtTile<bf16, DP>::at(r, 16 * s + 8 * h));
 }
-template <typename L> __device__ __forceinline__ f32x8 at_along(const float* tile, int r, int s, int h) {
-  return at_row(tile + L::at(r, 0), s, h);
+template <int DP> __device__ __forceinline__ f32x8 at_along(const float* tile, int r, int s, int h) {
+  const f32x4 a = *reinterpret_cast<const f32x4*>(tile + AtTile<float, DP>::at(r, 16 * s + 8 * h));
+  const f32x4 b =
+      *reinterpret_cast<const f32x4*>(tile + AtTile<float, DP>::at(r, 16 * s + 8 * h + 4));
+  return f32x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
 }
 
 // Four bf16 by the transposing LDS read: within each 16 lanes, lane j's
@@ -95,22 +89,20 @@ __device__ __forceinline__ at_bf16x4 at_read_tr(const bf16* p) {
 
 // Fragment across rows: column c0 + l % 32 of the tile, rows r0 + {4 h + 0 ..
 // 3, 8 + 4 h + 0 .. 3} (the order of a product's results).
-template <typename L> __device__ __forceinline__ bf16x8 at_across(const bf16* tile, int r0, int c0) {
+template <int DP> __device__ __forceinline__ bf16x8 at_across(const bf16* tile, int r0, int c0) {
   const int lane = threadIdx.x & 63, h = lane >> 5, q = lane & 15, g = lane >> 4;
   const int r = r0 + 4 * h + (q >> 2), c = c0 + 16 * (g & 1) + 4 * (q & 3);
-  const at_bf16x4 a = at_read_tr(tile + L::at(r, c));
-  const at_bf16x4 b = at_read_tr(tile + L::at(r + 8, c));
+  const at_bf16x4 a = at_read_tr(tile + AtTile<bf16, DP>::at(r, c));
+  const at_bf16x4 b = at_read_tr(tile + AtTile<bf16, DP>::at(r + 8, c));
   return bf16x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
 }
-template <typename L> __device__ __forceinline__ f32x8 at_across(const float* tile, int r0, int c0) {
-  const int lane = threadIdx.x & 63, h = lane >> 5;
-  constexpr int P = L::pitch;
-  const float* p = tile + (r0 + 4 * h) * P + c0 + (lane & 31);
+template <int DP> __device__ __forceinline__ f32x8 at_across(const float* tile, int r0, int c0) {
+  const int lane = threadIdx.x & 63, r = r0 + 4 * (lane >> 5), c = c0 + (lane & 31);
   f32x8 f;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    f[j] = p[j * P];
-    f[4 + j] = p[(8 + j) * P];
+    f[j] = tile[AtTile<float, DP>::at(r + j, c)];
+    f[4 + j] = tile[AtTile<float, DP>::at(r + 8 + j, c)];
   }
   return f;
 }
@@ -125,80 +117,162 @@ __device__ __forceinline__ void at_pack(const f32x16& x, int i, f32x8& f) {
   for (int j = 0; j < 8; ++j) f[j] = x[i + j];
 }
 
-// Four consecutive values to global memory.
+// Four consecutive values to global memory, at any element.
 __device__ __forceinline__ void at_store4(bf16* p, float a, float b, float c, float d) {
-  *reinterpret_cast<at_bf16x4*>(p) = at_bf16x4{(bf16)a, (bf16)b, (bf16)c, (bf16)d};
+  const at_bf16x4 v = {(bf16)a, (bf16)b, (bf16)c, (bf16)d};
+  __builtin_memcpy(p, &v, sizeof(v));
 }
 __device__ __forceinline__ void at_store4(float* p, float a, float b, float c, float d) {
-  *reinterpret_cast<at_f32x4*>(p) = at_f32x4{a, b, c, d};
+  const at_f32x4 v = {a, b, c, d};
+  __builtin_memcpy(p, &v, sizeof(v));
 }
-
-// Four bias values of a row, from column c on; the ones past `m` as zeros. A row
-// begins at any element, so the four are one unaligned load.
-__device__ __forceinline__ void at_bias4(const bf16* p, int64_t c, int64_t m, float* f) {
-  if (c + 4 <= m) {
-    at_bf16x4 v;
-    __builtin_memcpy(&v, p + c, 8);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) f[e] = (float)v[e];
-  } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) f[e] = c + e < m ? (float)p[c + e] : 0.0f;
-  }
-}
-__device__ __forceinline__ void at_bias4(const float* p, int64_t c, int64_t m, float* f) {
-  if (c + 4 <= m) {
-    __builtin_memcpy(f, p + c, 16);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) f[e] = c + e < m ? p[c + e] : 0.0f;
-  }
-}
-
-// A tile of ROWS token rows of D elements (D <= DP) on its way to LDS: pieces
-// of 16 bytes, one after another over the THREADS threads. The distances of a
-// thread's pieces from the tile's first row stay the same from tile to tile
-// (ld <= 2^22 keeps them in 32 bits), so a load is a uniform base and one
-// register. Rows past the last one read the last one (their weight is zero).
-template <typename T, int ROWS, int DP, int THREADS> struct AtStage {
-  static constexpr int kVec = 16 / sizeof(T);
-  static constexpr int kPieces = ROWS * DP / kVec / THREADS;
-  static_assert(ROWS * DP % (kVec * THREADS) == 0, "whole pieces");
-  typedef T Vec __attribute__((ext_vector_type(16 / sizeof(T))));
-  Vec v[kPieces];
-  uint32_t off[kPieces];
-  static __device__ __forceinline__ int row(int u) { return (threadIdx.x + u * THREADS) * kVec / DP; }
-  static __device__ __forceinline__ int col(int u) { return (threadIdx.x + u * THREADS) * kVec % DP; }
-  __device__ __forceinline__ AtStage(int64_t ld) {
-#pragma unroll
-    for (int u = 0; u < kPieces; ++u)
-      off[u] = (uint32_t)((row(u) * (uint32_t)ld + col(u)) * sizeof(T));
-  }
-  // first: the tile's first row; rows: how many there are from it on (>= 1)
-  __device__ __forceinline__ void load(const T* first, int64_t ld, int rows, int D) {
-    const char* base = reinterpret_cast<const char*>(first);
-    if (rows >= ROWS && D == DP) {
-#pragma unroll
-      for (int u = 0; u < kPieces; ++u) v[u] = *reinterpret_cast<const Vec*>(base + off[u]);
-    } else {
-#pragma unroll
-      for (int u = 0; u < kPieces; ++u) {
-        const int r = row(u) < rows ? row(u) : rows - 1, c = col(u);
-        v[u] = Vec{};
-        if (c < D) v[u] = *reinterpret_cast<const Vec*>(first + r * ld + c);
-      }
-    }
-  }
-  template <typename L> __device__ __forceinline__ void put(T* tile) const {
-#pragma unroll
-    for (int u = 0; u < kPieces; ++u)
-      *reinterpret_cast<Vec*>(tile + L::at(row(u), col(u))) = v[u];
-  }
-};
 
 // Keeps the compiler from turning a branch that few tiles take into selects
 // that every tile pays for.
 __device__ __forceinline__ void at_rare() { asm volatile("" ::: "memory"); }
+
+// The bias of a lane's row at NB blocks of 32 columns, four consecutive ones a
+// load (a row begins at any element: the loads are unaligned). Columns past
+// the row's end read as zeros.
+template <typename T, int NB> struct AtBias {
+  typedef T Vec __attribute__((ext_vector_type(4)));
+  Vec v[NB][4];
+  // row: the row's first column; c: the first block's first column; m: columns
+  __device__ __forceinline__ void load(const T* row, int c, int m, int h) {
+    if (c + 32 * NB <= m) {
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          __builtin_memcpy(&v[b][g], row + c + 4 * h + 32 * b + 8 * g, sizeof(Vec));
+    } else {
+      at_rare();
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int at = c + 32 * b + 8 * g + 4 * h + e;
+            v[b][g][e] = at < m ? row[at] : (T)0.0f;
+          }
+    }
+  }
+};
+
+// The LDS address of a __shared__ array.
+__device__ __forceinline__ uint32_t at_lds(const void* array) {
+  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char*)array;
+}
+
+// Loads that write LDS themselves, without passing a register: 64 lanes of
+// BYTES each, from an address a lane, to consecutive places from LDS address
+// `to` (the same for the wave). They have no result to wait for; at_arrive
+// waits. In assembly, because the compiler would wait for the builtin's loads
+// before every transposing LDS read, and with that for the tiles on their way.
+template <int BYTES> __device__ __forceinline__ void at_load_lds(const void* from, uint32_t to) {
+  static_assert(BYTES == 16 || BYTES == 4, "a lane loads one or four words");
+  const uint32_t lds = (uint32_t)__builtin_amdgcn_readfirstlane((int)to);
+  const uint64_t at = reinterpret_cast<uint64_t>(from);
+  if constexpr (BYTES == 16)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+                 ::"s"(lds), "v"(at) : "memory");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off"
+                 ::"s"(lds), "v"(at) : "memory");
+}
+// The same from a uniform base and a lane's distance in bytes.
+__device__ __forceinline__ void at_load_lds16(const char* base, uint32_t lane, uint32_t to) {
+  const uint32_t lds = (uint32_t)__builtin_amdgcn_readfirstlane((int)to);
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+               ::"s"(lds), "v"(lane), "s"(base) : "memory");
+}
+
+// Waits until all but the last OPS vector memory operations of the wave, and its
+// LDS reads, are done, then for the workgroup's other waves.
+template <int OPS> __device__ __forceinline__ void at_arrive() {
+  constexpr int N = OPS < 64 ? OPS : 63;  // the counter has six bits
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((N & 15) | (N >> 4) << 14 | 7 << 4);
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+__device__ const f32x4 kAtZeros = {0.0f, 0.0f, 0.0f, 0.0f};
+
+// A tile of ROWS token rows of D elements (D <= DP) on its way to LDS, THREADS
+// threads taking chunks one after another. A thread's distances from the
+// tile's first row stay the same from tile to tile (ld <= 2^22 keeps them in 32
+// bits). Rows past the last one read the last one (their weight is zero);
+// columns past D read zeros.
+template <typename T, int ROWS, int DP, int THREADS> struct AtLoad {
+  typedef AtTile<T, DP> L;
+  static constexpr int kPieces = ROWS * L::chunks / THREADS;  // loads of a wave
+  static_assert(ROWS * L::chunks % THREADS == 0, "whole pieces");
+  uint32_t off[kPieces];
+  static __device__ __forceinline__ int row(int u) {
+    return (threadIdx.x + u * THREADS) / L::chunks;
+  }
+  static __device__ __forceinline__ int col(int u) {
+    return (((threadIdx.x + u * THREADS) % L::chunks) ^ L::turn(row(u))) * L::vec;
+  }
+  __device__ __forceinline__ explicit AtLoad(int64_t ld) {
+#pragma unroll
+    for (int u = 0; u < kPieces; ++u)
+      off[u] = (uint32_t)((row(u) * (uint32_t)ld + col(u)) * sizeof(T));
+  }
+  // first: the tile's first row; rows: how many there are from it on (>= 1);
+  // tile: its LDS address
+  __device__ __forceinline__ void start(const T* first, int64_t ld, int rows, int D,
+                                        uint32_t tile) const {
+    const char* base = reinterpret_cast<const char*>(first);
+    const uint32_t to = tile + (threadIdx.x & ~63) * 16;
+    if (rows >= ROWS && D == DP) {
+#pragma unroll
+      for (int u = 0; u < kPieces; ++u) at_load_lds16(base, off[u], to + u * THREADS * 16);
+    } else {
+#pragma unroll
+      for (int u = 0; u < kPieces; ++u) {
+        const int r = row(u) < rows ? row(u) : rows - 1, c = col(u);
+        const void* from = c < D ? (const void*)(first + r * ld + c) : (const void*)&kAtZeros;
+        at_load_lds<16>(from, to + u * THREADS * 16);
+      }
+    }
+  }
+};
+
+// A value that the compiler may not compute with ahead of its use: what follows
+// from it stays in the branch that needs it.
+__device__ __forceinline__ int64_t at_opaque(int64_t x) {
+  asm volatile("" : "+s"(x));
+  return x;
+}
+
+// Single elements at a uniform base, a lane's distance and a uniform one (both
+// in bytes, below 2^31): a buffer instruction adds the three itself, where a
+// global one would take a 64-bit addition for each.
+struct AtBuffer {
+  __amdgpu_buffer_rsrc_t r;
+  __device__ __forceinline__ explicit AtBuffer(const void* p) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(p);
+    const uint64_t u = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(x >> 32)) << 32 |
+                       (uint32_t)__builtin_amdgcn_readfirstlane((int)x);
+    r = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(u), 0, 0xffffffff, 0x00027000);
+  }
+  template <typename T> __device__ __forceinline__ T load(uint32_t lane, uint32_t uniform) const {
+    if constexpr (sizeof(T) == 2)
+      return __builtin_bit_cast(T, (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, lane, uniform, 0));
+    else
+      return __builtin_bit_cast(T, (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(r, lane, uniform, 0));
+  }
+  template <typename T>
+  __device__ __forceinline__ void store(T x, uint32_t lane, uint32_t uniform) const {
+    if constexpr (sizeof(T) == 2)
+      __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, x), r, lane, uniform, 0);
+    else
+      __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, x), r, lane, uniform, 0);
+  }
+};
 
 // The larger of a lane's value and its partner's in the other half.
 __device__ __forceinline__ float at_halves_max(float x) {
