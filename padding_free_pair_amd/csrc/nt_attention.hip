@@ -120,7 +120,7 @@ __global__ __launch_bounds__(kAtThreads, sizeof(T) == 4 && DP > 64 ? 1 : 2) void
   float most = -INFINITY, sum = 0.0f;  // of this row; sum: this half's keys
   const float unit = BIAS ? 1.0f : scale * kLog2e;  // a score's unit in powers of two
   const Load load_k(a.ld_k), load_v(a.ld_v);
-  AtBias<T, NB> bias_even, bias_odd;
+  AtBias<T, NB> biases[BUFS];
   const int mine = 32 * kw * NB;  // this wave's first key in a tile
   const int tiles = (int)((c1 - c0 + KEYS - 1) / KEYS);
   kp += c0 * a.ld_k;
@@ -137,10 +137,12 @@ __global__ __launch_bounds__(kAtThreads, sizeof(T) == 4 && DP > 64 ? 1 : 2) void
 #pragma unroll
   for (int j = 0; j < AHEAD; ++j)
     if (j < tiles) start();
-  if (BIAS && tiles > 0) bias_even.load(bp, (int)c0 + mine, keys, h);
-  if (BIAS && tiles > 1) bias_odd.load(bp, (int)c0 + KEYS + mine, keys, h);
-  int buf = 0, c = (int)c0;
-  auto step = [&](int j, AtBias<T, NB>& bias) {
+  if (BIAS && tiles > 0) biases[0].load(bp, (int)c0 + mine, keys, h);
+  if (BIAS && tiles > 1) biases[1].load(bp, (int)c0 + KEYS + mine, keys, h);
+  int c = (int)c0;
+  auto step = [&](int j, auto index) {
+    constexpr int buf = decltype(index)::value;
+    const AtBias<T, NB>& bias = biases[buf];
     if (j + AHEAD < tiles) at_arrive<BEHIND>();
     else if (j + AHEAD - 1 < tiles) at_arrive<TAIL>();
     else at_arrive<0>();
@@ -160,7 +162,7 @@ __global__ __launch_bounds__(kAtThreads, sizeof(T) == 4 && DP > 64 ? 1 : 2) void
       for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int x = 0; x < 16; ++x) s[b][x] = s[b][x] * scale + to_f32((T)bias.v[b][x / 4][x % 4]);
-      if (j + 2 < tiles) bias.load(bp, c + 2 * KEYS + mine, keys, h);
+      if (j + 2 < tiles) biases[(buf + 2) % BUFS].load(bp, c + 2 * KEYS + mine, keys, h);
     }
     if (c + KEYS > (CAUSAL ? seen0 : keys)) {
       at_rare();
@@ -208,16 +210,8 @@ __global__ __launch_bounds__(kAtThreads, sizeof(T) == 4 && DP > 64 ? 1 : 2) void
         o[d] = at_mma(at_across<DP>(lv, mine + 16 * x, 32 * d), p, o[d]);
     }
     c += KEYS;
-    buf = buf + 1 == BUFS ? 0 : buf + 1;
   };
-  if constexpr (BIAS) {
-    for (int j = 0; j < tiles; j += 2) {
-      step(j, bias_even);
-      if (j + 1 < tiles) step(j + 1, bias_odd);
-    }
-  } else {
-    for (int j = 0; j < tiles; ++j) step(j, bias_even);
-  }
+  at_each<BUFS>(tiles, step);
   sum += __shfl_xor(sum, 32);
   if (KW > 1) {  // the waves of the same rows, in order, at their common maximum
     __syncthreads();

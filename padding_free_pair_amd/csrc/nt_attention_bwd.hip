@@ -125,7 +125,7 @@ __global__ __launch_bounds__(64 * QW * KW, sizeof(T) == 4 && DP > 64 ? 1 : 2) vo
   for (int d = 0; d < DT; ++d) gq[d] = f32x16{};
   const float unit = a.scale * kLog2e;
   const Load load_k(a.ld_k), load_v(a.ld_v);
-  AtBias<T, NB> bias_even, bias_odd;
+  AtBias<T, NB> biases[BUFS];
   const int mine = 32 * kw * NB;  // this wave's first key in a tile
   const int tiles = (int)((c1 + KEYS - 1) / KEYS);
   int left = keys, to = 0;  // keys from the tile to load on; its buffer
@@ -140,10 +140,12 @@ __global__ __launch_bounds__(64 * QW * KW, sizeof(T) == 4 && DP > 64 ? 1 : 2) vo
 #pragma unroll
   for (int j = 0; j < AHEAD; ++j)
     if (j < tiles) start();
-  if (BIAS && tiles > 0) bias_even.load(bp, mine, keys, h);
-  if (BIAS && tiles > 1) bias_odd.load(bp, KEYS + mine, keys, h);
-  int buf = 0, c = 0;
-  auto step = [&](int j, AtBias<T, NB>& bias) {
+  if (BIAS && tiles > 0) biases[0].load(bp, mine, keys, h);
+  if (BIAS && tiles > 1) biases[1].load(bp, KEYS + mine, keys, h);
+  int c = 0;
+  auto step = [&](int j, auto index) {
+    constexpr int buf = decltype(index)::value;
+    const AtBias<T, NB>& bias = biases[buf];
     if (j + AHEAD < tiles) at_arrive<BEHIND>();
     else if (j + AHEAD - 1 < tiles) at_arrive<TAIL>();
     else at_arrive<0>();
@@ -168,7 +170,8 @@ __global__ __launch_bounds__(64 * QW * KW, sizeof(T) == 4 && DP > 64 ? 1 : 2) vo
                        : s[b][x] * unit - base;
         s[b][x] = __builtin_amdgcn_exp2f(s[b][x]) * (dp[b][x] - delta);
       }
-    if (BIAS && j + 2 < tiles) bias.load(bp, c + 2 * KEYS + mine, keys, h);
+    if (BIAS && j + 2 < tiles)
+      biases[(buf + 2) % BUFS].load(bp, c + 2 * KEYS + mine, keys, h);
     if (c + KEYS > seen0) {
       at_rare();
       const int end = last - c - mine - 4 * h;
@@ -187,16 +190,8 @@ __global__ __launch_bounds__(64 * QW * KW, sizeof(T) == 4 && DP > 64 ? 1 : 2) vo
         gq[d] = at_mma(at_across<DP>(lk, mine + 16 * x, 32 * d), f, gq[d]);
     }
     c += KEYS;
-    buf = buf + 1 == BUFS ? 0 : buf + 1;
   };
-  if constexpr (BIAS) {
-    for (int j = 0; j < tiles; j += 2) {
-      step(j, bias_even);
-      if (j + 1 < tiles) step(j + 1, bias_odd);
-    }
-  } else {
-    for (int j = 0; j < tiles; ++j) step(j, bias_even);
-  }
+  at_each<BUFS>(tiles, step);
   if (KW > 1) {  // the waves of the same rows, in order
     __syncthreads();
     float* join = reinterpret_cast<float*>(lds_bytes);
@@ -332,7 +327,7 @@ __global__ __launch_bounds__(64 * KW * RW, DP > 64 || (sizeof(T) == 4 && RW == 4
   // register's distance (T_cols < 2^23 with a bias).
   struct Bias {
     T v[NB][16];
-  } bias_even, bias_odd;
+  } biases[BUFS];
   const uint32_t row_bytes = (uint32_t)(m * sizeof(T));
   const uint32_t b_off = 4 * h * row_bytes + (uint32_t)(keyc * sizeof(T));
   int bias_h = hk * G, bias_r = from;  // of the tile whose bias is loaded next
@@ -365,10 +360,12 @@ __global__ __launch_bounds__(64 * KW * RW, DP > 64 || (sizeof(T) == 4 && RW == 4
 #pragma unroll
   for (int j = 0; j < AHEAD; ++j)
     if (j < tiles) start();
-  if (BIAS && tiles > 0) load_bias(bias_even);
-  if (BIAS && tiles > 1) load_bias(bias_odd);
-  int buf = 0, hq = hk * G, r0 = from;
-  auto step = [&](int j, Bias& b) {
+  if (BIAS && tiles > 0) load_bias(biases[0]);
+  if (BIAS && tiles > 1) load_bias(biases[1]);
+  int hq = hk * G, r0 = from;
+  auto step = [&](int j, auto index) {
+    constexpr int buf = decltype(index)::value;
+    const Bias& b = biases[buf];
     if (j + AHEAD - 1 < tiles) at_arrive<BEHIND>();
     else at_arrive<0>();
     if (j + AHEAD < tiles) start();
@@ -416,7 +413,7 @@ __global__ __launch_bounds__(64 * KW * RW, DP > 64 || (sizeof(T) == 4 && RW == 4
           if (w < past || w >= end) s[u][x] = dp[u][x] = 0.0f;
         }
     }
-    if (BIAS && j + 2 < tiles) load_bias(b);
+    if (BIAS && j + 2 < tiles) load_bias(biases[(buf + 2) % BUFS]);
     if (BIAS && a.g_bias && live) {
       T* p = g_bias + (int64_t)hq * a.cells + (int64_t)(r0 + mine) * m;
       if (left >= 32 * NB) {
@@ -448,21 +445,13 @@ __global__ __launch_bounds__(64 * KW * RW, DP > 64 || (sizeof(T) == 4 && RW == 4
         gk[d] = at_mma(at_across<DP>(lq, mine + 16 * x, 32 * d), fs, gk[d]);
       }
     }
-    buf = buf + 1 == BUFS ? 0 : buf + 1;
     r0 += ROWS;
     if (r0 >= rows) {
       r0 = from;
       ++hq;
     }
   };
-  if constexpr (BIAS) {
-    for (int j = 0; j < tiles; j += 2) {
-      step(j, bias_even);
-      if (j + 1 < tiles) step(j + 1, bias_odd);
-    }
-  } else {
-    for (int j = 0; j < tiles; ++j) step(j, bias_even);
-  }
+  at_each<BUFS>(tiles, step);
   if (RW > 1) {  // the waves of the same keys, in order
     __syncthreads();
     float* join = reinterpret_cast<float*>(lds_bytes);

@@ -198,6 +198,22 @@ template <int OPS> __device__ __forceinline__ void at_arrive() {
   asm volatile("" ::: "memory");
 }
 
+// The buffer of a tile as a constant, so that its LDS addresses are a register
+// of the loop's and an immediate.
+template <int I> struct AtIndex {
+  static constexpr int value = I;
+};
+// step(j, AtIndex<j % BUFS>) for j = 0 .. n - 1.
+template <int BUFS, typename Step> __device__ __forceinline__ void at_each(int n, const Step& step) {
+  static_assert(BUFS == 2 || BUFS == 3, "one or two tiles ahead");
+  for (int j = 0; j < n; j += BUFS) {
+    step(j, AtIndex<0>());
+    if (j + 1 < n) step(j + 1, AtIndex<1>());
+    if constexpr (BUFS == 3)
+      if (j + 2 < n) step(j + 2, AtIndex<2>());
+  }
+}
+
 __device__ const f32x4 kAtZeros = {0.0f, 0.0f, 0.0f, 0.0f};
 
 // A tile of ROWS token rows of D elements (D <= DP) on its way to LDS, THREADS
