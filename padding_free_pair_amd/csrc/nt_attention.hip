@@ -118,7 +118,8 @@ __global__ __launch_bounds__(kAtThreads, sizeof(T) == 4 && DP > 64 ? 1 : 2) void
 #pragma unroll
   for (int d = 0; d < DT; ++d) o[d] = f32x16{};
   float most = -INFINITY, sum = 0.0f;  // of this row; sum: this half's keys
-  const float unit = BIAS ? 1.0f : scale * kLog2e;  // a score's unit in powers of two
+  const float unit = BIAS ? 1.0f : scale * kLog2e;
+  const float step = BIAS ? kLog2e : unit;  // a score's unit in powers of two
   const Load load_k(a.ld_k), load_v(a.ld_v);
   AtBias<T, NB> biases[BUFS];
   const int mine = 32 * kw * NB;  // this wave's first key in a tile
@@ -140,7 +141,7 @@ __global__ __launch_bounds__(kAtThreads, sizeof(T) == 4 && DP > 64 ? 1 : 2) void
   if (BIAS && tiles > 0) biases[0].load(bp, (int)c0 + mine, keys, h);
   if (BIAS && tiles > 1) biases[1].load(bp, (int)c0 + KEYS + mine, keys, h);
   int c = (int)c0;
-  auto step = [&](int j, auto index) {
+  auto tile_step = [&](int j, auto index) {
     constexpr int buf = decltype(index)::value;
     const AtBias<T, NB>& bias = biases[buf];
     if (j + AHEAD < tiles) at_arrive<BEHIND>();
@@ -179,11 +180,15 @@ __global__ __launch_bounds__(kAtThreads, sizeof(T) == 4 && DP > 64 ? 1 : 2) void
 #pragma unroll
       for (int x = 0; x < 16; ++x) top = fmaxf(top, s[b][x]);
     top = at_halves_max(top);
-    if (__any(top > most)) {
+    // The base of a row's powers moves when its maximum has outgrown it by 2^8,
+    // not at every new maximum: until then the powers stay below 2^8, which costs
+    // neither bf16 nor fp32 any precision, and the sums carry the same base. (Of 32
+    // rows one has a new maximum in most of the first 30 tiles, and moving scales
+    // all of o: 16 D / 32 products a lane.)
+    if (__any((top - most) * step > 8.0f)) {
       at_rare();
       const float now = fmaxf(most, top);
-      const float keep = now == -INFINITY ? 1.0f
-                                          : __builtin_amdgcn_exp2f((most - now) * (BIAS ? kLog2e : unit));
+      const float keep = now == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f((most - now) * step);
       most = now;
       sum *= keep;
 #pragma unroll
@@ -211,7 +216,7 @@ __global__ __launch_bounds__(kAtThreads, sizeof(T) == 4 && DP > 64 ? 1 : 2) void
     }
     c += KEYS;
   };
-  at_each<BUFS>(tiles, step);
+  at_each<BUFS>(tiles, tile_step);
   sum += __shfl_xor(sum, 32);
   if (KW > 1) {  // the waves of the same rows, in order, at their common maximum
     __syncthreads();
@@ -228,7 +233,6 @@ __global__ __launch_bounds__(kAtThreads, sizeof(T) == 4 && DP > 64 ? 1 : 2) void
     }
     __syncthreads();
     if (kw > 0) return;
-    const float step = BIAS ? kLog2e : unit;
     float now = most;
 #pragma unroll
     for (int w = 1; w < KW; ++w) now = fmaxf(now, join[((w - 1) * QW + qw) * kPart + lane]);
