@@ -37,7 +37,7 @@ struct AtArgs {
 };
 
 template <typename T, int DP, int QW, int KW, int NB, bool BIAS, bool CAUSAL>
-__global__ __launch_bounds__(kAtThreads, sizeof(T) == 4 && DP > 64 ? 1 : 2) void k_attention(
+__global__ __launch_bounds__(kAtThreads, sizeof(T) == 4 && (DP > 64 || BIAS) ? 1 : 2) void k_attention(
     AtArgs a) {
   static_assert(64 * QW * KW == kAtThreads, "four waves");
   constexpr int KS = DP / 16, DT = DP / 32;
@@ -47,15 +47,13 @@ __global__ __launch_bounds__(kAtThreads, sizeof(T) == 4 && DP > 64 ? 1 : 2) void
   constexpr int TILE = KEYS * AtTile<T, DP>::pitch, kPair = 2 * TILE * (int)sizeof(T);
   // Tiles in flight: two where three pairs of tiles leave room for a second
   // workgroup on the CU (160 KB), else one.
-  constexpr int AHEAD = 3 * kPair <= 80 * 1024 ? 2 : 1, BUFS = AHEAD + 1;
+  constexpr int AHEAD = !BIAS && 3 * kPair <= 80 * 1024 ? 2 : 1, BUFS = AHEAD + 1;
   constexpr int kLds = BUFS * kPair, kJoin = (KW - 1) * QW * (DP / 2 + 2) * 64 * 4;
-  // Operations behind a tile's own loads when it is needed: the next tile's
-  // loads, and the bias of whole tiles, which is loaded two tiles ahead of its
-  // use (a tile that ends within its block may take fewer loads than four a
-  // block, and is not counted).
-  constexpr int TAIL = (AHEAD - 1) * (2 * Load::kPieces + (BIAS ? 4 * NB : 0));
-  constexpr int BEHIND = (AHEAD - 1) * (2 * Load::kPieces + (BIAS ? 8 * NB : 0));
+  // Operations behind a tile's own loads when it is needed: the next tile's.
+  constexpr int BEHIND = (AHEAD - 1) * 2 * Load::kPieces;
+  typedef AtBiasTile<T, ROWS, KEYS, kAtThreads> Bias;
   __shared__ __align__(16) char lds_bytes[kLds > kJoin ? kLds : kJoin];
+  __shared__ __align__(16) T lds_bias[BIAS ? BUFS * ROWS * KEYS : 1];
   const T* lds = reinterpret_cast<const T*>(lds_bytes);
   const uint32_t lds_at = at_lds(lds_bytes);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l32 = lane & 31, h = lane >> 5;
@@ -112,7 +110,6 @@ __global__ __launch_bounds__(kAtThreads, sizeof(T) == 4 && DP > 64 ? 1 : 2) void
   }
   const T* kp = static_cast<const T*>(a.k) + a.mu[i] * a.ld_k + (int64_t)hk * a.D;
   const T* vp = static_cast<const T*>(a.v) + a.mu[i] * a.ld_v + (int64_t)hk * a.D;
-  const T* bp = BIAS ? static_cast<const T*>(a.bias) + hq * a.cells + a.cell0[i] + r * m : nullptr;
 
   f32x16 o[DT];
 #pragma unroll
@@ -121,7 +118,25 @@ __global__ __launch_bounds__(kAtThreads, sizeof(T) == 4 && DP > 64 ? 1 : 2) void
   const float unit = BIAS ? 1.0f : scale * kLog2e;
   const float step = BIAS ? kLog2e : unit;  // a score's unit in powers of two
   const Load load_k(a.ld_k), load_v(a.ld_v);
-  AtBias<T, NB> biases[BUFS];
+  // The bias: tile j's cells are loaded BUFS tiles ahead and put into LDS one
+  // ahead, so that a wait for them leaves the loads of the tiles between.
+  Bias biases[BUFS];
+  const T* cells[Bias::kPieces];
+  int cells_left = keys - (int)c0;
+  if (BIAS) {
+#pragma unroll
+    for (int u = 0; u < Bias::kPieces; ++u) {
+      const int64_t x = tile * ROWS + Bias::row(u) < n * G ? tile * ROWS + Bias::row(u) : n * G - 1;
+      cells[u] = static_cast<const T*>(a.bias) + (hk * G + x % G) * a.cells + a.cell0[i] +
+                 x / G * m + c0 + Bias::col(u);
+    }
+  }
+  auto load_bias = [&](Bias& to_load) {
+    to_load.load(cells, cells_left);
+#pragma unroll
+    for (int u = 0; u < Bias::kPieces; ++u) cells[u] += KEYS;
+    cells_left -= KEYS;
+  };
   const int mine = 32 * kw * NB;  // this wave's first key in a tile
   const int tiles = (int)((c1 - c0 + KEYS - 1) / KEYS);
   kp += c0 * a.ld_k;
@@ -138,16 +153,22 @@ __global__ __launch_bounds__(kAtThreads, sizeof(T) == 4 && DP > 64 ? 1 : 2) void
 #pragma unroll
   for (int j = 0; j < AHEAD; ++j)
     if (j < tiles) start();
-  if (BIAS && tiles > 0) biases[0].load(bp, (int)c0 + mine, keys, h);
-  if (BIAS && tiles > 1) biases[1].load(bp, (int)c0 + KEYS + mine, keys, h);
+  if (BIAS) {
+#pragma unroll
+    for (int j = 0; j < BUFS; ++j)
+      if (j < tiles) load_bias(biases[j]);
+    if (tiles > 0) biases[0].put(lds_bias);
+  }
   int c = (int)c0;
   auto tile_step = [&](int j, auto index) {
     constexpr int buf = decltype(index)::value;
-    const AtBias<T, NB>& bias = biases[buf];
-    if (j + AHEAD < tiles) at_arrive<BEHIND>();
-    else if (j + AHEAD - 1 < tiles) at_arrive<TAIL>();
+    if (j + AHEAD - 1 < tiles) at_arrive<BEHIND>();
     else at_arrive<0>();
     if (j + AHEAD < tiles) start();
+    if (BIAS) {
+      if (j + 1 < tiles) biases[(buf + 1) % BUFS].put(lds_bias + (buf + 1) % BUFS * ROWS * KEYS);
+      if (j + BUFS < tiles) load_bias(biases[buf]);
+    }
     const T* lk = lds + buf * 2 * TILE;
     const T* lv = lk + TILE;
     f32x16 s[NB];
@@ -162,8 +183,13 @@ __global__ __launch_bounds__(kAtThreads, sizeof(T) == 4 && DP > 64 ? 1 : 2) void
 #pragma unroll
       for (int b = 0; b < NB; ++b)
 #pragma unroll
-        for (int x = 0; x < 16; ++x) s[b][x] = s[b][x] * scale + to_f32((T)bias.v[b][x / 4][x % 4]);
-      if (j + 2 < tiles) biases[(buf + 2) % BUFS].load(bp, c + 2 * KEYS + mine, keys, h);
+        for (int y = 0; y < 4; ++y) {
+          const auto z = at_cells<KEYS>(lds_bias + buf * ROWS * KEYS, 32 * qw + l32,
+                                        mine + 32 * b + 8 * y + 4 * h);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            s[b][4 * y + e] = s[b][4 * y + e] * scale + to_f32((T)z[e]);
+        }
     }
     if (c + KEYS > (CAUSAL ? seen0 : keys)) {
       at_rare();
@@ -352,22 +378,18 @@ AtPlan plan_of(const nt_partition& p, const nt_attention& a) {
   return {qw, (int)(s < 1 ? 1 : s > 64 ? 64 : s)};
 }
 
-template <typename T, int DP, int QW, int KW, int NB>
+template <typename T, int DP, int QW, int KW, int NB, bool BIAS>
 hipError_t run(const AtArgs& x, bool causal, hipStream_t stream) {
   const unsigned g = (unsigned)(x.slots * x.splits * x.K);
-  if (x.bias) {
-    if (causal) k_attention<T, DP, QW, KW, NB, true, true><<<g, kAtThreads, 0, stream>>>(x);
-    else k_attention<T, DP, QW, KW, NB, true, false><<<g, kAtThreads, 0, stream>>>(x);
-  } else {
-    if (causal) k_attention<T, DP, QW, KW, NB, false, true><<<g, kAtThreads, 0, stream>>>(x);
-    else k_attention<T, DP, QW, KW, NB, false, false><<<g, kAtThreads, 0, stream>>>(x);
-  }
+  if (causal) k_attention<T, DP, QW, KW, NB, BIAS, true><<<g, kAtThreads, 0, stream>>>(x);
+  else k_attention<T, DP, QW, KW, NB, BIAS, false><<<g, kAtThreads, 0, stream>>>(x);
   return hipGetLastError();
 }
 template <typename T, int DP>
 hipError_t run(const AtArgs& x, int qw, bool causal, hipStream_t stream) {
-  if (qw == 4) return run<T, DP, 4, 1, 2>(x, causal, stream);
-  return run<T, DP, 2, 2, 1>(x, causal, stream);
+  if (x.bias) return run<T, DP, 2, 2, 1, true>(x, causal, stream);
+  if (qw == 4) return run<T, DP, 4, 1, 2, false>(x, causal, stream);
+  return run<T, DP, 2, 2, 1, false>(x, causal, stream);
 }
 
 template <typename T>

@@ -51,7 +51,7 @@ __device__ __forceinline__ float ab_dot(const f32x8& a, const f32x8& b) {
 // g_q of 32 virtual rows a wave, and their statistics. As in the forward, QW
 // waves own different rows, and KW waves the same rows and different keys.
 template <typename T, int DP, int QW, int KW, int NB, bool BIAS>
-__global__ __launch_bounds__(64 * QW * KW, sizeof(T) == 4 && DP > 64 ? 1 : 2) void k_attention_bwd_q(
+__global__ __launch_bounds__(64 * QW * KW, sizeof(T) == 4 && (DP > 64 || BIAS) ? 1 : 2) void k_attention_bwd_q(
     AbArgs a) {
   constexpr int KS = DP / 16, DT = DP / 32, THREADS = 64 * QW * KW;
   constexpr int ROWS = 32 * QW, KEYS = 32 * KW * NB;
@@ -59,11 +59,11 @@ __global__ __launch_bounds__(64 * QW * KW, sizeof(T) == 4 && DP > 64 ? 1 : 2) vo
   typedef AtLoad<T, KEYS, DP, THREADS> Load;
   constexpr int TILE = KEYS * AtTile<T, DP>::pitch, kPair = 2 * TILE * (int)sizeof(T);
   constexpr int AHEAD = ab_ahead(kPair), BUFS = AHEAD + 1;
-  // as in the forward
-  constexpr int TAIL = (AHEAD - 1) * (2 * Load::kPieces + (BIAS ? 4 * NB : 0));
-  constexpr int BEHIND = (AHEAD - 1) * (2 * Load::kPieces + (BIAS ? 8 * NB : 0));
+  constexpr int BEHIND = (AHEAD - 1) * 2 * Load::kPieces;
+  typedef AtBiasTile<T, ROWS, KEYS, THREADS> Bias;
   constexpr int kLds = BUFS * kPair, kJoin = (KW - 1) * QW * DP / 2 * 64 * 4;
   __shared__ __align__(16) char lds_bytes[kLds > kJoin ? kLds : kJoin];
+  __shared__ __align__(16) T lds_bias[BIAS ? BUFS * ROWS * KEYS : 1];
   const T* lds = reinterpret_cast<const T*>(lds_bytes);
   const uint32_t lds_at = at_lds(lds_bytes);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l32 = lane & 31, h = lane >> 5;
@@ -118,14 +118,29 @@ __global__ __launch_bounds__(64 * QW * KW, sizeof(T) == 4 && DP > 64 ? 1 : 2) vo
   }
   const T* kp = static_cast<const T*>(a.k) + a.mu[i] * a.ld_k + (int64_t)hk * a.D;
   const T* vp = static_cast<const T*>(a.v) + a.mu[i] * a.ld_v + (int64_t)hk * a.D;
-  const T* bp = static_cast<const T*>(a.bias) + hq * a.cells + a.cell0[i] + r * m;
-
   f32x16 gq[DT];
 #pragma unroll
   for (int d = 0; d < DT; ++d) gq[d] = f32x16{};
   const float unit = a.scale * kLog2e;
   const Load load_k(a.ld_k), load_v(a.ld_v);
-  AtBias<T, NB> biases[BUFS];
+  // the bias as in the forward: loaded BUFS tiles ahead, put into LDS one ahead
+  Bias biases[BUFS];
+  const T* cells[Bias::kPieces];
+  int cells_left = keys;
+  if (BIAS) {
+#pragma unroll
+    for (int u = 0; u < Bias::kPieces; ++u) {
+      const int64_t x = tile * ROWS + Bias::row(u) < n * G ? tile * ROWS + Bias::row(u) : n * G - 1;
+      cells[u] = static_cast<const T*>(a.bias) + (hk * G + x % G) * a.cells + a.cell0[i] +
+                 x / G * m + Bias::col(u);
+    }
+  }
+  auto load_bias = [&](Bias& to_load) {
+    to_load.load(cells, cells_left);
+#pragma unroll
+    for (int u = 0; u < Bias::kPieces; ++u) cells[u] += KEYS;
+    cells_left -= KEYS;
+  };
   const int mine = 32 * kw * NB;  // this wave's first key in a tile
   const int tiles = (int)((c1 + KEYS - 1) / KEYS);
   int left = keys, to = 0;  // keys from the tile to load on; its buffer
@@ -140,16 +155,22 @@ __global__ __launch_bounds__(64 * QW * KW, sizeof(T) == 4 && DP > 64 ? 1 : 2) vo
 #pragma unroll
   for (int j = 0; j < AHEAD; ++j)
     if (j < tiles) start();
-  if (BIAS && tiles > 0) biases[0].load(bp, mine, keys, h);
-  if (BIAS && tiles > 1) biases[1].load(bp, KEYS + mine, keys, h);
+  if (BIAS) {
+#pragma unroll
+    for (int j = 0; j < BUFS; ++j)
+      if (j < tiles) load_bias(biases[j]);
+    if (tiles > 0) biases[0].put(lds_bias);
+  }
   int c = 0;
   auto step = [&](int j, auto index) {
     constexpr int buf = decltype(index)::value;
-    const AtBias<T, NB>& bias = biases[buf];
-    if (j + AHEAD < tiles) at_arrive<BEHIND>();
-    else if (j + AHEAD - 1 < tiles) at_arrive<TAIL>();
+    if (j + AHEAD - 1 < tiles) at_arrive<BEHIND>();
     else at_arrive<0>();
     if (j + AHEAD < tiles) start();
+    if (BIAS) {
+      if (j + 1 < tiles) biases[(buf + 1) % BUFS].put(lds_bias + (buf + 1) % BUFS * ROWS * KEYS);
+      if (j + BUFS < tiles) load_bias(biases[buf]);
+    }
     const T* lk = lds + buf * 2 * TILE;
     const T* lv = lk + TILE;
     f32x16 s[NB], dp[NB];
@@ -165,13 +186,21 @@ __global__ __launch_bounds__(64 * QW * KW, sizeof(T) == 4 && DP > 64 ? 1 : 2) vo
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
-      for (int x = 0; x < 16; ++x) {
-        s[b][x] = BIAS ? (s[b][x] * a.scale + to_f32((T)bias.v[b][x / 4][x % 4]) - lse) * kLog2e
-                       : s[b][x] * unit - base;
-        s[b][x] = __builtin_amdgcn_exp2f(s[b][x]) * (dp[b][x] - delta);
+      for (int y = 0; y < 4; ++y) {
+        at_f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (BIAS) {
+          const auto cell = at_cells<KEYS>(lds_bias + buf * ROWS * KEYS, 32 * qw + l32,
+                                           mine + 32 * b + 8 * y + 4 * h);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) z[e] = to_f32((T)cell[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int x = 4 * y + e;
+          s[b][x] = BIAS ? (s[b][x] * a.scale + z[e] - lse) * kLog2e : s[b][x] * unit - base;
+          s[b][x] = __builtin_amdgcn_exp2f(s[b][x]) * (dp[b][x] - delta);
+        }
       }
-    if (BIAS && j + 2 < tiles)
-      biases[(buf + 2) % BUFS].load(bp, c + 2 * KEYS + mine, keys, h);
     if (c + KEYS > seen0) {
       at_rare();
       const int end = last - c - mine - 4 * h;
@@ -231,19 +260,20 @@ __global__ __launch_bounds__(64 * QW * KW, sizeof(T) == 4 && DP > 64 ? 1 : 2) vo
 // blocks of 32 rows of each tile, and their sums are joined at the end in
 // order, so few keys still fill the card.
 template <typename T, int DP, int KW, int RW, int NB, bool BIAS>
-__global__ __launch_bounds__(64 * KW * RW, DP > 64 || (sizeof(T) == 4 && RW == 4) ? 1 : 2) void k_attention_bwd_k(AbArgs a) {
+__global__ __launch_bounds__(64 * KW * RW, DP > 64 || (BIAS && (sizeof(T) == 4 || (RW == 4 && DP > 32))) ? 1 : 2) void k_attention_bwd_k(AbArgs a) {
   constexpr int KS = DP / 16, DT = DP / 32, THREADS = 64 * KW * RW, KEYS = 32 * KW;
   constexpr int ROWS = 32 * RW * NB;  // of a tile: NB blocks of a wave
   typedef typename AtFrag<T>::type Frag;
   typedef AtLoad<T, ROWS, DP, THREADS> Load;
   constexpr int TILE = ROWS * AtTile<T, DP>::pitch, kPair = 2 * TILE * (int)sizeof(T);
   constexpr int AHEAD = ab_ahead(kPair), BUFS = AHEAD + 1;
-  // behind a tile's loads: the next tile's, its bias and the next one's
-  constexpr int BEHIND = (AHEAD - 1) * (2 * Load::kPieces + NB + (BIAS ? 32 * NB : 0));
+  constexpr int BEHIND = (AHEAD - 1) * (2 * Load::kPieces + NB);  // the next tile's loads
+  typedef AtBiasTile<T, ROWS, KEYS, THREADS> Bias;
   constexpr int kLds = BUFS * kPair, kJoin = (RW - 1) * KW * 2 * DP * 32 * 4;
   __shared__ __align__(16) char lds_bytes[kLds > kJoin ? kLds : kJoin];
   // each wave's own rows: log sums, then deltas
   __shared__ __align__(16) float stats[BUFS][KW * RW][2][32 * NB];
+  __shared__ __align__(16) T lds_bias[BIAS ? BUFS * ROWS * KEYS : 1];
   const T* lds = reinterpret_cast<const T*>(lds_bytes);
   const uint32_t lds_at = at_lds(lds_bytes);
   const uint32_t stats_at = at_lds(stats);
@@ -285,7 +315,6 @@ __global__ __launch_bounds__(64 * KW * RW, DP > 64 || (sizeof(T) == 4 && RW == 4
     first = tile * KEYS - ahead;
     first = first < 0 ? 0 : first < n ? first : n;
   }
-  const T* bias = static_cast<const T*>(a.bias) + a.cell0[i];
   T* g_bias = static_cast<T*>(a.g_bias) + a.cell0[i];
   if (BIAS && a.g_bias && live)
     for (int g = 0; g < G; ++g)
@@ -322,53 +351,49 @@ __global__ __launch_bounds__(64 * KW * RW, DP > 64 || (sizeof(T) == 4 && RW == 4
       ++load_h;
     }
   };
-  // Bias of this lane's key at its rows of a tile: rows are m elements apart
-  // from a uniform base, the lane's key and its half's four rows are one
-  // register's distance (T_cols < 2^23 with a bias).
-  struct Bias {
-    T v[NB][16];
-  } biases[BUFS];
+  // The bias as in the forward, for the tiles of rows in turn. Its gradient's
+  // rows are m elements apart from a uniform base, the lane's key and its half's
+  // four rows are one register's distance (T_cols < 2^23 with a bias).
   const uint32_t row_bytes = (uint32_t)(m * sizeof(T));
   const uint32_t b_off = 4 * h * row_bytes + (uint32_t)(keyc * sizeof(T));
+  Bias biases[BUFS];
   int bias_h = hk * G, bias_r = from;  // of the tile whose bias is loaded next
-  auto load_bias = [&](Bias& b) {
-    const T* p = bias + (int64_t)bias_h * a.cells + (int64_t)bias_r * m;
-    const int left = rows - bias_r;
+  const int cells_left = (int)(m - tile * KEYS);
+  auto load_bias = [&](Bias& to_load) {
+    const T* p = static_cast<const T*>(a.bias) + (int64_t)bias_h * a.cells + a.cell0[i] +
+                 bias_r * m + tile * KEYS;
+    const T* cells[Bias::kPieces];
+#pragma unroll
+    for (int u = 0; u < Bias::kPieces; ++u) {
+      const int r = Bias::row(u) < rows - bias_r ? Bias::row(u) : rows - bias_r - 1;
+      cells[u] = p + r * m + Bias::col(u);
+    }
+    to_load.load(cells, cells_left);
     bias_r += ROWS;
     if (bias_r >= rows) {
       bias_r = from;
       ++bias_h;
     }
-    if (left >= ROWS) {
-      const AtBuffer buffer(p);
-#pragma unroll
-      for (int u = 0; u < NB; ++u)
-#pragma unroll
-        for (int x = 0; x < 16; ++x)
-          b.v[u][x] = buffer.load<T>(b_off, (32 * (rw * NB + u) + 8 * (x / 4) + x % 4) * row_bytes);
-    } else {
-      const int64_t step = at_opaque(m);
-#pragma unroll
-      for (int u = 0; u < NB; ++u)
-#pragma unroll
-        for (int x = 0; x < 16; ++x) {
-          const int r = 32 * (rw * NB + u) + 8 * (x / 4) + 4 * h + x % 4;
-          b.v[u][x] = p[(r < left ? r : left - 1) * step + keyc];
-        }
-    }
   };
 #pragma unroll
   for (int j = 0; j < AHEAD; ++j)
     if (j < tiles) start();
-  if (BIAS && tiles > 0) load_bias(biases[0]);
-  if (BIAS && tiles > 1) load_bias(biases[1]);
+  if (BIAS) {
+#pragma unroll
+    for (int j = 0; j < BUFS; ++j)
+      if (j < tiles) load_bias(biases[j]);
+    if (tiles > 0) biases[0].put(lds_bias);
+  }
   int hq = hk * G, r0 = from;
   auto step = [&](int j, auto index) {
     constexpr int buf = decltype(index)::value;
-    const Bias& b = biases[buf];
     if (j + AHEAD - 1 < tiles) at_arrive<BEHIND>();
     else at_arrive<0>();
     if (j + AHEAD < tiles) start();
+    if (BIAS) {
+      if (j + 1 < tiles) biases[(buf + 1) % BUFS].put(lds_bias + (buf + 1) % BUFS * ROWS * KEYS);
+      if (j + BUFS < tiles) load_bias(biases[buf]);
+    }
     const T* lq = lds + buf * 2 * TILE;
     const T* lg = lq + TILE;
     const int mine = 32 * rw * NB;  // this wave's first row in the tile
@@ -383,7 +408,12 @@ __global__ __launch_bounds__(64 * KW * RW, DP > 64 || (sizeof(T) == 4 && RW == 4
       }
     }
 #pragma unroll
-    for (int u = 0; u < NB; ++u)
+    for (int u = 0; u < NB; ++u) {
+      Frag cell[2] = {};
+      if (BIAS)
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          cell[x] = at_across<KEYS>(lds_bias + buf * ROWS * KEYS, mine + 32 * u + 16 * x, 32 * kw);
 #pragma unroll
       for (int y = 0; y < 4; ++y) {
         const int w = 32 * u + 8 * y + 4 * h;
@@ -393,12 +423,13 @@ __global__ __launch_bounds__(64 * KW * RW, DP > 64 || (sizeof(T) == 4 && RW == 4
         for (int e = 0; e < 4; ++e) {
           const int x = 4 * y + e;
           const float p = __builtin_amdgcn_exp2f(
-              BIAS ? (s[u][x] * a.scale + to_f32(b.v[u][x]) - z[e]) * kLog2e
+              BIAS ? (s[u][x] * a.scale + to_f32((T)cell[x / 8][x % 8]) - z[e]) * kLog2e
                    : s[u][x] * unit - z[e]);
           s[u][x] = p;
           dp[u][x] = p * (dp[u][x] - d[e]);
         }
       }
+    }
     // rows of this tile from this wave's first on, and the first that sees its keys
     const int left = rows - r0 - mine;
     if (left < 32 * NB || (a.causal && k0 + 31 > r0 + mine + ahead)) {
@@ -413,7 +444,6 @@ __global__ __launch_bounds__(64 * KW * RW, DP > 64 || (sizeof(T) == 4 && RW == 4
           if (w < past || w >= end) s[u][x] = dp[u][x] = 0.0f;
         }
     }
-    if (BIAS && j + 2 < tiles) load_bias(biases[(buf + 2) % BUFS]);
     if (BIAS && a.g_bias && live) {
       T* p = g_bias + (int64_t)hq * a.cells + (int64_t)(r0 + mine) * m;
       if (left >= 32 * NB) {
@@ -533,9 +563,11 @@ hipError_t run(const nt_partition& p, AbArgs x, hipStream_t stream) {
   if (!p.T_cols) return hipSuccess;
   if constexpr (can_share)
     if (at_slots(p.T_cols, p.B, 1, 128) * x.K >= 2048) return run_k<T, DP, 4, 1, 2, BIAS>(p, x, stream);
-  if constexpr (sizeof(T) == 2 || DP <= 64)  // its tiles of 128 rows would not fit LDS
+  if constexpr (sizeof(T) == 2)  // its tiles of 128 rows fit LDS
     if (at_slots(p.T_cols, p.B, 1, 64) * x.K < 384) return run_k<T, DP, 1, 4, 1, BIAS>(p, x, stream);
-  return run_k<T, DP, 2, 2, 1, BIAS>(p, x, stream);
+  // (wide fp32 tiles leave LDS for a bias tile of 32 keys)
+  if constexpr (sizeof(T) == 4 && DP > 64 && BIAS) return run_k<T, DP, 1, 2, 1, BIAS>(p, x, stream);
+  else return run_k<T, DP, 2, 2, 1, BIAS>(p, x, stream);
 }
 
 template <typename T, int DP>

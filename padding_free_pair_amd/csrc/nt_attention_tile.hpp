@@ -131,34 +131,12 @@ __device__ __forceinline__ void at_store4(float* p, float a, float b, float c, f
 // that every tile pays for.
 __device__ __forceinline__ void at_rare() { asm volatile("" ::: "memory"); }
 
-// The bias of a lane's row at NB blocks of 32 columns, four consecutive ones a
-// load (a row begins at any element: the loads are unaligned). Columns past
-// the row's end read as zeros.
-template <typename T, int NB> struct AtBias {
-  typedef T Vec __attribute__((ext_vector_type(4)));
-  Vec v[NB][4];
-  // row: the row's first column; c: the first block's first column; m: columns
-  __device__ __forceinline__ void load(const T* row, int c, int m, int h) {
-    if (c + 32 * NB <= m) {
-#pragma unroll
-      for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int g = 0; g < 4; ++g)
-          __builtin_memcpy(&v[b][g], row + c + 4 * h + 32 * b + 8 * g, sizeof(Vec));
-    } else {
-      at_rare();
-#pragma unroll
-      for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int g = 0; g < 4; ++g)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int at = c + 32 * b + 8 * g + 4 * h + e;
-            v[b][g][e] = at < m ? row[at] : (T)0.0f;
-          }
-    }
-  }
-};
+// An address that is the same for the wave, in scalar registers.
+__device__ __forceinline__ uint64_t at_uniform(const void* p) {
+  const uint64_t x = reinterpret_cast<uint64_t>(p);
+  return (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(x >> 32)) << 32 |
+         (uint32_t)__builtin_amdgcn_readfirstlane((int)x);
+}
 
 // The LDS address of a __shared__ array.
 __device__ __forceinline__ uint32_t at_lds(const void* array) {
@@ -184,8 +162,9 @@ template <int BYTES> __device__ __forceinline__ void at_load_lds(const void* fro
 // The same from a uniform base and a lane's distance in bytes.
 __device__ __forceinline__ void at_load_lds16(const char* base, uint32_t lane, uint32_t to) {
   const uint32_t lds = (uint32_t)__builtin_amdgcn_readfirstlane((int)to);
+  const uint64_t at = at_uniform(base);
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
-               ::"s"(lds), "v"(lane), "s"(base) : "memory");
+               ::"s"(lds), "v"(lane), "s"(at) : "memory");
 }
 
 // Waits until all but the last OPS vector memory operations of the wave, and its
@@ -257,29 +236,22 @@ template <typename T, int ROWS, int DP, int THREADS> struct AtLoad {
   }
 };
 
-// A value that the compiler may not compute with ahead of its use: what follows
-// from it stays in the branch that needs it.
+// A count (the same for the wave) that the compiler may not compute with ahead
+// of its use: what follows from it stays in the branch that needs it.
 __device__ __forceinline__ int64_t at_opaque(int64_t x) {
-  asm volatile("" : "+s"(x));
-  return x;
+  int y = __builtin_amdgcn_readfirstlane((int)x);
+  asm volatile("" : "+s"(y));
+  return y;
 }
 
-// Single elements at a uniform base, a lane's distance and a uniform one (both
-// in bytes, below 2^31): a buffer instruction adds the three itself, where a
-// global one would take a 64-bit addition for each.
+// Stores of single elements at a uniform base, a lane's distance and a uniform
+// one (both in bytes, below 2^31): a buffer instruction adds the three itself,
+// where a global one would take a 64-bit addition for each.
 struct AtBuffer {
   __amdgpu_buffer_rsrc_t r;
   __device__ __forceinline__ explicit AtBuffer(const void* p) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(p);
-    const uint64_t u = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(x >> 32)) << 32 |
-                       (uint32_t)__builtin_amdgcn_readfirstlane((int)x);
-    r = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(u), 0, 0xffffffff, 0x00027000);
-  }
-  template <typename T> __device__ __forceinline__ T load(uint32_t lane, uint32_t uniform) const {
-    if constexpr (sizeof(T) == 2)
-      return __builtin_bit_cast(T, (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, lane, uniform, 0));
-    else
-      return __builtin_bit_cast(T, (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(r, lane, uniform, 0));
+    r = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(at_uniform(p)), 0, 0xffffffff,
+                                          0x00027000);
   }
   template <typename T>
   __device__ __forceinline__ void store(T x, uint32_t lane, uint32_t uniform) const {
@@ -295,6 +267,54 @@ __device__ __forceinline__ float at_halves_max(float x) {
   const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, x),
                                                   __builtin_bit_cast(uint32_t, x), false, false);
   return fmaxf(__builtin_bit_cast(float, (uint32_t)r[0]), __builtin_bit_cast(float, (uint32_t)r[1]));
+}
+
+// A tile of the bias, ROWS rows of COLS cells, on its way to LDS through
+// registers (a row begins at any element, which loads to LDS do not allow): 16
+// bytes a thread and piece, consecutive threads along a row, so a row of the
+// tile is read as whole lines, where lanes that read their own scores' cells
+// touch 32 rows each time. In LDS it is an AtTile, read along or across rows.
+// Rows past the last one read the last one; cells past a row's end are left as
+// they are (their scores are masked).
+template <typename T, int ROWS, int COLS, int THREADS> struct AtBiasTile {
+  typedef AtTile<T, COLS> L;
+  typedef T Vec __attribute__((ext_vector_type(16 / sizeof(T))));
+  static constexpr int kPieces = ROWS * L::chunks / THREADS;
+  static_assert(ROWS * L::chunks % THREADS == 0, "whole pieces");
+  Vec v[kPieces];
+  static __device__ __forceinline__ int row(int u) {
+    return (threadIdx.x + u * THREADS) / L::chunks;
+  }
+  static __device__ __forceinline__ int col(int u) {
+    return (threadIdx.x + u * THREADS) % L::chunks * L::vec;
+  }
+  // at[u]: the cell of the thread's u-th piece; cells: how many of the row
+  // there are from the tile's first column on
+  __device__ __forceinline__ void load(const T* const (&at)[kPieces], int cells) {
+    if (cells >= COLS) {
+#pragma unroll
+      for (int u = 0; u < kPieces; ++u) __builtin_memcpy(&v[u], at[u], sizeof(Vec));
+    } else {
+      at_rare();
+#pragma unroll
+      for (int u = 0; u < kPieces; ++u)
+#pragma unroll
+        for (int e = 0; e < L::vec; ++e) v[u][e] = col(u) + e < cells ? at[u][e] : (T)0.0f;
+    }
+  }
+  __device__ __forceinline__ void put(T* tile) const {
+#pragma unroll
+    for (int u = 0; u < kPieces; ++u)
+      *reinterpret_cast<Vec*>(tile + L::at(row(u), col(u))) = v[u];
+  }
+};
+
+// Four cells of a bias tile's row, from column c (a multiple of 4) on.
+template <int COLS> __device__ __forceinline__ at_bf16x4 at_cells(const bf16* tile, int r, int c) {
+  return *reinterpret_cast<const at_bf16x4*>(tile + AtTile<bf16, COLS>::at(r, c));
+}
+template <int COLS> __device__ __forceinline__ at_f32x4 at_cells(const float* tile, int r, int c) {
+  return *reinterpret_cast<const at_f32x4*>(tile + AtTile<float, COLS>::at(r, c));
 }
 
 // Tiles of `tile` rows of ragged samples without a list of them: sample i
