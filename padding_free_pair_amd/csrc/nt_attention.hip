@@ -164,11 +164,10 @@ __global__ __launch_bounds__(kAtThreads, sizeof(T) == 4 && (DP > 64 || BIAS) ? 1
     constexpr int buf = decltype(index)::value;
     if (j + AHEAD - 1 < tiles) at_arrive<BEHIND>();
     else at_arrive<0>();
+    if (BIAS && j + 1 < tiles)
+      biases[(buf + 1) % BUFS].put(lds_bias + (buf + 1) % BUFS * ROWS * KEYS);
     if (j + AHEAD < tiles) start();
-    if (BIAS) {
-      if (j + 1 < tiles) biases[(buf + 1) % BUFS].put(lds_bias + (buf + 1) % BUFS * ROWS * KEYS);
-      if (j + BUFS < tiles) load_bias(biases[buf]);
-    }
+    if (BIAS && j + BUFS < tiles) load_bias(biases[buf]);
     const T* lk = lds + buf * 2 * TILE;
     const T* lv = lk + TILE;
     f32x16 s[NB];

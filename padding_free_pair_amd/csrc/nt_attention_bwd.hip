@@ -58,7 +58,7 @@ __global__ __launch_bounds__(64 * QW * KW, sizeof(T) == 4 && (DP > 64 || BIAS) ?
   typedef typename AtFrag<T>::type Frag;
   typedef AtLoad<T, KEYS, DP, THREADS> Load;
   constexpr int TILE = KEYS * AtTile<T, DP>::pitch, kPair = 2 * TILE * (int)sizeof(T);
-  constexpr int AHEAD = ab_ahead(kPair), BUFS = AHEAD + 1;
+  constexpr int AHEAD = BIAS ? 1 : ab_ahead(kPair), BUFS = AHEAD + 1;
   constexpr int BEHIND = (AHEAD - 1) * 2 * Load::kPieces;
   typedef AtBiasTile<T, ROWS, KEYS, THREADS> Bias;
   constexpr int kLds = BUFS * kPair, kJoin = (KW - 1) * QW * DP / 2 * 64 * 4;
@@ -166,11 +166,10 @@ __global__ __launch_bounds__(64 * QW * KW, sizeof(T) == 4 && (DP > 64 || BIAS) ?
     constexpr int buf = decltype(index)::value;
     if (j + AHEAD - 1 < tiles) at_arrive<BEHIND>();
     else at_arrive<0>();
+    if (BIAS && j + 1 < tiles)
+      biases[(buf + 1) % BUFS].put(lds_bias + (buf + 1) % BUFS * ROWS * KEYS);
     if (j + AHEAD < tiles) start();
-    if (BIAS) {
-      if (j + 1 < tiles) biases[(buf + 1) % BUFS].put(lds_bias + (buf + 1) % BUFS * ROWS * KEYS);
-      if (j + BUFS < tiles) load_bias(biases[buf]);
-    }
+    if (BIAS && j + BUFS < tiles) load_bias(biases[buf]);
     const T* lk = lds + buf * 2 * TILE;
     const T* lv = lk + TILE;
     f32x16 s[NB], dp[NB];
@@ -266,7 +265,7 @@ __global__ __launch_bounds__(64 * KW * RW, DP > 64 || (BIAS && (sizeof(T) == 4 |
   typedef typename AtFrag<T>::type Frag;
   typedef AtLoad<T, ROWS, DP, THREADS> Load;
   constexpr int TILE = ROWS * AtTile<T, DP>::pitch, kPair = 2 * TILE * (int)sizeof(T);
-  constexpr int AHEAD = ab_ahead(kPair), BUFS = AHEAD + 1;
+  constexpr int AHEAD = BIAS ? 1 : ab_ahead(kPair), BUFS = AHEAD + 1;
   constexpr int BEHIND = (AHEAD - 1) * (2 * Load::kPieces + NB);  // the next tile's loads
   typedef AtBiasTile<T, ROWS, KEYS, THREADS> Bias;
   constexpr int kLds = BUFS * kPair, kJoin = (RW - 1) * KW * 2 * DP * 32 * 4;
@@ -389,11 +388,10 @@ __global__ __launch_bounds__(64 * KW * RW, DP > 64 || (BIAS && (sizeof(T) == 4 |
     constexpr int buf = decltype(index)::value;
     if (j + AHEAD - 1 < tiles) at_arrive<BEHIND>();
     else at_arrive<0>();
+    if (BIAS && j + 1 < tiles)
+      biases[(buf + 1) % BUFS].put(lds_bias + (buf + 1) % BUFS * ROWS * KEYS);
     if (j + AHEAD < tiles) start();
-    if (BIAS) {
-      if (j + 1 < tiles) biases[(buf + 1) % BUFS].put(lds_bias + (buf + 1) % BUFS * ROWS * KEYS);
-      if (j + BUFS < tiles) load_bias(biases[buf]);
-    }
+    if (BIAS && j + BUFS < tiles) load_bias(biases[buf]);
     const T* lq = lds + buf * 2 * TILE;
     const T* lg = lq + TILE;
     const int mine = 32 * rw * NB;  // this wave's first row in the tile
