@@ -28,7 +28,7 @@ struct AtArgs {
   const int32_t *rows, *cols;
   int64_t cells, slots, ld_q, ld_k, ld_v;
   int64_t part_rows;  // split keys: rows of one split's partial results
-  int B, H, K, D, splits;
+  int B, H, K, D, splits, chunk;
   float scale;
   const void *q, *k, *v, *bias;
   void* o;
@@ -63,8 +63,9 @@ __global__ __launch_bounds__(kAtThreads, sizeof(T) == 4 && (DP > 64 || BIAS) ? 1
   // together. Tiles in reverse, so that a causal sample's longest rows begin
   // first and the short ones fill the end.
   const int hk = blockIdx.x % a.K;
-  const int split = blockIdx.x / a.K % a.splits;
-  const int64_t slot = a.slots - 1 - blockIdx.x / a.K / a.splits;
+  const int64_t all = blockIdx.x / a.K;
+  const int split = (int)((uint32_t)all / (uint32_t)a.slots);
+  const int64_t slot = a.slots - 1 - (uint32_t)all % (uint32_t)a.slots;
   const int G = a.H / a.K;
   const int i = at_sample_of(a.eta, a.B, G, ROWS, slot);
   const int64_t tile = slot - (a.eta[i] * G / ROWS + i);
@@ -89,9 +90,18 @@ __global__ __launch_bounds__(kAtThreads, sizeof(T) == 4 && (DP > 64 || BIAS) ? 1
   }
   int64_t c0 = 0;
   if (a.splits > 1) {
-    const int64_t per = ((c1 + a.splits - 1) / a.splits + KEYS - 1) / KEYS * KEYS;
+    int64_t per = ((c1 + a.splits - 1) / a.splits + KEYS - 1) / KEYS * KEYS;
+    per = per < a.chunk ? a.chunk : per;
     c0 = split * per < c1 ? split * per : c1;
     c1 = c0 + per < c1 ? c0 + per : c1;
+    if (c0 == c1 && split > 0) {
+      if (live && kw == 0 && h == 0) {
+        float* ml = a.part_ml + ((int64_t)split * a.part_rows + t * a.H + hq) * 2;
+        ml[0] = -INFINITY;
+        ml[1] = 0.0f;
+      }
+      return;
+    }
   }
   const int keys = (int)m, last = (int)seen;
   // the fewest keys that a row of this wave sees: no masks below it
@@ -168,6 +178,9 @@ __global__ __launch_bounds__(kAtThreads, sizeof(T) == 4 && (DP > 64 || BIAS) ? 1
       biases[(buf + 1) % BUFS].put(lds_bias + (buf + 1) % BUFS * ROWS * KEYS);
     if (j + AHEAD < tiles) start();
     if (BIAS && j + BUFS < tiles) load_bias(biases[buf]);
+    // (the loads go out before the products: mixed with them by the compiler, long
+    // causal 258 us, in this order 233)
+    __builtin_amdgcn_sched_barrier(0);
     const T* lk = lds + buf * 2 * TILE;
     const T* lv = lk + TILE;
     f32x16 s[NB];
@@ -324,6 +337,8 @@ __global__ __launch_bounds__(256) void k_attention_join(const float* part_o, con
       most = part_ml[(lane * rows + at) * 2];
       sum = part_ml[(lane * rows + at) * 2 + 1];
     }
+    // splits behind the row's last key hold nothing
+    const int used = 64 - __builtin_clzll(__ballot(sum != 0.0f) | 1);
     float top = most;
 #pragma unroll
     for (int x = 1; x < 64; x <<= 1) top = fmaxf(top, __shfl_xor(top, x));
@@ -333,17 +348,17 @@ __global__ __launch_bounds__(256) void k_attention_join(const float* part_o, con
     for (int x = 1; x < 64; x <<= 1) sum += __shfl_xor(sum, x);
     float acc[2] = {0.0f, 0.0f};
     const int d0 = lane < D ? lane : 0, d1 = lane + 64 < D ? lane + 64 : 0;
-    for (int s = 0; s < splits; s += 8) {  // eight loads at a time
+    for (int s = 0; s < used; s += 8) {  // eight loads at a time
       float v[8][2];
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
-        const float* p = part_o + ((s + u < splits ? s + u : s) * rows + at) * D;
+        const float* p = part_o + ((s + u < used ? s + u : s) * rows + at) * D;
         v[u][0] = p[d0];
         v[u][1] = p[d1];
       }
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
-        if (s + u < splits) {
+        if (s + u < used) {
           const float ws = __shfl(w, s + u);
           acc[0] += ws * v[u][0];
           acc[1] += ws * v[u][1];
@@ -358,23 +373,45 @@ __global__ __launch_bounds__(256) void k_attention_join(const float* part_o, con
   }
 }
 
-// How the waves of a workgroup are shared out, and in how many parts the keys
-// are split over workgroups.
+// How the waves of a workgroup are shared out, in how many parts the keys are
+// split over workgroups, and the fewest keys of a part.
 struct AtPlan {
-  int qw, splits;
+  int qw, splits, chunk;
 };
+// Workgroups of 128 rows read each tile of keys half as often as those of 64,
+// and there have to be enough of them: uniform 8 x 2,048 rows (D 64, 16 heads,
+// 2,176 workgroups of 128) and the long causal batch (1,520) take MORE.
+//
+// A split costs its partial sums (fp32, written and read) and a second launch,
+// 5 us at least. Where a sample's rows fill half a tile of 64 or less (decoding)
+// they are small beside the keys, and parts of about 512 keys also even out
+// samples of different lengths; below that, parts as short as make 512
+// workgroups. The launch holds twice the parts that the mean length fills, and
+// those behind a sample's last key return: one row each of 16 samples of 8,192 ..
+// 1 keys (8 key heads of 4, D 128): 44 us; with 1,024 workgroups 46, 2,048: 50;
+// with four times the mean's parts 48, once 69. 64 such samples: 133 us, unsplit
+// 191; 256: 494. One of 8,192 keys: 20.
+// With more rows only few workgroups over many keys gain: 256 rows over 8,192
+// keys 98 -> 54 us, 128 over 2,000 28 -> 18, but 1,000 over 1,000 (D 32, 12 heads)
+// 12 -> 18, and 4,000 over 4,000 (D 64, 252 workgroups) 37 -> 40.
 AtPlan plan_of(const nt_partition& p, const nt_attention& a) {
-  if (p.T == 0 || p.B == 0) return {4, 1};
+  if (p.T == 0 || p.B == 0) return {4, 1, 0};
   const int G = a.heads / a.kv_heads;
   auto groups = [&](int qw) { return at_slots(p.T, p.B, G, 32 * qw) * a.kv_heads; };
   const int qw = groups(4) >= 1024 ? 4 : 2;
   const int64_t keys = p.T_cols / p.B;
-  int64_t s = 1;
-  if (groups(qw) < 512 && keys >= 512) {
-    s = 2048 / groups(qw);
-    if (s > keys / 128) s = keys / 128;
+  const bool few = p.T * G <= 32 * (int64_t)p.B;
+  int64_t s = 1, chunk = 0;
+  if (keys >= 512 && (few ? groups(qw) < 4096 : groups(qw) <= 192 && p.T_cols >= 1536)) {
+    chunk = (keys * groups(qw) / 512 + 63) / 64 * 64;
+    const int64_t most = keys / 4 > 512 ? keys / 4 : 512;
+    if (few && chunk > most) chunk = most / 64 * 64;
+    if (chunk < 128) chunk = 128;
+    s = 2 * keys / chunk;
+    if (s > 64) s = 64;
+    if (s < 1) s = 1;
   }
-  return {qw, (int)(s < 1 ? 1 : s > 64 ? 64 : s)};
+  return {qw, (int)s, (int)(chunk < (1 << 30) ? chunk : 1 << 30)};
 }
 
 template <typename T, int DP, int QW, int KW, int NB, bool BIAS>
@@ -444,6 +481,7 @@ hipError_t launch_attention(const nt_partition& p, const nt_attention& a, const 
   const AtPlan plan = plan_of(p, a);
   x.slots = at_slots(p.T, p.B, a.heads / a.kv_heads, 32 * plan.qw);
   x.splits = plan.splits;
+  x.chunk = plan.chunk;
   x.scale = a.scale;
   x.q = q;
   x.k = k;
