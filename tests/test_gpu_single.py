@@ -293,6 +293,34 @@ def test_attention_backward(nt, case):
         np.testing.assert_array_equal(bits(x, torch), bits(y, torch))
 
 
+SPLITS = [
+    # few rows (parts of equal length, most of them empty in short samples), then many rows
+    ([1, 1, 0, 2, 1, 1], [5000, 1, 700, 0, 64, 3001], 8, 2, 128, "none", False, "bf16", "split"),
+    ([1, 2, 1], [2500, 65, 129], 4, 2, 64, "masked", True, "bf16", "split"),
+    ([1] * 4, [3000, 900, 513, 300], 2, 1, 40, "plain", False, "f32", "split"),
+    ([1] * 70, [8] * 69 + [50000], 4, 4, 32, "none", False, "bf16", "split"),
+    ([150, 3], [2100, 40], 2, 1, 64, "masked", True, "f32", "split"),
+]
+
+
+@pytest.mark.parametrize("case", SPLITS)
+def test_attention_split_over_keys(nt, case):
+    """Parts behind a row's last key leave nothing: the workspace holds NaN before."""
+    rows, cols, H, K, D, kind, causal, dtype, layout = case
+    announce(f"attention split {case}"[:300])
+    c, (q, k, v, b), (q64, k64, v64, b64), scale = _attention_inputs(np.random.default_rng(23), case)
+    p = _part(nt, rows, cols)
+    need = nt.nt_attention_workspace_bytes(p, H, K, D, q.dtype, causal)
+    assert need > 0
+    ws = torch.full((need // 4,), float("nan"), dtype=torch.float32, device="cuda")
+    o, lse = nt.nt_single_attention(p, q, k, v, bias=b, causal=causal, workspace=ws)
+    torch.cuda.synchronize()
+    ro, rl = oracle.attention(rows, c, q64, k64, v64, b64, causal, scale)
+    bo, bl = sb.attention_bound(rows, c, q64, k64, v64, ro, rl, b64, causal, scale, dtype)
+    _within("o", f64(o, torch), ro, bo)
+    _within("lse", f64(lse, torch), rl, bl)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_attention_lowest_value_masks(nt, dtype):
     """A bias of the type's lowest value leaves a row's other keys, and a row
