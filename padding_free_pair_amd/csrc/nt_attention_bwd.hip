@@ -11,7 +11,12 @@
 // dP = G V^T give P and dS as fragments of g_v^T += G^T P and g_k^T += Q^T dS,
 // and shared key heads sum in registers. The scores and dP are formed twice (7
 // products instead of 5); joining the walks would need g_q summed across
-// workgroups.
+// workgroups. Both are bound by what a tile costs beside its products (LDS
+// reads, exponentials, conversions): causal lengths 4096, 2500, 1111, 300 (16
+// heads over 8, D 64) 228 us, 64 % of the rate of a large matrix product over
+// the 7 products; lengths 1024, 768, 384, 96 with a bias and its gradient (12
+// heads, D 32) 51 us, where the bias is read twice and its gradient written
+// once (129 MB).
 #include <math.h>
 
 #include "nt_attention_tile.hpp"
@@ -253,8 +258,10 @@ __global__ __launch_bounds__(64 * QW * KW, sizeof(T) == 4 && (DP > 64 || BIAS) ?
 }
 
 // g_k and g_v of 32 keys a wave, and the bias's gradient dS: a store covers 64
-// bytes of two rows. (From the first kernel, whose lanes hold four cells each of
-// 32 rows, the stores took 14 us instead of 5 on 21.5 million cells.) KW waves of a
+// bytes of two rows, 5 us for 21.5 million cells. (From the first kernel, whose
+// lanes hold four cells each of 32 rows, 14 us; put through LDS there and stored
+// as whole lines, both kernels together took 56 us against 51, since the first
+// one also fetches the bias from memory.) KW waves of a
 // workgroup own different keys; RW waves own the same keys and take different
 // blocks of 32 rows of each tile, and their sums are joined at the end in
 // order, so few keys still fill the card.
@@ -540,11 +547,12 @@ hipError_t run_k(const nt_partition& p, AbArgs x, hipStream_t stream) {
 
 // Waves share a tile of 128 rows (keys) where that makes eight workgroups a CU,
 // and two of them each 64 otherwise; fewer than one and a half workgroups of 64
-// keys a CU are split once more. Gradients of eight samples of 2,048 (D 64, 16
-// heads, 2,048 workgroups): 243 us against 260 with two waves for the queries,
-// 388 against 438 for the keys; of lengths 1024, 768, 384, 96 with a bias (D 32,
-// 12 heads, 252): 35 against 31, and 55 against 38; of 2,000 rows with 4 key
-// heads (D 128), keys: 126 with two waves, 79 with one.
+// keys a CU are split once more (bf16). Four waves against two sharing, uniform
+// 8 x 2,048 (D 64, 16 heads, 2,048 workgroups of 128): queries 271 us against
+// 291, keys 381 against 476; causal lengths 4096 .. 300 (D 64, 8 key heads, 528):
+// 124 against 112, 228 against 184. Keys in one wave against two: 2,000 rows
+// (D 128, 4 key heads, 128 workgroups of 64) 94 us against 143; lengths 1024 .. 96
+// with a bias (D 32, 12 heads, 468): 36 against 32.
 template <typename T, int DP, bool BIAS>
 hipError_t run(const nt_partition& p, AbArgs x, hipStream_t stream) {
   // (two blocks of 32 at a time; a bias or fp32 fragments would not leave it the registers)
