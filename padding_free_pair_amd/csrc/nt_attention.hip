@@ -488,7 +488,8 @@ hipError_t launch_attention(const nt_partition& p, const nt_attention& a, const 
   x.K = a.kv_heads;
   x.D = a.head_dim;
   const AtPlan plan = plan_of(p, a);
-  x.slots = at_slots(p.T, p.B, a.heads / a.kv_heads, 32 * plan.qw);
+  const int qw = bias ? 2 : plan.qw;  // (the workspace's size does not depend on the bias)
+  x.slots = at_slots(p.T, p.B, a.heads / a.kv_heads, 32 * qw);
   x.splits = plan.splits;
   x.chunk = plan.chunk;
   x.scale = a.scale;
@@ -500,8 +501,8 @@ hipError_t launch_attention(const nt_partition& p, const nt_attention& a, const 
   x.lse = lse;
   x.part_o = static_cast<float*>(ws);
   x.part_ml = x.part_o + (int64_t)x.splits * x.part_rows * a.head_dim;
-  return dtype == NT_BF16 ? forward<bf16>(p, a, x, plan.qw, stream)
-                          : forward<float>(p, a, x, plan.qw, stream);
+  return dtype == NT_BF16 ? forward<bf16>(p, a, x, qw, stream)
+                          : forward<float>(p, a, x, qw, stream);
 }
 
 }  // namespace nt

@@ -321,6 +321,43 @@ def test_attention_split_over_keys(nt, case):
     _within("lse", f64(lse, torch), rl, bl)
 
 
+MANY = [
+    # enough workgroups for tiles of 128 rows, for two launches of the gradient, and wide heads
+    ([32] * 256 + [0, 45, 1, 90], None, 8, 8, 16, "none", True, "bf16", "fused"),
+    ([64] * 139 + [30], None, 8, 8, 24, "masked", False, "bf16", "split"),
+    ([64] * 139 + [30], None, 8, 4, 32, "none", False, "f32", "split"),
+    ([64] * 40, None, 8, 8, 128, "plain", True, "bf16", "split"),
+    ([64] * 40, None, 16, 8, 72, "none", False, "bf16", "fused"),
+    ([50, 70], None, 2, 2, 128, "plain", True, "f32", "split"),
+]
+
+
+@pytest.mark.parametrize("case", MANY)
+def test_attention_many_workgroups(nt, case):
+    rows, cols, H, K, D, kind, causal, dtype, layout = case
+    announce(f"attention, many workgroups {case[2:]}")
+    rng = np.random.default_rng(24)
+    c, (q, k, v, b), (q64, k64, v64, b64), scale = _attention_inputs(rng, case)
+    g, g64 = _dev(rng.normal(size=tuple(q.shape)), dtype)
+    p = _part(nt, rows, cols)
+    o, lse = nt.nt_single_attention(p, q, k, v, bias=b, causal=causal)
+    got = nt.nt_single_attention_backward(p, q, k, v, o, lse, g, bias=b, causal=causal)
+    again = nt.nt_single_attention_backward(p, q, k, v, o, lse, g, bias=b, causal=causal)
+    torch.cuda.synchronize()
+    ro, rl = oracle.attention(rows, c, q64, k64, v64, b64, causal, scale)
+    bo, bl = sb.attention_bound(rows, c, q64, k64, v64, ro, rl, b64, causal, scale, dtype)
+    o64, l64 = f64(o, torch), f64(lse, torch)
+    _within("o", o64, ro, bo)
+    _within("lse", l64, rl, bl)
+    ref = oracle.attention_backward(rows, c, q64, k64, v64, o64, l64, g64, b64, causal, scale)
+    bound = sb.attention_backward_bound(rows, c, q64, k64, v64, o64, l64, g64, ref[:3], b64,
+                                        causal, scale, dtype)
+    for name, x, y, r, e in zip(("g_q", "g_k", "g_v", "g_bias"), got, again, ref, bound):
+        if r is not None:
+            _within(name, f64(x, torch), r, e)
+            np.testing.assert_array_equal(bits(x, torch), bits(y, torch))
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_attention_lowest_value_masks(nt, dtype):
     """A bias of the type's lowest value leaves a row's other keys, and a row
