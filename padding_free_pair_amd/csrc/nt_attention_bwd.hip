@@ -1,12 +1,13 @@
 // Gradients of the attention of pair rows over pair columns, which recompute
 // the probabilities from the scores and the forward's log sums.
 //
-// Two kernels, each with its own order of sums and no atomics, so results
+// Two walks, each with its own order of sums and no atomics, so results
 // repeat bit by bit. The first owns 32 virtual rows (queries of one key head,
 // as in the forward) in a wave and walks over the keys: it forms S^T = K Q^T and
 // dP^T = V G^T, and their dS^T is, as it stands, the fragment of
 // g_q^T += K^T dS^T. It also leaves each row's log sum and delta, prepared and
-// row by row for each head, to the second, which owns 32 keys in a wave and
+// row by row for each head, to the second (where both go out in one launch a
+// small kernel before it does), which owns 32 keys in a wave and
 // walks over the rows of each query head of the group in turn: S = Q K^T and
 // dP = G V^T give P and dS as fragments of g_v^T += G^T P and g_k^T += Q^T dS,
 // and shared key heads sum in registers. The scores and dP are formed twice (7
@@ -15,7 +16,7 @@
 // reads, exponentials, conversions): causal lengths 4096, 2500, 1111, 300 (16
 // heads over 8, D 64) 228 us, 64 % of the rate of a large matrix product over
 // the 7 products; lengths 1024, 768, 384, 96 with a bias and its gradient (12
-// heads, D 32) 51 us, where the bias is read twice and its gradient written
+// heads, D 32) 50 us, where the bias is read twice and its gradient written
 // once (129 MB).
 #include <math.h>
 
@@ -55,27 +56,33 @@ __device__ __forceinline__ float ab_dot(const f32x8& a, const f32x8& b) {
 
 // g_q of 32 virtual rows a wave, and their statistics. As in the forward, QW
 // waves own different rows, and KW waves the same rows and different keys.
-template <typename T, int DP, int QW, int KW, int NB, bool BIAS>
-__global__ __launch_bounds__(64 * QW * KW, sizeof(T) == 4 && (DP > 64 || BIAS) ? 1 : 2) void k_attention_bwd_q(
-    AbArgs a) {
-  constexpr int KS = DP / 16, DT = DP / 32, THREADS = 64 * QW * KW;
-  constexpr int ROWS = 32 * QW, KEYS = 32 * KW * NB;
+template <typename T, int DP, int QW, int KW, int NB, bool BIAS> struct AbQ {
+  static constexpr int THREADS = 64 * QW * KW, ROWS = 32 * QW, KEYS = 32 * KW * NB;
+  static constexpr int TILE = KEYS * AtTile<T, DP>::pitch, kPair = 2 * TILE * (int)sizeof(T);
+  static constexpr int AHEAD = BIAS ? 1 : ab_ahead(kPair), BUFS = AHEAD + 1;
+  static constexpr int kTiles = BUFS * kPair, kJoin = (KW - 1) * QW * DP / 2 * 64 * 4;
+  static constexpr int kBias = kTiles > kJoin ? kTiles : kJoin;  // where the bias tiles are
+  static constexpr int kLds = kBias + (BIAS ? BUFS * ROWS * KEYS * (int)sizeof(T) : 0);
+};
+// READY: the statistics are there already.
+template <typename T, int DP, int QW, int KW, int NB, bool BIAS, bool READY>
+__device__ __forceinline__ void ab_queries(const AbArgs& a, char* lds_bytes, uint32_t block) {
+  typedef AbQ<T, DP, QW, KW, NB, BIAS> P;
+  constexpr int KS = DP / 16, DT = DP / 32, THREADS = P::THREADS;
+  constexpr int ROWS = P::ROWS, KEYS = P::KEYS;
   typedef typename AtFrag<T>::type Frag;
   typedef AtLoad<T, KEYS, DP, THREADS> Load;
-  constexpr int TILE = KEYS * AtTile<T, DP>::pitch, kPair = 2 * TILE * (int)sizeof(T);
-  constexpr int AHEAD = BIAS ? 1 : ab_ahead(kPair), BUFS = AHEAD + 1;
+  constexpr int TILE = P::TILE, kPair = P::kPair, AHEAD = P::AHEAD, BUFS = P::BUFS;
   constexpr int BEHIND = (AHEAD - 1) * 2 * Load::kPieces;
   typedef AtBiasTile<T, ROWS, KEYS, THREADS> Bias;
-  constexpr int kLds = BUFS * kPair, kJoin = (KW - 1) * QW * DP / 2 * 64 * 4;
-  __shared__ __align__(16) char lds_bytes[kLds > kJoin ? kLds : kJoin];
-  __shared__ __align__(16) T lds_bias[BIAS ? BUFS * ROWS * KEYS : 1];
+  T* lds_bias = reinterpret_cast<T*>(lds_bytes + P::kBias);
   const T* lds = reinterpret_cast<const T*>(lds_bytes);
   const uint32_t lds_at = at_lds(lds_bytes);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l32 = lane & 31, h = lane >> 5;
   const int qw = wave / KW, kw = wave % KW;
   // as in the forward: key heads fastest, a causal sample's longest rows first
-  const int hk = blockIdx.x % a.K;
-  const int64_t slot = a.slots - 1 - blockIdx.x / a.K;
+  const int hk = block % a.K;
+  const int64_t slot = a.slots - 1 - block / a.K;
   const int G = a.H / a.K;
   const int i = at_sample_of(a.eta, a.B, G, ROWS, slot);
   const int64_t tile = slot - (a.eta[i] * G / ROWS + i);
@@ -110,16 +117,21 @@ __global__ __launch_bounds__(64 * QW * KW, sizeof(T) == 4 && (DP > 64 || BIAS) ?
     if (16 * s + 8 * h < a.D) {
       q[s] = at_row(qp, s, h);
       g[s] = at_row(gp, s, h);
-      delta += ab_dot(g[s], at_row(op, s, h));
+      if (!READY) delta += ab_dot(g[s], at_row(op, s, h));
     }
   }
-  delta += __shfl_xor(delta, 32);
   // a row that saw nothing gives nothing
-  const float lse = a.lse[at] == -INFINITY ? INFINITY : a.lse[at];
-  const float base = lse * kLog2e;
-  if (live && h == 0 && kw == 0) {
-    a.logs[hq * a.T + t] = BIAS ? lse : base;
-    a.delta[hq * a.T + t] = delta;
+  const float given = READY ? a.logs[hq * a.T + t] : a.lse[at];
+  const float lse = given == -INFINITY ? INFINITY : given;
+  const float base = READY ? given : lse * kLog2e;
+  if (READY) {
+    delta = a.delta[hq * a.T + t];
+  } else {
+    delta += __shfl_xor(delta, 32);
+    if (live && h == 0 && kw == 0) {
+      a.logs[hq * a.T + t] = BIAS ? lse : base;
+      a.delta[hq * a.T + t] = delta;
+    }
   }
   const T* kp = static_cast<const T*>(a.k) + a.mu[i] * a.ld_k + (int64_t)hk * a.D;
   const T* vp = static_cast<const T*>(a.v) + a.mu[i] * a.ld_v + (int64_t)hk * a.D;
@@ -257,6 +269,13 @@ __global__ __launch_bounds__(64 * QW * KW, sizeof(T) == 4 && (DP > 64 || BIAS) ?
                   gq[d][4 * y + 2] * a.scale, gq[d][4 * y + 3] * a.scale);
 }
 
+template <typename T, int DP, int QW, int KW, int NB, bool BIAS>
+__global__ __launch_bounds__(64 * QW * KW, sizeof(T) == 4 && (DP > 64 || BIAS) ? 1 : 2) void k_attention_bwd_q(
+    AbArgs a) {
+  __shared__ __align__(16) char lds[AbQ<T, DP, QW, KW, NB, BIAS>::kLds];
+  ab_queries<T, DP, QW, KW, NB, BIAS, false>(a, lds, blockIdx.x);
+}
+
 // g_k and g_v of 32 keys a wave, and the bias's gradient dS: a store covers 64
 // bytes of two rows, 5 us for 21.5 million cells. (From the first kernel, whose
 // lanes hold four cells each of 32 rows, 14 us; put through LDS there and stored
@@ -265,29 +284,39 @@ __global__ __launch_bounds__(64 * QW * KW, sizeof(T) == 4 && (DP > 64 || BIAS) ?
 // workgroup own different keys; RW waves own the same keys and take different
 // blocks of 32 rows of each tile, and their sums are joined at the end in
 // order, so few keys still fill the card.
+template <typename T, int DP, int KW, int RW, int NB, bool BIAS> struct AbK {
+  static constexpr int THREADS = 64 * KW * RW, KEYS = 32 * KW;
+  static constexpr int ROWS = 32 * RW * NB;  // of a tile: NB blocks of a wave
+  static constexpr int TILE = ROWS * AtTile<T, DP>::pitch, kPair = 2 * TILE * (int)sizeof(T);
+  static constexpr int AHEAD = BIAS ? 1 : ab_ahead(kPair), BUFS = AHEAD + 1;
+  static constexpr int kTiles = BUFS * kPair, kJoin = (RW - 1) * KW * 2 * DP * 32 * 4;
+  // the rows' statistics, then the bias tiles
+  static constexpr int kStats = kTiles > kJoin ? kTiles : kJoin;
+  static constexpr int kBias = kStats + BUFS * KW * RW * 2 * 32 * NB * 4;
+  static constexpr int kLds = kBias + (BIAS ? BUFS * ROWS * KEYS * (int)sizeof(T) : 0);
+  static constexpr int kWaves = DP > 64 || (BIAS && (sizeof(T) == 4 || (RW == 4 && DP > 32))) ? 1 : 2;
+};
 template <typename T, int DP, int KW, int RW, int NB, bool BIAS>
-__global__ __launch_bounds__(64 * KW * RW, DP > 64 || (BIAS && (sizeof(T) == 4 || (RW == 4 && DP > 32))) ? 1 : 2) void k_attention_bwd_k(AbArgs a) {
-  constexpr int KS = DP / 16, DT = DP / 32, THREADS = 64 * KW * RW, KEYS = 32 * KW;
-  constexpr int ROWS = 32 * RW * NB;  // of a tile: NB blocks of a wave
+__device__ __forceinline__ void ab_keys(const AbArgs& a, char* lds_bytes, uint32_t block) {
+  typedef AbK<T, DP, KW, RW, NB, BIAS> P;
+  constexpr int KS = DP / 16, DT = DP / 32, THREADS = P::THREADS, KEYS = P::KEYS, ROWS = P::ROWS;
   typedef typename AtFrag<T>::type Frag;
   typedef AtLoad<T, ROWS, DP, THREADS> Load;
-  constexpr int TILE = ROWS * AtTile<T, DP>::pitch, kPair = 2 * TILE * (int)sizeof(T);
-  constexpr int AHEAD = BIAS ? 1 : ab_ahead(kPair), BUFS = AHEAD + 1;
+  constexpr int TILE = P::TILE, kPair = P::kPair, AHEAD = P::AHEAD, BUFS = P::BUFS;
   constexpr int BEHIND = (AHEAD - 1) * (2 * Load::kPieces + NB);  // the next tile's loads
   typedef AtBiasTile<T, ROWS, KEYS, THREADS> Bias;
-  constexpr int kLds = BUFS * kPair, kJoin = (RW - 1) * KW * 2 * DP * 32 * 4;
-  __shared__ __align__(16) char lds_bytes[kLds > kJoin ? kLds : kJoin];
   // each wave's own rows: log sums, then deltas
-  __shared__ __align__(16) float stats[BUFS][KW * RW][2][32 * NB];
-  __shared__ __align__(16) T lds_bias[BIAS ? BUFS * ROWS * KEYS : 1];
+  typedef float Stats[KW * RW][2][32 * NB];
+  Stats* stats = reinterpret_cast<Stats*>(lds_bytes + P::kStats);
+  T* lds_bias = reinterpret_cast<T*>(lds_bytes + P::kBias);
   const T* lds = reinterpret_cast<const T*>(lds_bytes);
   const uint32_t lds_at = at_lds(lds_bytes);
   const uint32_t stats_at = at_lds(stats);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l32 = lane & 31, h = lane >> 5;
   const int kw = wave / RW, rw = wave % RW;
   // a causal sample's first keys, which the most rows see, begin first
-  const int hk = blockIdx.x % a.K;
-  const int64_t slot = blockIdx.x / a.K;
+  const int hk = block % a.K;
+  const int64_t slot = block / a.K;
   const int G = a.H / a.K;
   const int i = at_sample_of(a.mu, a.B, 1, KEYS, slot);
   const int64_t tile = slot - (a.mu[i] / KEYS + i);
@@ -530,6 +559,44 @@ __global__ __launch_bounds__(64 * KW * RW, DP > 64 || (BIAS && (sizeof(T) == 4 |
     }
 }
 
+template <typename T, int DP, int KW, int RW, int NB, bool BIAS>
+__global__ __launch_bounds__(64 * KW * RW, (AbK<T, DP, KW, RW, NB, BIAS>::kWaves)) void k_attention_bwd_k(
+    AbArgs a) {
+  __shared__ __align__(16) char lds[AbK<T, DP, KW, RW, NB, BIAS>::kLds];
+  ab_keys<T, DP, KW, RW, NB, BIAS>(a, lds, blockIdx.x);
+}
+
+// Both walks in one launch, the keys' (the longer ones) first, behind a kernel
+// that prepares the rows' statistics.
+template <typename T, int DP, bool BIAS>
+__global__ __launch_bounds__(256, (AbK<T, DP, 2, 2, 1, BIAS>::kWaves)) void k_attention_bwd_both(
+    AbArgs a, uint32_t key_blocks) {
+  constexpr int kQ = AbQ<T, DP, 2, 2, 1, BIAS>::kLds, kK = AbK<T, DP, 2, 2, 1, BIAS>::kLds;
+  __shared__ __align__(16) char lds[kQ > kK ? kQ : kK];
+  if (blockIdx.x < key_blocks) ab_keys<T, DP, 2, 2, 1, BIAS>(a, lds, blockIdx.x);
+  else ab_queries<T, DP, 2, 2, 1, BIAS, true>(a, lds, blockIdx.x - key_blocks);
+}
+
+// The log sum and delta = o . g_o of every row and head: 8 dimensions a lane,
+// the next power of two of D / 8 lanes a group.
+template <typename T>
+__global__ __launch_bounds__(256) void k_attention_bwd_rows(AbArgs a, int lanes, bool with_bias) {
+  const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) / lanes;  // t H + head
+  const int e0 = threadIdx.x % lanes * 8;
+  const bool live = at < a.T * a.H;
+  float delta = 0.0f;
+  if (live && e0 < a.D)
+    delta = ab_dot(at_row(static_cast<const T*>(a.g_o) + at * a.D + e0, 0, 0),
+                   at_row(static_cast<const T*>(a.o) + at * a.D + e0, 0, 0));
+  for (int x = 1; x < lanes; x <<= 1) delta += __shfl_xor(delta, x);
+  if (!live || e0) return;
+  // a row that saw nothing gives nothing
+  const float lse = a.lse[at] == -INFINITY ? INFINITY : a.lse[at];
+  const int64_t to = at % a.H * a.T + at / a.H;
+  a.logs[to] = with_bias ? lse : lse * kLog2e;
+  a.delta[to] = delta;
+}
+
 template <typename T, int DP, int QW, int KW, int NB, bool BIAS>
 hipError_t run_q(const nt_partition& p, AbArgs x, hipStream_t stream) {
   x.slots = at_slots(p.T, p.B, x.H / x.K, 32 * QW);
@@ -553,10 +620,37 @@ hipError_t run_k(const nt_partition& p, AbArgs x, hipStream_t stream) {
 // 124 against 112, 228 against 184. Keys in one wave against two: 2,000 rows
 // (D 128, 4 key heads, 128 workgroups of 64) 94 us against 143; lengths 1024 .. 96
 // with a bias (D 32, 12 heads, 468): 36 against 32.
+//
+// Up to 3,200 workgroups of both walks go out in one launch (512 where the keys'
+// registers leave one workgroup a CU): neither walk alone fills the card to its
+// end. Against two launches: lengths 1024 .. 96 with a bias 50 us against 51,
+// without 29 against 33, 2,000 rows (D 32, 12 heads, causal) 34 against 48, 1,000 +
+// 500 + 300 (D 64, 12 heads) with a bias 54 against 79, causal 4096 .. 300 (3,064)
+// 228 against 231; 8 x 1,024 with a bias (3,264) 195 against 192, 2,000 rows of D
+// 128 and 16 heads (1,024) 123 against 112. Shared key heads with few keys are
+// better split (2,000 rows, D 64, 16 heads over 4: 91 us, in one launch 124).
 template <typename T, int DP, bool BIAS>
 hipError_t run(const nt_partition& p, AbArgs x, hipStream_t stream) {
   // (two blocks of 32 at a time; a bias or fp32 fragments would not leave it the registers)
   constexpr bool can_share = sizeof(T) == 2 && !BIAS;
+  typedef AbK<T, DP, 2, 2, 1, BIAS> Keys;
+  if constexpr (Keys::kLds <= 86 * 1024) {  // (not wide fp32 heads, whose tiles fill LDS)
+    const int64_t q_blocks = at_slots(p.T, p.B, x.H / x.K, 64) * x.K;
+    const int64_t k_blocks = at_slots(p.T_cols, p.B, 1, 64) * x.K;
+    if (p.T && p.T_cols && q_blocks + k_blocks <= (Keys::kWaves == 2 ? 3200 : 512) &&
+        (x.H == x.K || k_blocks >= 384)) {
+      int lanes = 1;
+      while (lanes * 8 < x.D) lanes *= 2;
+      const int64_t rows = (p.T * x.H * lanes + 255) / 256;
+      k_attention_bwd_rows<T><<<(unsigned)rows, 256, 0, stream>>>(x, lanes, BIAS);
+      hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+      x.slots = at_slots(p.T, p.B, x.H / x.K, 64);
+      k_attention_bwd_both<T, DP, BIAS>
+          <<<(unsigned)(q_blocks + k_blocks), 256, 0, stream>>>(x, (uint32_t)k_blocks);
+      return hipGetLastError();
+    }
+  }
   if (p.T) {
     bool many = false;
     if constexpr (can_share) many = at_slots(p.T, p.B, x.H / x.K, 128) * x.K >= 2048;
