@@ -581,9 +581,13 @@ __global__ __launch_bounds__(256, (AbK<T, DP, 2, 2, 1, BIAS>::kWaves)) void k_at
 // the next power of two of D / 8 lanes a group.
 template <typename T>
 __global__ __launch_bounds__(256) void k_attention_bwd_rows(AbArgs a, int lanes, bool with_bias) {
-  const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) / lanes;  // t H + head
+  // a head's rows one after another: the statistics are written as whole lines
+  // (T H < 2^29: a grid of 32-row tiles fits)
+  const uint32_t per = 256 / lanes, rows = (uint32_t)a.T;
+  const uint32_t to = blockIdx.x * per + threadIdx.x / lanes;  // head T + t
   const int e0 = threadIdx.x % lanes * 8;
-  const bool live = at < a.T * a.H;
+  const bool live = to < rows * a.H;
+  const int64_t at = live ? (int64_t)(to % rows) * a.H + to / rows : 0;
   float delta = 0.0f;
   if (live && e0 < a.D)
     delta = ab_dot(at_row(static_cast<const T*>(a.g_o) + at * a.D + e0, 0, 0),
@@ -592,7 +596,6 @@ __global__ __launch_bounds__(256) void k_attention_bwd_rows(AbArgs a, int lanes,
   if (!live || e0) return;
   // a row that saw nothing gives nothing
   const float lse = a.lse[at] == -INFINITY ? INFINITY : a.lse[at];
-  const int64_t to = at % a.H * a.T + at / a.H;
   a.logs[to] = with_bias ? lse : lse * kLog2e;
   a.delta[to] = delta;
 }
