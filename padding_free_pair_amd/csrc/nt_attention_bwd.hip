@@ -14,7 +14,7 @@
 // products instead of 5); joining the walks would need g_q summed across
 // workgroups. Both are bound by what a tile costs beside its products (LDS
 // reads, exponentials, conversions): causal lengths 4096, 2500, 1111, 300 (16
-// heads over 8, D 64) 228 us, 64 % of the rate of a large matrix product over
+// heads over 8, D 64) 229 us, 64 % of the rate of a large matrix product over
 // the 7 products; lengths 1024, 768, 384, 96 with a bias and its gradient (12
 // heads, D 32) 50 us, where the bias is read twice and its gradient written
 // once (129 MB).
