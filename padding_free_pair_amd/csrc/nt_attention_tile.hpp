@@ -12,6 +12,7 @@
 // are its 16 values of k in another order, which the other operand takes too.
 #pragma once
 
+#include "nt_attention_index.hpp"
 #include "nt_device.hpp"
 
 namespace nt {
@@ -36,27 +37,7 @@ __device__ __forceinline__ f32x16 at_mma(const f32x8& a, const f32x8& b, f32x16 
   return c;
 }
 
-// Where a tile of token rows keeps its elements in LDS: rows of 16-byte chunks
-// without padding (so that loads can write them as they come), chunk c of row
-// r at c ^ f(r). Fragments along rows read one chunk of 16 rows at once, which f
-// must send to the 16 chunks of 256 bytes. Fragments across rows read, in bf16,
-// 4 neighbouring chunks of 4 rows at once, which f must send to the 4 different
-// 64-byte pieces: f's high bits are r's low ones. In fp32 they read 8 chunks of
-// two rows 4 apart, which f sends to the two halves where a row has 16 chunks.
-template <typename T, int DP> struct AtTile {
-  static constexpr int vec = 16 / (int)sizeof(T);       // elements of a chunk
-  static constexpr int pitch = DP == 96 ? 128 : DP;     // elements of a row
-  static constexpr int chunks = pitch / vec;            // of a row
-  static __device__ __forceinline__ int turn(int r) {   // f
-    if (sizeof(T) == 2)
-      return chunks == 16 ? (r & 3) << 2 | ((r >> 2) & 3)
-             : chunks == 8 ? ((r >> 1) & 1) << 2 | ((r >> 2) & 3) : (r >> 2) & 3;
-    return chunks == 8 ? (r >> 1) & 7 : ((r >> 2) & 1) << 3 | ((r >> 3) & 1) << 2 | (r & 3);
-  }
-  static __device__ __forceinline__ int at(int r, int c) {
-    return r * pitch + ((c / vec) ^ turn(r)) * vec + c % vec;
-  }
-};
+template <typename T, int DP> struct AtTile : AtTileMap<(int)sizeof(T), DP> {};
 
 // Values 16 s + 8 h .. of a row in global memory as a fragment.
 __device__ __forceinline__ bf16x8 at_row(const bf16* row, int s, int h) {
@@ -197,24 +178,16 @@ __device__ const f32x4 kAtZeros = {0.0f, 0.0f, 0.0f, 0.0f};
 
 // A tile of ROWS token rows of D elements (D <= DP) on its way to LDS, THREADS
 // threads taking chunks one after another. A thread's distances from the
-// tile's first row stay the same from tile to tile (ld <= 2^22 keeps them in 32
-// bits). Rows past the last one read the last one (their weight is zero);
-// columns past D read zeros.
+// tile's first row stay the same from tile to tile. Rows past the last one read
+// the last one (their weight is zero); where a tile is not whole, columns past D
+// read zeros.
 template <typename T, int ROWS, int DP, int THREADS> struct AtLoad {
-  typedef AtTile<T, DP> L;
-  static constexpr int kPieces = ROWS * L::chunks / THREADS;  // loads of a wave
-  static_assert(ROWS * L::chunks % THREADS == 0, "whole pieces");
+  typedef AtLoadMap<(int)sizeof(T), ROWS, DP, THREADS> Map;
+  static constexpr int kPieces = Map::pieces;  // loads of a wave
   uint32_t off[kPieces];
-  static __device__ __forceinline__ int row(int u) {
-    return (threadIdx.x + u * THREADS) / L::chunks;
-  }
-  static __device__ __forceinline__ int col(int u) {
-    return (((threadIdx.x + u * THREADS) % L::chunks) ^ L::turn(row(u))) * L::vec;
-  }
   __device__ __forceinline__ explicit AtLoad(int64_t ld) {
 #pragma unroll
-    for (int u = 0; u < kPieces; ++u)
-      off[u] = (uint32_t)((row(u) * (uint32_t)ld + col(u)) * sizeof(T));
+    for (int u = 0; u < kPieces; ++u) off[u] = Map::whole(threadIdx.x, u, (uint32_t)ld);
   }
   // first: the tile's first row; rows: how many there are from it on (>= 1);
   // tile: its LDS address
@@ -228,7 +201,8 @@ template <typename T, int ROWS, int DP, int THREADS> struct AtLoad {
     } else {
 #pragma unroll
       for (int u = 0; u < kPieces; ++u) {
-        const int r = row(u) < rows ? row(u) : rows - 1, c = col(u);
+        const int row = Map::row(threadIdx.x, u), c = Map::col(threadIdx.x, u);
+        const int r = row < rows ? row : rows - 1;
         const void* from = c < D ? (const void*)(first + r * ld + c) : (const void*)&kAtZeros;
         at_load_lds<16>(from, to + u * THREADS * 16);
       }
