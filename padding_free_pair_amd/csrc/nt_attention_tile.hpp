@@ -134,18 +134,19 @@ template <int BYTES> __device__ __forceinline__ void at_load_lds(const void* fro
   const uint32_t lds = (uint32_t)__builtin_amdgcn_readfirstlane((int)to);
   const uint64_t at = reinterpret_cast<uint64_t>(from);
   if constexpr (BYTES == 16)
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
-                 ::"s"(lds), "v"(at) : "memory");
+    asm volatile("s_nop 4\n\tglobal_load_lds_dwordx4 %1, off" ::"{m0}"(lds), "v"(at) : "memory");
   else
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off"
-                 ::"s"(lds), "v"(at) : "memory");
+    asm volatile("s_nop 4\n\tglobal_load_lds_dword %1, off" ::"{m0}"(lds), "v"(at) : "memory");
 }
-// The same from a uniform base and a lane's distance in bytes.
+// The same from a uniform base and a lane's distance in bytes. The base may have
+// been written by a vector instruction just before (v_readfirstlane, or the return
+// of a register that was put aside in a vector one): five wait states must pass
+// before a load reads it, which the compiler does not see to within assembly.
 __device__ __forceinline__ void at_load_lds16(const char* base, uint32_t lane, uint32_t to) {
   const uint32_t lds = (uint32_t)__builtin_amdgcn_readfirstlane((int)to);
   const uint64_t at = at_uniform(base);
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
-               ::"s"(lds), "v"(lane), "s"(at) : "memory");
+  asm volatile("s_nop 4\n\tglobal_load_lds_dwordx4 %1, %2"
+               ::"{m0}"(lds), "v"(lane), "s"(at) : "memory");
 }
 
 // Waits until all but the last OPS vector memory operations of the wave, and its

@@ -59,3 +59,22 @@ WHOLE = [
 def test_attention_whole_tiles(nt, case):  # noqa: F811
     announce(f"attention, whole tiles {case}")
     _check(nt, case, 51)
+
+
+WIDE_F32 = [
+    # the fp32 kernels above 64 dimensions, whose tile addresses pass through vector registers;
+    # whole tiles and partial ones
+    ([64, 128], None, 2, 2, 96, "none", False, "f32", "split"),
+    ([70, 33], None, 2, 1, 96, "none", True, "f32", "fused"),
+    ([100], None, 4, 2, 88, "none", False, "f32", "split"),
+    ([128, 65], None, 2, 2, 128, "none", True, "f32", "split"),
+    ([90], None, 2, 1, 104, "none", False, "f32", "split"),
+    ([64, 61], None, 2, 2, 96, "plain", False, "f32", "split"),
+    ([3], [200], 2, 1, 96, "masked", True, "f32", "split"),
+]
+
+
+@pytest.mark.parametrize("case", WIDE_F32)
+def test_attention_wide_f32(nt, case):  # noqa: F811
+    announce(f"attention, wide fp32 {case}")
+    _check(nt, case, 52)
