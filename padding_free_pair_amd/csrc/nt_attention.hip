@@ -44,6 +44,16 @@ struct AtArgs {
   float *part_o, *part_ml;
 };
 
+// The base of a row's powers, in powers of two: its running maximum times the
+// scores' unit, rounded. Without a bias the unit carries the scale, the powers are
+// formed from unrounded products less this number, and whatever brings two bases
+// together (a move, the waves' join) takes the difference of the rounded ones:
+// beside scores of 10^5 the unrounded difference is off by up to 2^-7.
+__device__ __forceinline__ float at_base(float most, float unit) {
+#pragma clang fp contract(off)
+  return most * unit;
+}
+
 template <typename T, int DP, int QW, int KW, int NB, bool BIAS, bool CAUSAL>
 __global__ __launch_bounds__(kAtThreads, sizeof(T) == 4 && (DP > 64 || BIAS) ? 1 : 2) void k_attention(
     AtArgs a) {
@@ -234,7 +244,8 @@ __global__ __launch_bounds__(kAtThreads, sizeof(T) == 4 && (DP > 64 || BIAS) ? 1
     if (__any((top - most) * step > 8.0f)) {
       at_rare();
       const float now = fmaxf(most, top);
-      const float keep = now == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f((most - now) * step);
+      const float moved = BIAS ? (most - now) * step : at_base(most, step) - at_base(now, step);
+      const float keep = now == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(moved);
       most = now;
       sum *= keep;
 #pragma unroll
@@ -248,7 +259,7 @@ __global__ __launch_bounds__(kAtThreads, sizeof(T) == 4 && (DP > 64 || BIAS) ? 1
 #pragma unroll
       for (int x = 0; x < 16; ++x) {
         const float p = BIAS ? __builtin_amdgcn_exp2f((s[b][x] - base) * kLog2e)
-                             : __builtin_amdgcn_exp2f(s[b][x] * unit - base * unit);
+                             : __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][x], unit, -at_base(base, unit)));
         s[b][x] = p;
         sum += p;
       }
@@ -283,7 +294,10 @@ __global__ __launch_bounds__(kAtThreads, sizeof(T) == 4 && (DP > 64 || BIAS) ? 1
 #pragma unroll
     for (int w = 1; w < KW; ++w) now = fmaxf(now, join[((w - 1) * QW + qw) * kPart + lane]);
     const float base = now == -INFINITY ? 0.0f : now;
-    float keep = __builtin_amdgcn_exp2f((most - base) * step);
+    auto keep_of = [&](float x) {
+      return __builtin_amdgcn_exp2f(BIAS ? (x - base) * step : at_base(x, step) - at_base(base, step));
+    };
+    float keep = keep_of(most);
     sum *= keep;
 #pragma unroll
     for (int d = 0; d < DT; ++d)
@@ -292,7 +306,7 @@ __global__ __launch_bounds__(kAtThreads, sizeof(T) == 4 && (DP > 64 || BIAS) ? 1
 #pragma unroll
     for (int w = 1; w < KW; ++w) {
       const float* p = join + ((w - 1) * QW + qw) * kPart + lane;
-      keep = __builtin_amdgcn_exp2f((p[0] - base) * step);
+      keep = keep_of(p[0]);
       sum += p[64] * keep;
 #pragma unroll
       for (int d = 0; d < DT; ++d)
@@ -303,19 +317,22 @@ __global__ __launch_bounds__(kAtThreads, sizeof(T) == 4 && (DP > 64 || BIAS) ? 1
   }
   if (!live) return;
   const int64_t at = t * a.H + hq;
+  // what the rounding of its base adds to a row's powers, as a power of two
+  const float added = BIAS || most == -INFINITY ? 0.0f : __builtin_fmaf(most, step, -at_base(most, step));
   if (a.splits > 1) {
+    const float keep = __builtin_amdgcn_exp2f(-added);
     float* po = a.part_o + ((int64_t)split * a.part_rows + at) * a.D;
 #pragma unroll
     for (int d = 0; d < DT; ++d)
 #pragma unroll
       for (int g = 0; g < 4; ++g)
         if (32 * d + 8 * g + 4 * h < a.D)
-          at_store4(po + 32 * d + 8 * g + 4 * h, o[d][4 * g], o[d][4 * g + 1], o[d][4 * g + 2],
-                    o[d][4 * g + 3]);
+          at_store4(po + 32 * d + 8 * g + 4 * h, o[d][4 * g] * keep, o[d][4 * g + 1] * keep,
+                    o[d][4 * g + 2] * keep, o[d][4 * g + 3] * keep);
     if (h == 0) {
       float* ml = a.part_ml + ((int64_t)split * a.part_rows + at) * 2;
-      ml[0] = BIAS ? most : most * scale;
-      ml[1] = sum;
+      ml[0] = most;
+      ml[1] = sum * keep;
     }
     return;
   }
@@ -328,15 +345,16 @@ __global__ __launch_bounds__(kAtThreads, sizeof(T) == 4 && (DP > 64 || BIAS) ? 1
       if (32 * d + 8 * g + 4 * h < a.D)
         at_store4(op + 32 * d + 8 * g + 4 * h, o[d][4 * g] * inv, o[d][4 * g + 1] * inv,
                   o[d][4 * g + 2] * inv, o[d][4 * g + 3] * inv);
-  if (h == 0) a.lse[at] = (BIAS ? most : most * scale) + logf(sum);
+  if (h == 0) a.lse[at] = (BIAS ? most : most * scale) + (logf(sum) - added * kLn2);
 }
 
 // Joins the splits of a row: a wave for each. The lanes first hold the splits'
-// maxima and sums (at most 64), then the dimensions, two each.
+// maxima (of scores that `scale` is still to multiply) and sums (at most 64), then
+// the dimensions, two each.
 template <typename T>
 __global__ __launch_bounds__(256) void k_attention_join(const float* part_o, const float* part_ml,
-                                                        int splits, int64_t rows, int D, T* o,
-                                                        float* lse) {
+                                                        int splits, int64_t rows, int D, float scale,
+                                                        T* o, float* lse) {
   const int lane = threadIdx.x & 63;
   for (int64_t at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); at < rows;
        at += (int64_t)gridDim.x * 4) {
@@ -350,7 +368,7 @@ __global__ __launch_bounds__(256) void k_attention_join(const float* part_o, con
     float top = most;
 #pragma unroll
     for (int x = 1; x < 64; x <<= 1) top = fmaxf(top, __shfl_xor(top, x));
-    const float w = lane < splits ? expf(most - (top == -INFINITY ? 0.0f : top)) : 0.0f;
+    const float w = lane < splits ? expf((most - (top == -INFINITY ? 0.0f : top)) * scale) : 0.0f;
     sum *= w;
 #pragma unroll
     for (int x = 1; x < 64; x <<= 1) sum += __shfl_xor(sum, x);
@@ -377,7 +395,7 @@ __global__ __launch_bounds__(256) void k_attention_join(const float* part_o, con
 #pragma unroll
     for (int e = 0; e < 2; ++e)
       if (lane + 64 * e < D) o[at * D + lane + 64 * e] = from_f32<T>(acc[e] * inv);
-    if (lane == 0) lse[at] = top + logf(sum);
+    if (lane == 0) lse[at] = top * scale + logf(sum);
   }
 }
 
@@ -448,7 +466,8 @@ hipError_t forward(const nt_partition& p, const nt_attention& a, const AtArgs& x
   if (e != hipSuccess || x.splits == 1) return e;
   const int64_t rows = p.T * a.heads, blocks = (rows + 3) / 4;
   k_attention_join<T><<<(unsigned)(blocks < (1 << 20) ? blocks : (1 << 20)), 256, 0, stream>>>(
-      x.part_o, x.part_ml, x.splits, rows, a.head_dim, static_cast<T*>(x.o), x.lse);
+      x.part_o, x.part_ml, x.splits, rows, a.head_dim,
+      x.bias || a.scale == 0.0f ? 1.0f : fabsf(a.scale), static_cast<T*>(x.o), x.lse);
   return hipGetLastError();
 }
 

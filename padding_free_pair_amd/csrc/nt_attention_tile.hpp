@@ -18,6 +18,7 @@
 namespace nt {
 
 constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
 
 typedef float f32x8 __attribute__((ext_vector_type(8)));
 typedef short at_i16x4 __attribute__((ext_vector_type(4)));
