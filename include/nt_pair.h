@@ -742,8 +742,11 @@ nt_status nt_attention_backward_workspace_bytes(const nt_partition* p, const nt_
  *   delta = sum_d g_o o,  dS = P (g_o . v - delta),
  *   g_v = P^T g_o, g_q = scale dS k, g_k = scale dS^T q, g_bias = dS,
  * shared key heads summing over their query heads. Masked cells and rows
- * with lse = -inf give zero. With NT_BF16 P and dS are rounded to bf16 before
- * their products. Sums run in a fixed order (no atomics). NT_ERR_OVERFLOW as
+ * with lse = -inf give zero. Where lse is 2^10 or more in magnitude (masks of -1e9
+ * or of the type's lowest value in all of a row's cells, a large offset) an fp32 lse
+ * no longer holds the row's sum: there P = exp(S - max S) / sum exp(S - max S), formed
+ * anew from the fp32 scores, as the forward weighs them. With NT_BF16 P and dS are
+ * rounded to bf16 before their products. Sums run in a fixed order (no atomics). NT_ERR_OVERFLOW as
  * the forward's, and with a bias T_cols of 2^23 or more. The gradients
  * must not overlap the inputs or each other. workspace: device, 16-byte
  * aligned.

@@ -5,7 +5,7 @@
 // repeat bit by bit. The first owns 32 virtual rows (queries of one key head,
 // as in the forward) in a wave and walks over the keys: it forms S^T = K Q^T and
 // dP^T = V G^T, and their dS^T is, as it stands, the fragment of
-// g_q^T += K^T dS^T. It also leaves each row's log sum and delta, prepared and
+// g_q^T += K^T dS^T. It also leaves each row's base (its log sum) and delta, prepared and
 // row by row for each head, to the second (where both go out in one launch a
 // small kernel before it does), which owns 32 keys in a wave and
 // walks over the rows of each query head of the group in turn: S = Q K^T and
@@ -35,7 +35,8 @@ struct AbArgs {
   const void *q, *k, *v, *bias, *o, *g_o;
   const float* lse;
   void *g_q, *g_k, *g_v, *g_bias;
-  float *logs, *delta;  // [H, T]
+  float *base, *share, *delta;  // [H, T]
+  int *sharing;  // [units of 32 virtual rows, K]: whether one of them has a share
 };
 
 // Tiles in flight: two where that leaves room for a second workgroup on the CU.
@@ -52,6 +53,71 @@ __device__ __forceinline__ float ab_dot(const f32x8& a, const f32x8& b) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) s += a[j] * b[j];
   return s;
+}
+
+// A row's probabilities are exp(S - base) share. Its log sum is the base, with a
+// share of 1, as long as half a step of it, which is the relative error of all of
+// the row's probabilities, stays below 2^-14. Beyond that (all of a row's scores
+// near a mask of -1e9 or of the type's lowest value, or a large offset that they
+// have in common) the sum is lost in it: at the lowest value every probability
+// would be 1. There the base is the row's maximum, whose differences to the scores
+// are exact, and the share one over the sum, both found by a walk over the keys of
+// its own, which only waves with such a row take.
+constexpr float kAbLarge = 1024.0f;
+__device__ __forceinline__ bool ab_large(float lse) {
+  return fabsf(lse) >= kAbLarge && fabsf(lse) < INFINITY;
+}
+
+// The base of a row whose share is 1, in powers of two without a bias. A row that
+// saw nothing gives nothing.
+template <bool BIAS> __device__ __forceinline__ float ab_base(float lse) {
+  const float x = lse == -INFINITY ? INFINITY : lse;
+  return BIAS ? x : x * kLog2e;
+}
+
+// The base and share of a wave's 32 rows (queries q, as fragments), each over its
+// first `last` keys, at most `most` of the m at k. bias: the cells of the lane's
+// row. The scores are formed as in the walks.
+template <typename T, int DP, bool BIAS>
+__device__ __forceinline__ void ab_normalise(const AbArgs& a, const typename AtFrag<T>::type* q,
+                                             const T* k, const T* bias, int m, int most, int last,
+                                             float* base, float* share) {
+  typedef typename AtFrag<T>::type Frag;
+  constexpr int KS = DP / 16;
+  const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
+  const float unit = a.scale * kLog2e;
+  float top = -INFINITY, sum = 0.0f;
+  for (int c = 0; c < most; c += 32) {
+    const T* kp = k + (int64_t)(c + l32 < m ? c + l32 : m - 1) * a.ld_k;
+    f32x16 s = {};
+#pragma unroll
+    for (int x = 0; x < KS; ++x) {
+      Frag f = {};
+      if (16 * x + 8 * h < a.D) f = at_row(kp, x, h);
+      s = at_mma(f, q[x], s);
+    }
+    float now = top, v[16];
+#pragma unroll
+    for (int x = 0; x < 16; ++x) {
+      const int key = c + 8 * (x / 4) + 4 * h + x % 4;
+      v[x] = -INFINITY;
+      if (key < last) v[x] = BIAS ? __builtin_fmaf(s[x], a.scale, to_f32(bias[key])) : s[x] * unit;
+      now = fmaxf(now, v[x]);
+    }
+    now = at_halves_max(now);
+    const float zero = now == -INFINITY ? 0.0f : now;
+    sum *= __builtin_amdgcn_exp2f((top - zero) * (BIAS ? kLog2e : 1.0f));
+#pragma unroll
+    for (int x = 0; x < 16; ++x)
+      if (v[x] != -INFINITY)
+        sum += __builtin_amdgcn_exp2f(BIAS ? (v[x] - zero) * kLog2e
+                                           : __builtin_fmaf(s[x], unit, -zero));
+    top = now;
+  }
+  sum += __shfl_xor(sum, 32);
+  const bool none = sum == 0.0f;
+  *base = none ? INFINITY : top;
+  *share = none ? 1.0f : 1.0f / sum;
 }
 
 // g_q of 32 virtual rows a wave, and their statistics. As in the forward, QW
@@ -120,21 +186,36 @@ __device__ __forceinline__ void ab_queries(const AbArgs& a, char* lds_bytes, uin
       if (!READY) delta += ab_dot(g[s], at_row(op, s, h));
     }
   }
-  // a row that saw nothing gives nothing
-  const float given = READY ? a.logs[hq * a.T + t] : a.lse[at];
-  const float lse = given == -INFINITY ? INFINITY : given;
-  const float base = READY ? given : lse * kLog2e;
+  const T* kp = static_cast<const T*>(a.k) + a.mu[i] * a.ld_k + (int64_t)hk * a.D;
+  const T* vp = static_cast<const T*>(a.v) + a.mu[i] * a.ld_v + (int64_t)hk * a.D;
+  float base, share = 1.0f;  // (a row's share enters its g_q at the end)
   if (READY) {
+    base = a.base[hq * a.T + t];
+    share = a.share[hq * a.T + t];
     delta = a.delta[hq * a.T + t];
   } else {
+    base = ab_base<BIAS>(a.lse[at]);
+    const bool large = ab_large(a.lse[at]), any = __any(large);
+    if (lane == 0 && kw == 0 && live)
+      a.sharing[(a.eta[i] * G / 32 + i + tile * QW + qw) * a.K + hk] = any;
+    if (any) {
+      at_rare();
+      float to_base, to_share;
+      ab_normalise<T, DP, BIAS>(
+          a, q, kp, BIAS ? static_cast<const T*>(a.bias) + hq * a.cells + a.cell0[i] + r * m : nullptr,
+          keys, (int)c1, last, &to_base, &to_share);
+      if (large) {
+        base = to_base;
+        share = to_share;
+      }
+    }
     delta += __shfl_xor(delta, 32);
     if (live && h == 0 && kw == 0) {
-      a.logs[hq * a.T + t] = BIAS ? lse : base;
+      a.base[hq * a.T + t] = base;
+      a.share[hq * a.T + t] = share;
       a.delta[hq * a.T + t] = delta;
     }
   }
-  const T* kp = static_cast<const T*>(a.k) + a.mu[i] * a.ld_k + (int64_t)hk * a.D;
-  const T* vp = static_cast<const T*>(a.v) + a.mu[i] * a.ld_v + (int64_t)hk * a.D;
   f32x16 gq[DT];
 #pragma unroll
   for (int d = 0; d < DT; ++d) gq[d] = f32x16{};
@@ -213,7 +294,8 @@ __device__ __forceinline__ void ab_queries(const AbArgs& a, char* lds_bytes, uin
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int x = 4 * y + e;
-          s[b][x] = BIAS ? (s[b][x] * a.scale + z[e] - lse) * kLog2e : s[b][x] * unit - base;
+          s[b][x] = BIAS ? (__builtin_fmaf(s[b][x], a.scale, z[e]) - base) * kLog2e
+                         : __builtin_fmaf(s[b][x], unit, -base);
           s[b][x] = __builtin_amdgcn_exp2f(s[b][x]) * (dp[b][x] - delta);
         }
       }
@@ -259,14 +341,15 @@ __device__ __forceinline__ void ab_queries(const AbArgs& a, char* lds_bytes, uin
     }
   }
   if (!live) return;
+  const float unit_q = a.scale * share;
   T* out = static_cast<T*>(a.g_q) + t * a.ld_gq + (int64_t)hq * a.D;
 #pragma unroll
   for (int d = 0; d < DT; ++d)
 #pragma unroll
     for (int y = 0; y < 4; ++y)
       if (32 * d + 8 * y + 4 * h < a.D)
-        at_store4(out + 32 * d + 8 * y + 4 * h, gq[d][4 * y] * a.scale, gq[d][4 * y + 1] * a.scale,
-                  gq[d][4 * y + 2] * a.scale, gq[d][4 * y + 3] * a.scale);
+        at_store4(out + 32 * d + 8 * y + 4 * h, gq[d][4 * y] * unit_q, gq[d][4 * y + 1] * unit_q,
+                  gq[d][4 * y + 2] * unit_q, gq[d][4 * y + 3] * unit_q);
 }
 
 template <typename T, int DP, int QW, int KW, int NB, bool BIAS>
@@ -290,9 +373,10 @@ template <typename T, int DP, int KW, int RW, int NB, bool BIAS> struct AbK {
   static constexpr int TILE = ROWS * AtTile<T, DP>::pitch, kPair = 2 * TILE * (int)sizeof(T);
   static constexpr int AHEAD = BIAS ? 1 : ab_ahead(kPair), BUFS = AHEAD + 1;
   static constexpr int kTiles = BUFS * kPair, kJoin = (RW - 1) * KW * 2 * DP * 32 * 4;
-  // the rows' statistics, then the bias tiles
+  // the rows' bases and deltas, the shares of those that have one, then the bias tiles
   static constexpr int kStats = kTiles > kJoin ? kTiles : kJoin;
-  static constexpr int kBias = kStats + BUFS * KW * RW * 2 * 32 * NB * 4;
+  static constexpr int kShares = kStats + BUFS * KW * RW * 2 * 32 * NB * 4;
+  static constexpr int kBias = kShares + KW * RW * 32 * 4;
   static constexpr int kLds = kBias + (BIAS ? BUFS * ROWS * KEYS * (int)sizeof(T) : 0);
   static constexpr int kWaves = DP > 64 || (BIAS && (sizeof(T) == 4 || (RW == 4 && DP > 32))) ? 1 : 2;
 };
@@ -305,9 +389,11 @@ __device__ __forceinline__ void ab_keys(const AbArgs& a, char* lds_bytes, uint32
   constexpr int TILE = P::TILE, kPair = P::kPair, AHEAD = P::AHEAD, BUFS = P::BUFS;
   constexpr int BEHIND = (AHEAD - 1) * (2 * Load::kPieces + NB);  // the next tile's loads
   typedef AtBiasTile<T, ROWS, KEYS, THREADS> Bias;
-  // each wave's own rows: log sums, then deltas
+  // each wave's own rows: bases, then deltas
   typedef float Stats[KW * RW][2][32 * NB];
   Stats* stats = reinterpret_cast<Stats*>(lds_bytes + P::kStats);
+  typedef float Shares[32];
+  Shares* shares = reinterpret_cast<Shares*>(lds_bytes + P::kShares);
   T* lds_bias = reinterpret_cast<T*>(lds_bytes + P::kBias);
   const T* lds = reinterpret_cast<const T*>(lds_bytes);
   const uint32_t lds_at = at_lds(lds_bytes);
@@ -341,6 +427,12 @@ __device__ __forceinline__ void ab_keys(const AbArgs& a, char* lds_bytes, uint32
 #pragma unroll
   for (int d = 0; d < DT; ++d) gk[d] = gv[d] = f32x16{};
   const float unit = a.scale * kLog2e;
+  // Whether a row of the walk has a share, known before the walk. (Found from each
+  // tile's bases: causal 4096 .. 300 238 us against 235; without shares 230.)
+  bool sharing = false;
+  const int64_t units = a.eta[i] * G / 32 + i, unit_end = units + (n * G + 31) / 32;
+  for (int64_t x = units + lane; x < unit_end; x += 64) sharing |= a.sharing[x * a.K + hk] != 0;
+  sharing = __any(sharing);
 
   // Rows from the first that sees a key of this workgroup, for each query head
   // in turn; the cells of the bias's gradient before it are zero.
@@ -368,7 +460,7 @@ __device__ __forceinline__ void ab_keys(const AbArgs& a, char* lds_bytes, uint32
                  a.D, lds_at + to * kPair);
     load_g.start(static_cast<const T*>(a.g_o) + (t0 * a.H + load_h) * a.D, (int64_t)a.H * a.D,
                  left, a.D, lds_at + to * kPair + kPair / 2);
-    const float* p = a.logs + load_h * a.T + t0;
+    const float* p = a.base + load_h * a.T + t0;
     const float* d = a.delta + load_h * a.T + t0;
     const uint32_t stats_to = stats_at + (to * KW * RW + wave) * 2 * 32 * NB * 4;
     if (NB == 1) {  // a half of the wave each
@@ -457,8 +549,8 @@ __device__ __forceinline__ void ab_keys(const AbArgs& a, char* lds_bytes, uint32
         for (int e = 0; e < 4; ++e) {
           const int x = 4 * y + e;
           const float p = __builtin_amdgcn_exp2f(
-              BIAS ? (s[u][x] * a.scale + to_f32((T)cell[x / 8][x % 8]) - z[e]) * kLog2e
-                   : s[u][x] * unit - z[e]);
+              BIAS ? (__builtin_fmaf(s[u][x], a.scale, to_f32((T)cell[x / 8][x % 8])) - z[e]) * kLog2e
+                   : __builtin_fmaf(s[u][x], unit, -z[e]));
           s[u][x] = p;
           dp[u][x] = p * (dp[u][x] - d[e]);
         }
@@ -466,8 +558,26 @@ __device__ __forceinline__ void ab_keys(const AbArgs& a, char* lds_bytes, uint32
     }
     // rows of this tile from this wave's first on, and the first that sees its keys
     const int left = rows - r0 - mine;
-    if (left < 32 * NB || (a.causal && k0 + 31 > r0 + mine + ahead)) {
+    if (sharing || left < 32 * NB || (a.causal && k0 + 31 > r0 + mine + ahead)) {
       at_rare();
+      if (sharing) {
+#pragma unroll
+        for (int u = 0; u < NB; ++u) {
+          const int r = r0 + mine + 32 * u + l32;
+          shares[wave][l32] = a.share[hq * a.T + a.eta[i] + (r < rows ? r : rows - 1)];
+          __builtin_amdgcn_wave_barrier();  // (the wave's own rows: no other wave writes here)
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const f32x4 f = *reinterpret_cast<const f32x4*>(&shares[wave][8 * y + 4 * h]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              s[u][4 * y + e] *= f[e];
+              dp[u][4 * y + e] *= f[e];
+            }
+          }
+          __builtin_amdgcn_wave_barrier();
+        }
+      }
       const int past = a.causal ? (int)(key - ahead) - r0 - mine - 4 * h : 0;
       const int end = left - 4 * h;
 #pragma unroll
@@ -577,10 +687,53 @@ __global__ __launch_bounds__(256, (AbK<T, DP, 2, 2, 1, BIAS>::kWaves)) void k_at
   else ab_queries<T, DP, 2, 2, 1, BIAS, true>(a, lds, blockIdx.x - key_blocks);
 }
 
-// The log sum and delta = o . g_o of every row and head: 8 dimensions a lane,
-// the next power of two of D / 8 lanes a group.
-template <typename T>
-__global__ __launch_bounds__(256) void k_attention_bwd_rows(AbArgs a, int lanes, bool with_bias) {
+// The statistics of rows whose log sum is large, 32 virtual rows a wave, and which
+// waves' rows hold one.
+template <typename T, int DP, bool BIAS>
+__device__ __forceinline__ void ab_large_rows(const AbArgs& a, uint32_t block) {
+  constexpr int KS = DP / 16, ROWS = 128;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l32 = lane & 31, h = lane >> 5;
+  const int hk = block % a.K, G = a.H / a.K;
+  const int64_t slot = block / a.K;
+  const int i = at_sample_of(a.eta, a.B, G, ROWS, slot);
+  const int64_t first = (slot - (a.eta[i] * G / ROWS + i)) * ROWS + 32 * wave;
+  const int64_t n = a.rows[i], m = a.cols[i];
+  if (first >= n * G) return;
+  const bool live = first + l32 < n * G;
+  const int64_t vr = live ? first + l32 : n * G - 1, r = vr / G, t = a.eta[i] + r;
+  const int hq = hk * G + (int)(vr % G);
+  const bool large = live && ab_large(a.lse[t * a.H + hq]), any = __any(large);
+  if (lane == 0) a.sharing[(a.eta[i] * G / 32 + i + first / 32) * a.K + hk] = any;
+  if (!any) return;
+  // the keys of this row, and of the wave's last one
+  const int64_t last_r = (first + 31 < n * G ? first + 31 : n * G - 1) / G;
+  int64_t seen = a.causal ? r + 1 + m - n : m, most = a.causal ? last_r + 1 + m - n : m;
+  seen = seen < 0 ? 0 : seen < m ? seen : m;
+  most = most < 0 ? 0 : most < m ? most : m;
+  typename AtFrag<T>::type q[KS];
+  const T* qp = static_cast<const T*>(a.q) + t * a.ld_q + (int64_t)hq * a.D;
+#pragma unroll
+  for (int s = 0; s < KS; ++s) {
+    q[s] = typename AtFrag<T>::type{};
+    if (16 * s + 8 * h < a.D) q[s] = at_row(qp, s, h);
+  }
+  float base, share;
+  ab_normalise<T, DP, BIAS>(
+      a, q, static_cast<const T*>(a.k) + a.mu[i] * a.ld_k + (int64_t)hk * a.D,
+      BIAS ? static_cast<const T*>(a.bias) + hq * a.cells + a.cell0[i] + r * m : nullptr, (int)m,
+      (int)most, (int)seen, &base, &share);
+  if (!large || h) return;
+  a.base[hq * a.T + t] = base;
+  a.share[hq * a.T + t] = share;
+}
+
+// The base, share and delta = o . g_o of every row and head: 8 dimensions a lane,
+// the next power of two of D / 8 lanes a group; behind those workgroups, ones that
+// look for rows with a large log sum, and write their base and share and where
+// they are.
+template <typename T, int DP, bool BIAS>
+__global__ __launch_bounds__(256) void k_attention_bwd_rows(AbArgs a, int lanes, uint32_t blocks) {
+  if (blockIdx.x >= blocks) return ab_large_rows<T, DP, BIAS>(a, blockIdx.x - blocks);
   // a head's rows one after another: the statistics are written as whole lines
   // (T H < 2^29: a grid of 32-row tiles fits)
   const uint32_t per = 256 / lanes, rows = (uint32_t)a.T;
@@ -594,10 +747,11 @@ __global__ __launch_bounds__(256) void k_attention_bwd_rows(AbArgs a, int lanes,
                    at_row(static_cast<const T*>(a.o) + at * a.D + e0, 0, 0));
   for (int x = 1; x < lanes; x <<= 1) delta += __shfl_xor(delta, x);
   if (!live || e0) return;
-  // a row that saw nothing gives nothing
-  const float lse = a.lse[at] == -INFINITY ? INFINITY : a.lse[at];
-  a.logs[to] = with_bias ? lse : lse * kLog2e;
   a.delta[to] = delta;
+  const float lse = a.lse[at];
+  if (ab_large(lse)) return;
+  a.base[to] = ab_base<BIAS>(lse);
+  a.share[to] = 1.0f;
 }
 
 template <typename T, int DP, int QW, int KW, int NB, bool BIAS>
@@ -645,7 +799,9 @@ hipError_t run(const nt_partition& p, AbArgs x, hipStream_t stream) {
       int lanes = 1;
       while (lanes * 8 < x.D) lanes *= 2;
       const int64_t rows = (p.T * x.H * lanes + 255) / 256;
-      k_attention_bwd_rows<T><<<(unsigned)rows, 256, 0, stream>>>(x, lanes, BIAS);
+      const int64_t tiles = at_slots(p.T, p.B, x.H / x.K, 128) * x.K;
+      k_attention_bwd_rows<T, DP, BIAS>
+          <<<(unsigned)(rows + tiles), 256, 0, stream>>>(x, lanes, (uint32_t)rows);
       hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
       x.slots = at_slots(p.T, p.B, x.H / x.K, 64);
@@ -689,7 +845,8 @@ hipError_t backward(const nt_partition& p, const AbArgs& x, hipStream_t stream) 
 }  // namespace
 
 size_t attention_backward_ws_bytes(const nt_partition& p, const nt_attention& a, nt_dtype) {
-  return (size_t)p.T * a.heads * 2 * sizeof(float);
+  const int64_t units = at_slots(p.T, p.B, a.heads / a.kv_heads, 32) * a.kv_heads;
+  return (size_t)p.T * a.heads * 3 * sizeof(float) + (size_t)units * sizeof(int);
 }
 
 hipError_t launch_attention_backward(const nt_partition& p, const nt_attention& a, const void* q,
@@ -729,8 +886,10 @@ hipError_t launch_attention_backward(const nt_partition& p, const nt_attention& 
   x.g_k = g.k;
   x.g_v = g.v;
   x.g_bias = g.bias;
-  x.logs = static_cast<float*>(ws);
-  x.delta = x.logs + p.T * a.heads;
+  x.base = static_cast<float*>(ws);
+  x.share = x.base + p.T * a.heads;
+  x.delta = x.share + p.T * a.heads;
+  x.sharing = reinterpret_cast<int*>(x.delta + p.T * a.heads);
   return dtype == NT_BF16 ? backward<bf16>(p, x, stream) : backward<float>(p, x, stream);
 }
 

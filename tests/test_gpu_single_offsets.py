@@ -138,3 +138,67 @@ def test_large_products(nt, shape, sign, dtype):  # noqa: F811
         e[start:start + len(s), h] = (s.shape[1] + 32 + 8 * np.abs(at)) * U
     z = z + common
     _within("lse", f64(lse, torch), z, e + 4 * U * np.abs(np.where(np.isfinite(z), z, 0.0)))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_masks_and_offsets_of_whole_rows(nt, shape, causal, dtype):  # noqa: F811
+    """Every fifth row: all cells at the lowest value; at -2^30 (a score below 32
+    vanishes beside it); at an offset of -2^20, or of 2^20, beside which fp32 holds
+    steps of 1/8; nothing at all; then an ordinary row."""
+    rows, cols, H, K, D = shape
+    announce(f"attention offsets {shape} {causal} {dtype}"[:200])
+    rng = np.random.default_rng(61)
+    c = cols or rows
+    T, Tc, cells = sum(rows), sum(c), sum(n * m for n, m in zip(rows, c))
+    lowest = float(torch.finfo(getattr(torch, DT[dtype])).min)
+    kinds = [lowest, -2.0 ** 30, -2.0 ** 20, 2.0 ** 20, -math.inf, 0.0]
+    (q, q64), (k, k64) = (_dev(rng.integers(-1, 2, size=s), dtype) for s in ((T, H, D), (Tc, K, D)))
+    (v, v64), (g, g64) = (_dev(rng.normal(size=s), dtype) for s in ((Tc, K, D), (T, H, D)))
+    b = np.zeros((H, cells))
+    small = {}
+    for r, cc, x, n, m, h, kh in _walk(rows, c, H, K):
+        if not n or not m:
+            continue
+        s = SCALE * q64[r, h] @ k64[cc, kh].T
+        at = np.array([kinds[(i + h) % 6] for i in range(n)])
+        b[h, x] = np.repeat(at, m)
+        s = np.where((np.abs(at) > 2.0 ** 25)[:, None], 0.0, s)  # all of them one value
+        s = np.where(np.isneginf(at)[:, None], -np.inf, s)
+        if causal:
+            s = np.where(np.arange(m)[None] > np.arange(n)[:, None] + m - n, -np.inf, s)
+        small[r.start, h] = s
+    bias, _ = _dev(b, dtype)
+    p = _part(nt, rows, cols)
+    o, lse = nt.nt_single_attention(p, q, k, v, bias=bias, causal=causal, scale=SCALE)
+    need = nt.nt_attention_backward_workspace_bytes(p, H, K, D, q.dtype, causal)
+    ws = torch.full((need // 4,), float("nan"), device="cuda")
+    call = lambda: nt.nt_single_attention_backward(  # noqa: E731
+        p, q, k, v, o, lse, g, bias=bias, causal=causal, scale=SCALE, workspace=ws)
+    got, again = call(), call()
+    torch.cuda.synchronize()
+    val, low = _reference(rows, c, small, q64, k64, v64, g64, SCALE, dtype)
+    for name, x, r, e in zip(("o", "g_q", "g_k", "g_v", "g_bias"), (o,) + got, val, low):
+        _within(name, f64(x, torch), r, e)
+    for x, y in zip(got, again):
+        np.testing.assert_array_equal(bits(x, torch), bits(y, torch))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_large_products_gradient(nt, shape, sign, dtype):  # noqa: F811
+    rows, cols, H, K, D = shape
+    announce(f"attention gradient, large products {shape} {sign} {dtype}"[:200])
+    rng = np.random.default_rng(63)
+    c = cols or rows
+    q, q64, k, k64, small, _ = _large_products(rng, rows, cols, H, K, D, dtype, sign)
+    (v, v64), (g, g64) = (_dev(rng.normal(size=s), dtype) for s in ((sum(c), K, D), (sum(rows), H, D)))
+    p = _part(nt, rows, cols)
+    o, lse = nt.nt_single_attention(p, q, k, v, causal=True, scale=SCALE)
+    got = nt.nt_single_attention_backward(p, q, k, v, o, lse, g, causal=True, scale=SCALE)
+    torch.cuda.synchronize()
+    val, low = _reference(rows, c, small, q64, k64, v64, g64, SCALE, dtype)
+    for name, x, r, e in zip(("o", "g_q", "g_k", "g_v"), (o,) + got, val, low):
+        _within(name, f64(x, torch), r, e)
