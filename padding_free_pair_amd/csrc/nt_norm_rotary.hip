@@ -218,7 +218,9 @@ __global__ __launch_bounds__(kNrThreads) void k_norm_rotary(NrSide<T> q, NrSide<
 #pragma unroll
         for (int i = 0; i < kNrVec; ++i) {
           v[i] = to_f32(now[u].own[i]) * r * w[i] * c[i];
-          if (R) v[i] += now[u].partner(i) * r * wp[i] * s[i];
+          // (a select, not a product with zero: an infinity behind the rotated part stays one)
+          const float turned = v[i] + now[u].partner(i) * r * wp[i] * s[i];
+          v[i] = ec + i < R ? turned : v[i];
         }
         if (live && h + u < h1) nr_store<T>(y + (h + u) * D + e0, v);
       }
@@ -291,7 +293,8 @@ __global__ __launch_bounds__(kNrThreads) void k_norm_rotary_bwd(NrSide<T> q, NrS
 #pragma unroll
         for (int i = 0; i < kNrVec; ++i) {
           d[i] = to_f32(gc[u].own[i]) * c[i];
-          if (R) d[i] -= gc[u].partner(i) * s[i];
+          const float turned = d[i] - gc[u].partner(i) * s[i];
+          d[i] = ec + i < R ? turned : d[i];
         }
         if (a.w) {
           float sum = 0.0f, dot = 0.0f, v[kNrVec];
