@@ -791,7 +791,8 @@ typedef struct nt_adamw {
  * else the parameter. Everything is fp32 between reading and writing. With
  * 8-bit states m and sqrt(v) are kept as e4m3 codes (OCP: 448 the largest)
  * times a scale for each NT_ADAMW_BLOCK elements, the block's largest
- * magnitude over 448; a positive sqrt(v) keeps at least the least code, so
+ * magnitude times the fp32 number next to 1/448 (the quotient by 448, or the number
+ * beside it); a positive sqrt(v) keeps at least the least code, so
  * that no step divides by a moment rounded away. The step itself uses m and
  * v before that rounding. A state that is not finite is stored as the NaN
  * code and left out of its block's scale. With step_device and lr_device a

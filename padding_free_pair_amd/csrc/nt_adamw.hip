@@ -102,7 +102,9 @@ __device__ __forceinline__ float aw_wave_max(float v) {
   return v;
 }
 
-// The codes of a wave's 256 values and their scale. Values that are not
+// The codes of a wave's 256 values and their scale, which is their largest
+// magnitude times the rounded 1/448, not the rounded quotient (part of the format:
+// a state is read back with the scale that it was written with). Values that are not
 // finite get the NaN code and do not enter the scale.
 __device__ __forceinline__ uint32_t aw_codes(const float* f, bool positive, float* scale) {
   float top = 0.0f;
