@@ -40,7 +40,7 @@ struct AdamwArgs {
 struct AdamwNumbers {
   float lr, beta1, rest1, beta2, rest2, eps, decay;
   float c1, c2;          // 1 / (1 - beta^step)
-  double b1, b2, lr64, wd64;
+  double b1, b2, wd64;
   const int64_t* step_device;
   const float* lr_device;
 };
@@ -213,7 +213,6 @@ hipError_t launch_adamw(const nt_adamw_tensor* tensors, int32_t count, const nt_
   x.c2 = (float)(1.0 / (1.0 - pow(h.beta2, (double)h.step)));
   x.b1 = h.beta1;
   x.b2 = h.beta2;
-  x.lr64 = h.lr;
   x.wd64 = h.weight_decay;
   x.step_device = h.step_device;
   x.lr_device = h.lr_device;

@@ -250,8 +250,8 @@ __device__ __forceinline__ float at_halves_max(float x) {
 // bytes a thread and piece, consecutive threads along a row, so a row of the
 // tile is read as whole lines, where lanes that read their own scores' cells
 // touch 32 rows each time. In LDS it is an AtTile, read along or across rows.
-// Rows past the last one read the last one; cells past a row's end are left as
-// they are (their scores are masked).
+// Rows past the last one read the last one; cells past a row's end read zeros (and
+// their scores are masked).
 template <typename T, int ROWS, int COLS, int THREADS> struct AtBiasTile {
   typedef AtTile<T, COLS> L;
   typedef T Vec __attribute__((ext_vector_type(16 / sizeof(T))));
