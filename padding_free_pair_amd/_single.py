@@ -72,6 +72,8 @@ def _on(torch, device, stream):
         return _Guard(torch, device, None)
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=device)
+    elif stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
     return _Guard(torch, device, stream)
 
 
