@@ -62,7 +62,8 @@ __device__ __forceinline__ float ab_dot(const f32x8& a, const f32x8& b) {
 // have in common) the sum is lost in it: at the lowest value every probability
 // would be 1. There the base is the row's maximum, whose differences to the scores
 // are exact, and the share one over the sum, both found by a walk over the keys of
-// its own, which only waves with such a row take.
+// its own, which only waves with such a row take. The search for such rows costs the
+// others 0.5 us of 50 (lengths 1024 .. 96, bias) to 4 of 230 (causal 4096 .. 300).
 constexpr float kAbLarge = 1024.0f;
 __device__ __forceinline__ bool ab_large(float lse) {
   return fabsf(lse) >= kAbLarge && fabsf(lse) < INFINITY;
@@ -75,46 +76,84 @@ template <bool BIAS> __device__ __forceinline__ float ab_base(float lse) {
   return BIAS ? x : x * kLog2e;
 }
 
-// The base and share of a wave's 32 rows (queries q, as fragments), each over its
-// first `last` keys, at most `most` of the m at k. bias: the cells of the lane's
-// row. The scores are formed as in the walks.
+// The maximum of a wave's 32 rows' scores (queries q, as fragments) and the sum of
+// their powers, each lane over the keys of its half: of the row's first `last`, at
+// most `most` of the m at k, the pieces of keys that begin at from, from +
+// step, ... bias: the cells of the lane's row. The scores are formed as in the
+// walks; a piece's loads are on their way together (pieces twice as long leave the
+// small kernel before the joint walks fewer waves: 15 us instead of 13, causal 4096 ..
+// 300). Lengths 1024, 768, 384, 96 with one row of lowest-value masks each: 65 us
+// instead of 51; with nothing else 98.
+template <typename T, int DP> struct AbNormalise {
+  static constexpr int blocks = sizeof(T) == 2 && DP <= 64 ? 2 : 1, keys = 32 * blocks;
+};
 template <typename T, int DP, bool BIAS>
 __device__ __forceinline__ void ab_normalise(const AbArgs& a, const typename AtFrag<T>::type* q,
                                              const T* k, const T* bias, int m, int most, int last,
-                                             float* base, float* share) {
+                                             int from, int step, float* to_top, float* to_sum) {
   typedef typename AtFrag<T>::type Frag;
+  typedef T Cells __attribute__((ext_vector_type(4)));
+  typedef AbNormalise<T, DP> P;
   constexpr int KS = DP / 16;
   const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
   const float unit = a.scale * kLog2e;
   float top = -INFINITY, sum = 0.0f;
-  for (int c = 0; c < most; c += 32) {
-    const T* kp = k + (int64_t)(c + l32 < m ? c + l32 : m - 1) * a.ld_k;
-    f32x16 s = {};
+  for (int c = from; c < most; c += step) {
+    Frag f[P::blocks][KS];
+    Cells z[P::blocks][4];
 #pragma unroll
-    for (int x = 0; x < KS; ++x) {
-      Frag f = {};
-      if (16 * x + 8 * h < a.D) f = at_row(kp, x, h);
-      s = at_mma(f, q[x], s);
+    for (int b = 0; b < P::blocks; ++b) {
+      const int row = c + 32 * b + l32;
+      const T* kp = k + (int64_t)(row < m ? row : m - 1) * a.ld_k;
+#pragma unroll
+      for (int x = 0; x < KS; ++x) {
+        f[b][x] = Frag{};
+        if (16 * x + 8 * h < a.D) f[b][x] = at_row(kp, x, h);
+      }
+      if (BIAS) {
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const int key = c + 32 * b + 8 * y + 4 * h;
+          z[b][y] = Cells{};
+          if (key + 4 <= m) {
+            __builtin_memcpy(&z[b][y], bias + key, sizeof(Cells));
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (key + e < m) z[b][y][e] = bias[key + e];
+          }
+        }
+      }
     }
-    float now = top, v[16];
 #pragma unroll
-    for (int x = 0; x < 16; ++x) {
-      const int key = c + 8 * (x / 4) + 4 * h + x % 4;
-      v[x] = -INFINITY;
-      if (key < last) v[x] = BIAS ? __builtin_fmaf(s[x], a.scale, to_f32(bias[key])) : s[x] * unit;
-      now = fmaxf(now, v[x]);
+    for (int b = 0; b < P::blocks; ++b) {
+      f32x16 s = {};
+#pragma unroll
+      for (int x = 0; x < KS; ++x) s = at_mma(f[b][x], q[x], s);
+      float now = top, v[16];
+#pragma unroll
+      for (int x = 0; x < 16; ++x) {
+        const int key = c + 32 * b + 8 * (x / 4) + 4 * h + x % 4;
+        v[x] = BIAS ? __builtin_fmaf(s[x], a.scale, to_f32((T)z[b][x / 4][x % 4])) : s[x] * unit;
+        if (key >= last) v[x] = -INFINITY;
+        now = fmaxf(now, v[x]);
+      }
+      now = at_halves_max(now);
+      const float zero = now == -INFINITY ? 0.0f : now;
+      sum *= __builtin_amdgcn_exp2f((top - zero) * (BIAS ? kLog2e : 1.0f));
+#pragma unroll
+      for (int x = 0; x < 16; ++x)
+        if (v[x] != -INFINITY)
+          sum += __builtin_amdgcn_exp2f(BIAS ? (v[x] - zero) * kLog2e
+                                             : __builtin_fmaf(s[x], unit, -zero));
+      top = now;
     }
-    now = at_halves_max(now);
-    const float zero = now == -INFINITY ? 0.0f : now;
-    sum *= __builtin_amdgcn_exp2f((top - zero) * (BIAS ? kLog2e : 1.0f));
-#pragma unroll
-    for (int x = 0; x < 16; ++x)
-      if (v[x] != -INFINITY)
-        sum += __builtin_amdgcn_exp2f(BIAS ? (v[x] - zero) * kLog2e
-                                           : __builtin_fmaf(s[x], unit, -zero));
-    top = now;
   }
-  sum += __shfl_xor(sum, 32);
+  *to_top = top;
+  *to_sum = sum;
+}
+// A row's base and share from them (a row without a sum gives nothing).
+__device__ __forceinline__ void ab_base_share(float top, float sum, float* base, float* share) {
   const bool none = sum == 0.0f;
   *base = none ? INFINITY : top;
   *share = none ? 1.0f : 1.0f / sum;
@@ -200,14 +239,12 @@ __device__ __forceinline__ void ab_queries(const AbArgs& a, char* lds_bytes, uin
       a.sharing[(a.eta[i] * G / 32 + i + tile * QW + qw) * a.K + hk] = any;
     if (any) {
       at_rare();
-      float to_base, to_share;
+      float top, sum;
       ab_normalise<T, DP, BIAS>(
           a, q, kp, BIAS ? static_cast<const T*>(a.bias) + hq * a.cells + a.cell0[i] + r * m : nullptr,
-          keys, (int)c1, last, &to_base, &to_share);
-      if (large) {
-        base = to_base;
-        share = to_share;
-      }
+          keys, (int)c1, last, 0, AbNormalise<T, DP>::keys, &top, &sum);
+      sum += __shfl_xor(sum, 32);
+      if (large) ab_base_share(top, sum, &base, &share);
     }
     delta += __shfl_xor(delta, 32);
     if (live && h == 0 && kw == 0) {
@@ -428,7 +465,7 @@ __device__ __forceinline__ void ab_keys(const AbArgs& a, char* lds_bytes, uint32
   for (int d = 0; d < DT; ++d) gk[d] = gv[d] = f32x16{};
   const float unit = a.scale * kLog2e;
   // Whether a row of the walk has a share, known before the walk. (Found from each
-  // tile's bases: causal 4096 .. 300 238 us against 235; without shares 230.)
+  // tile's bases: causal 4096 .. 300 3 us more.)
   bool sharing = false;
   const int64_t units = a.eta[i] * G / 32 + i, unit_end = units + (n * G + 31) / 32;
   for (int64_t x = units + lane; x < unit_end; x += 64) sharing |= a.sharing[x * a.K + hk] != 0;
@@ -687,44 +724,71 @@ __global__ __launch_bounds__(256, (AbK<T, DP, 2, 2, 1, BIAS>::kWaves)) void k_at
   else ab_queries<T, DP, 2, 2, 1, BIAS, true>(a, lds, blockIdx.x - key_blocks);
 }
 
-// The statistics of rows whose log sum is large, 32 virtual rows a wave, and which
-// waves' rows hold one.
+// The statistics of rows whose log sum is large, of 128 virtual rows, and which 32 of
+// them hold one: the four waves look at 32 each, then share the keys of those that do.
 template <typename T, int DP, bool BIAS>
 __device__ __forceinline__ void ab_large_rows(const AbArgs& a, uint32_t block) {
-  constexpr int KS = DP / 16, ROWS = 128;
+  constexpr int KS = DP / 16, ROWS = 128, KEYS = AbNormalise<T, DP>::keys;
+  __shared__ float tops[4][32], sums[4][32];
+  __shared__ int some[4];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l32 = lane & 31, h = lane >> 5;
   const int hk = block % a.K, G = a.H / a.K;
   const int64_t slot = block / a.K;
   const int i = at_sample_of(a.eta, a.B, G, ROWS, slot);
-  const int64_t first = (slot - (a.eta[i] * G / ROWS + i)) * ROWS + 32 * wave;
-  const int64_t n = a.rows[i], m = a.cols[i];
-  if (first >= n * G) return;
-  const bool live = first + l32 < n * G;
-  const int64_t vr = live ? first + l32 : n * G - 1, r = vr / G, t = a.eta[i] + r;
-  const int hq = hk * G + (int)(vr % G);
-  const bool large = live && ab_large(a.lse[t * a.H + hq]), any = __any(large);
-  if (lane == 0) a.sharing[(a.eta[i] * G / 32 + i + first / 32) * a.K + hk] = any;
-  if (!any) return;
-  // the keys of this row, and of the wave's last one
-  const int64_t last_r = (first + 31 < n * G ? first + 31 : n * G - 1) / G;
-  int64_t seen = a.causal ? r + 1 + m - n : m, most = a.causal ? last_r + 1 + m - n : m;
-  seen = seen < 0 ? 0 : seen < m ? seen : m;
-  most = most < 0 ? 0 : most < m ? most : m;
-  typename AtFrag<T>::type q[KS];
-  const T* qp = static_cast<const T*>(a.q) + t * a.ld_q + (int64_t)hq * a.D;
-#pragma unroll
-  for (int s = 0; s < KS; ++s) {
-    q[s] = typename AtFrag<T>::type{};
-    if (16 * s + 8 * h < a.D) q[s] = at_row(qp, s, h);
+  const int64_t tile = (slot - (a.eta[i] * G / ROWS + i)) * ROWS;
+  const int64_t n = a.rows[i], m = a.cols[i], end = n * G;
+  if (tile >= end) return;
+  {
+    const int64_t vr = tile + 32 * wave + l32;
+    const bool any = __any(vr < end && ab_large(a.lse[(a.eta[i] + vr / G) * a.H + hk * G + vr % G]));
+    if (lane == 0) {
+      some[wave] = any;
+      if (vr < end) a.sharing[(a.eta[i] * G / 32 + i + vr / 32) * a.K + hk] = any;
+    }
   }
-  float base, share;
-  ab_normalise<T, DP, BIAS>(
-      a, q, static_cast<const T*>(a.k) + a.mu[i] * a.ld_k + (int64_t)hk * a.D,
-      BIAS ? static_cast<const T*>(a.bias) + hq * a.cells + a.cell0[i] + r * m : nullptr, (int)m,
-      (int)most, (int)seen, &base, &share);
-  if (!large || h) return;
-  a.base[hq * a.T + t] = base;
-  a.share[hq * a.T + t] = share;
+  __syncthreads();
+  for (int w = 0; w < 4; ++w) {
+    if (!some[w]) continue;
+    const int64_t first = tile + 32 * w;
+    const bool live = first + l32 < end;
+    const int64_t vr = live ? first + l32 : end - 1, r = vr / G, t = a.eta[i] + r;
+    const int hq = hk * G + (int)(vr % G);
+    // the keys of this row, and of the last of the 32
+    const int64_t last_r = (first + 31 < end ? first + 31 : end - 1) / G;
+    int64_t seen = a.causal ? r + 1 + m - n : m, most = a.causal ? last_r + 1 + m - n : m;
+    seen = seen < 0 ? 0 : seen < m ? seen : m;
+    most = most < 0 ? 0 : most < m ? most : m;
+    typename AtFrag<T>::type q[KS];
+    const T* qp = static_cast<const T*>(a.q) + t * a.ld_q + (int64_t)hq * a.D;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      q[s] = typename AtFrag<T>::type{};
+      if (16 * s + 8 * h < a.D) q[s] = at_row(qp, s, h);
+    }
+    float top, sum;
+    ab_normalise<T, DP, BIAS>(
+        a, q, static_cast<const T*>(a.k) + a.mu[i] * a.ld_k + (int64_t)hk * a.D,
+        BIAS ? static_cast<const T*>(a.bias) + hq * a.cells + a.cell0[i] + r * m : nullptr, (int)m,
+        (int)most, (int)seen, wave * KEYS, 4 * KEYS, &top, &sum);
+    sum += __shfl_xor(sum, 32);
+    if (h == 0) {
+      tops[wave][l32] = top;
+      sums[wave][l32] = sum;
+    }
+    __syncthreads();
+    if (wave == 0 && h == 0 && live && ab_large(a.lse[t * a.H + hq])) {  // in the waves' order
+      for (int x = 1; x < 4; ++x) top = fmaxf(top, tops[x][l32]);
+      const float zero = top == -INFINITY ? 0.0f : top;
+      sum = 0.0f;
+      for (int x = 0; x < 4; ++x)
+        sum += sums[x][l32] * __builtin_amdgcn_exp2f((tops[x][l32] - zero) * (BIAS ? kLog2e : 1.0f));
+      float base, share;
+      ab_base_share(top, sum, &base, &share);
+      a.base[hq * a.T + t] = base;
+      a.share[hq * a.T + t] = share;
+    }
+    __syncthreads();
+  }
 }
 
 // The base, share and delta = o . g_o of every row and head: 8 dimensions a lane,
