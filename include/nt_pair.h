@@ -679,7 +679,7 @@ nt_status nt_qk_norm_rotary_backward_workspace_bytes(const nt_partition* p,
  *   g_x = r (h w - xhat mean_d(h w xhat))         (w NULL: g_x = h).
  * g_q_in, g_k_in (`dtype`) may be g_q, g_k (contiguous), not q or k. g_w_q,
  * g_w_k: fp32 [D], written when w_q, w_k are given, summed in a fixed order.
- * workspace: device, 16-byte aligned.
+ * workspace: device, 16-byte aligned, of one call at a time.
  */
 nt_status nt_qk_norm_rotary_backward(const nt_partition* p, const nt_norm_rotary* n,
                                      const void* q, const void* k, const void* g_q,
@@ -749,7 +749,7 @@ nt_status nt_attention_backward_workspace_bytes(const nt_partition* p, const nt_
  * rounded to bf16 before their products. Sums run in a fixed order (no atomics). NT_ERR_OVERFLOW as
  * the forward's, and with a bias T_cols of 2^23 or more. The gradients
  * must not overlap the inputs or each other. workspace: device, 16-byte
- * aligned.
+ * aligned, of one call at a time.
  */
 nt_status nt_single_attention_backward(const nt_partition* p, const nt_attention* a,
                                        const void* q, const void* k, const void* v,

@@ -14,9 +14,9 @@
 // keys of each tile, each with its own running maximum, and are joined at the
 // end: few or short samples then still fill the card.
 //
-// Measured: causal lengths 6000, 4097, 1500, 257 (16 heads over 4, D 128) 235 us,
-// 960 TFLOP/s of the 1190 that a large matrix product reaches: the matrix cores,
-// with the exponentials beside them. 16 samples of 231 .. 256 tokens with a bias
+// Measured: causal lengths 6000, 4097, 1500, 257 (16 heads over 4, D 128) 237 us,
+// 950 TFLOP/s of the 1190 that a large matrix product reaches: the matrix cores (53 %
+// of their cycles), with the vector unit's exponentials beside them (48 %). 16 samples of 231 .. 256 tokens with a bias
 // (12 heads, D 32) 17 us: the bias, 23 MB, and the few tiles of a workgroup, whose
 // first loads nothing hides. One token each of 16 samples over 8192 .. 1 keys (32
 // heads over 8, D 128) 46 us, 35 of them this kernel's and 4 the join's: the keys
@@ -404,10 +404,14 @@ __global__ __launch_bounds__(256) void k_attention_join(const float* part_o, con
 struct AtPlan {
   int qw, splits, chunk;
 };
-// Workgroups of 128 rows read each tile of keys half as often as those of 64,
-// where there are 1,024 or more of them: causal lengths 6000 .. 257 (1,496) 299 us
-// against 380; the near-uniform batch (552) 25 against 20. (Both before the tiles
-// were loaded straight into LDS, and with a bias, which now always takes 64.)
+// Without a bias, workgroups of 128 rows read each tile of keys half as often as
+// those of 64, and leave fewer of them: taken where there are 1,024 or more. 64 against
+// 128 rows, bf16: 8 x 1,024 of D 32, 12 heads (864 workgroups of 128) 33 against 37 us,
+// 16 heads (1,152) 47 against 44; 16 x 256 of D 64, 32 heads (1,536) 29 against 25; 8 x
+// 1,024 of D 128, 16 heads (1,152) 103 against 86; causal 6000 .. 257 (D 128, 1,496) 293
+// against 253, causal 2 x 4,096 (D 64, 1,056) 105 against 107. Wide heads would gain
+// from fewer already (4 x 1,024 of D 128, 16 heads, 576 workgroups: 54 against 47), D 64
+// not always (8 x 1,024, 8 heads, 576: 34 against 36).
 //
 // A split costs its partial sums (fp32, written and read) and a second launch,
 // 5 us at least. Where a sample's rows fill half a tile of 64 or less (decoding)
@@ -417,10 +421,14 @@ struct AtPlan {
 // those behind a sample's last key return: one row each of 16 samples of 8,192 ..
 // 1 keys (32 heads over 8, D 128): 44 to 46 us; with 1,024 workgroups 46, 2,048: 50;
 // with four times the mean's parts 48, once 69. 64 such samples: 133 us, unsplit
-// 191; 256: 494. One of 8,192 keys: 20.
-// With more rows only few workgroups over many keys gain: 256 rows over 8,192
-// keys 98 -> 54 us, 128 over 2,000 28 -> 18, but 1,000 over 1,000 (D 32, 12 heads)
-// 12 -> 18, and 4,000 over 4,000 (D 64, 252 workgroups) 37 -> 40.
+// 191; 256: 494. One of 8,192 keys: 20. The mean length decides: 16 of 512 keys take 15
+// us, unsplit 13, of 700 keys 17 and 16; one of 16,384 keys among 63 of 200 is not split
+// (mean 453) and takes 204.
+// With more rows only few workgroups over many keys gain, from about 1,536 keys on: 256
+// rows (D 64, 8 heads) over 1,000 keys 14 us either way, over 1,536 17 -> 15, 2,048 22 ->
+// 16, 8,192 73 -> 21; 500 rows (D 128, 8 heads) over 1,536 24 either way, 3,000 41 -> 27;
+// 1,000 over 1,000 (D 32, 12 heads) would go 12 -> 18. 1,600 over 1,600 (6 heads) loses,
+// 16 -> 19.
 AtPlan plan_of(const nt_partition& p, const nt_attention& a) {
   if (p.T == 0 || p.B == 0) return {4, 1, 0};
   const int G = a.heads / a.kv_heads;

@@ -12,12 +12,13 @@
 // dP = G V^T give P and dS as fragments of g_v^T += G^T P and g_k^T += Q^T dS,
 // and shared key heads sum in registers. The scores and dP are formed twice (7
 // products instead of 5); joining the walks would need g_q summed across
-// workgroups. Both are bound by what a tile costs beside its products (LDS
-// reads, exponentials, conversions): causal lengths 4096, 2500, 1111, 300 (16
-// heads over 8, D 64) 229 us, 64 % of the rate of a large matrix product over
-// the 7 products; lengths 1024, 768, 384, 96 with a bias and its gradient (12
-// heads, D 32) 50 us, where the bias is read twice and its gradient written
-// once (129 MB).
+// workgroups. Causal lengths 4096, 2500, 1111, 300 (16 heads over 8, D 64) 235 us, 62 %
+// of the rate of a large matrix product over the 7 products: of a CU's cycles the
+// matrix cores are busy for 36 %, the vector unit (exponentials, differences,
+// conversions) for 43 %, LDS for 24 % without conflicts, and with two waves a SIMD the
+// first two do not overlap much. Lengths 1024, 768, 384, 96 with a bias and its gradient
+// (12 heads, D 32) 50 us: 60 MB fetched (the bias, 43 MB, comes from memory 1.3 times),
+// 47 written, and the chain of a tile.
 #include <math.h>
 
 #include "nt_attention_tile.hpp"
@@ -844,12 +845,15 @@ hipError_t run_k(const nt_partition& p, AbArgs x, hipStream_t stream) {
 //
 // Up to 3,200 workgroups of both walks go out in one launch (512 where the keys'
 // registers leave one workgroup a CU): neither walk alone fills the card to its
-// end. Against two launches: lengths 1024 .. 96 with a bias 50 us against 51,
-// without 29 against 33, 2,000 rows (D 32, 12 heads, causal) 34 against 48, 1,000 +
-// 500 + 300 (D 64, 12 heads) with a bias 54 against 79, causal 4096 .. 300 (3,064)
-// 228 against 231; 8 x 1,024 with a bias (3,264) 195 against 192, 2,000 rows of D
-// 128 and 16 heads (1,024) 123 against 112. Shared key heads with few keys are
-// better split (2,000 rows, D 64, 16 heads over 4: 91 us, in one launch 124).
+// end. Against two launches: 1,000 + 500 + 300 with a bias (D 64, 12 heads, about 750) 56
+// us against 84, (D 128, 8 heads, 500) 82 against 123; 8 x 512 (D 32, 12 heads, 1,700) 34
+// against 38; 8 x 1,024 with a bias (D 32, 8 heads, 2,176) 136 against 145. Near the limit
+// they are alike (causal 4096 .. 300, 3,064: 251 against 249; 8 x 1,024 of D 32, 12
+// heads, 3,264: 95 against 96), beyond it one launch loses: 8 x 1,024 of D 64, 16
+// heads (4,352) 186 against 181, causal 8,192 (4,128) 601 against 581. D 128: 2,000 rows,
+// 8 heads (512) 110 against 117, 16 heads (1,024) 208 against 185; 8 x 512 with a bias
+// (1,152) 109 against 94. Shared key heads with few keys are better split (2,000 rows,
+// D 64, 16 heads over 4: 91 us, in one launch 124).
 template <typename T, int DP, bool BIAS>
 hipError_t run(const nt_partition& p, AbArgs x, hipStream_t stream) {
   // (two blocks of 32 at a time; a bias or fp32 fragments would not leave it the registers)
