@@ -802,6 +802,122 @@ typedef struct nt_adamw {
 nt_status nt_adamw_step(const nt_adamw_tensor* tensors, int32_t count, const nt_adamw* h,
                         nt_dtype dtype, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Tokens and singles: the embedding that makes singles of tokens, the
+ * singles' norm with the residual's addition, and the cross entropy of singles
+ * over a vocabulary, with their gradients. All work on packed rows [T, C] (the
+ * singles of all samples, in any partition), C a multiple of 8 and at most
+ * 16384. Tokens and targets are int32; they and the fp32 arrays of one number a
+ * token (nll, lse, g_nll, g_lse) need the alignment of their type only, so that
+ * targets may be tokens + 1. T is below 2^31 and a vocabulary V at least 1
+ * and at most 2^26. Gradients of activations have the storage type, those of
+ * weights and tables fp32; with `accumulate` 1 the latter are added to what
+ * the array holds (a table that is both the embedding's and the loss's takes
+ * both gradients). Sums run in a fixed order (no atomics). Written arrays must
+ * not overlap others, except where said.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * out[t] = scale table[tokens[t]]: table [V, C], out [T, C] of `dtype`, rounded
+ * once. A token below zero is absent: its row is zero. A token of V or more gives
+ * NaN.
+ */
+nt_status nt_token_embedding(const void* table, const int32_t* tokens, void* out, int64_t T,
+                             int64_t V, int32_t C, float scale, nt_dtype dtype, void* stream);
+
+/* Workspace bytes nt_token_embedding_backward needs. */
+nt_status nt_token_embedding_backward_workspace_bytes(int64_t T, int64_t V, int32_t C,
+                                                      size_t* bytes);
+
+/*
+ * Gradient of nt_token_embedding for its table:
+ *   g_table[v] (+)= scale sum over the places t with tokens[t] = v of g_out[t].
+ * g_out: [T, C] of `dtype`; g_table: fp32 [V, C], every row written unless
+ * accumulated. Tokens outside of [0, V) add nothing. workspace: device, 16-byte
+ * aligned, of one call at a time.
+ */
+nt_status nt_token_embedding_backward(const int32_t* tokens, const void* g_out, float* g_table,
+                                      int64_t T, int64_t V, int32_t C, float scale,
+                                      int32_t accumulate, nt_dtype dtype, void* workspace,
+                                      size_t workspace_bytes, void* stream);
+
+/*
+ * h = x + residual, rounded to `dtype`, and y = h / sqrt(mean_c h^2 + eps) * w of
+ * the rounded h, with fp32 statistics, rounded once. x, residual, h, y: [rows,
+ * C]; w: fp32 [C]. residual NULL: h is x (its pointer is not read); w NULL: no
+ * weight. h may be x or residual, y may be x or residual where h is not.
+ */
+nt_status nt_residual_norm(const void* x, const void* residual, const float* w, void* h, void* y,
+                           int64_t rows, int32_t C, float eps, nt_dtype dtype, void* stream);
+
+/*
+ * The same with y in 8 bits: codes [rows, C] are e4m3 values (OCP: 448 the
+ * largest) in units of scales, fp32 [rows] for group 0 (a row shares one) or
+ * [rows, C / group] (group: a power of two from 8 to 512 that divides C). A
+ * scale is the largest finite magnitude of its values times the fp32 number next
+ * to 1/448; values that are not finite are NaN codes.
+ */
+nt_status nt_residual_norm_8bit(const void* x, const void* residual, const float* w, void* h,
+                                uint8_t* codes, float* scales, int64_t rows, int32_t C,
+                                int32_t group, float eps, nt_dtype dtype, void* stream);
+
+/* Workspace bytes nt_residual_norm_backward needs (with weights). */
+nt_status nt_residual_norm_backward_workspace_bytes(int64_t rows, int32_t C, size_t* bytes);
+
+/*
+ * Gradient of nt_residual_norm from its h: for g_y = dL/dy and, where h is used
+ * beside y (the next residual), g_h = dL/dh (NULL: none), with r = 1 /
+ * sqrt(mean h^2 + eps) and xhat = h r,
+ *   g = r (g_y w - xhat mean_c(g_y w xhat)) + g_h,   g_w = sum over rows of g_y xhat.
+ * g ([rows, C] of `dtype`) is the gradient of x and of the residual; it may be
+ * g_y or g_h. g_w: fp32 [C], written when w is given. workspace: device, 16-byte
+ * aligned, of one call at a time (not read without w).
+ */
+nt_status nt_residual_norm_backward(const void* h, const void* g_y, const void* g_h,
+                                    const float* w, void* g, float* g_w, int64_t rows, int32_t C,
+                                    float eps, nt_dtype dtype, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+
+/* Workspace bytes nt_token_loss needs: a few numbers for each token and 128
+ * rows of the vocabulary. */
+nt_status nt_token_loss_workspace_bytes(int64_t T, int64_t V, int32_t C, nt_dtype dtype,
+                                        size_t* bytes);
+
+/*
+ * Cross entropy of singles over a vocabulary, for each token:
+ *   z[t, v] = scale x_t . W_v,  lse[t] = log sum_v exp z[t, v],  nll[t] = lse[t] - z[t, target_t].
+ * x: [T, C], W: [V, C] of `dtype`, targets: [T]; nll, lse: fp32 [T]. Logits are
+ * fp32 and are not kept. A token whose target is below zero takes no part: nll
+ * = lse = 0, whatever its row holds. A target of V or more has nll NaN.
+ * NT_ERR_OVERFLOW: more than 2^22 tiles of 128 rows of W x 128 tokens.
+ * workspace: device, 16-byte aligned, of one call at a time.
+ */
+nt_status nt_token_loss(const void* x, const void* W, const int32_t* targets, float* nll,
+                        float* lse, int64_t T, int64_t V, int32_t C, float scale, nt_dtype dtype,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes nt_token_loss_backward needs: the gradients of the logits of
+ * a piece of the vocabulary (at most 512 MiB, or of 256 rows), sums of g_x, a copy of x. */
+nt_status nt_token_loss_backward_workspace_bytes(int64_t T, int64_t V, int32_t C, nt_dtype dtype,
+                                                 size_t* bytes);
+
+/*
+ * Gradients of nt_token_loss for g_nll = dL/dnll and g_lse = dL/dlse (fp32 [T];
+ * g_lse NULL: none) from its inputs and its lse. The logits are formed anew,
+ * piece by piece of the vocabulary:
+ *   d[t, v] = (g_nll[t] + g_lse[t]) exp(z[t, v] - lse[t]) - g_nll[t] [v = target_t],
+ *   g_x = scale d W,   g_W (+)= scale d^T x.
+ * g_x: [T, C] of `dtype`, zero for tokens without a target; g_W: fp32 [V, C].
+ * Either may be NULL. With NT_BF16 g_x takes d rounded to bf16 and g_W takes it
+ * as a pair of bf16, hi + lo (to 2^-17). A target of V or more makes its
+ * gradients NaN. workspace: device, 16-byte aligned, of one call at a time.
+ */
+nt_status nt_token_loss_backward(const void* x, const void* W, const int32_t* targets,
+                                 const float* lse, const float* g_nll, const float* g_lse,
+                                 void* g_x, float* g_W, int64_t T, int64_t V, int32_t C,
+                                 float scale, int32_t accumulate, nt_dtype dtype, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
 /* Thread-local description of the last failure in this thread ("" if none). */
 const char* nt_last_error(void);
 

@@ -38,6 +38,9 @@ single.py holds attention among the singles of a sample (biased by the pair
 state) with its gradients, the norms and rotation of its queries and keys, and
 the AdamW step.
 
+tokens.py holds the embedding of tokens as singles, the singles' norm with the
+residual, and the cross entropy over a vocabulary, with their gradients.
+
 The block's transition is z + relu(z W1^T) W2^T (a two-layer ReLU MLP without
 normalisation, the transition of the measured workloads). The paper's own
 pre-normalised SwiGLU transition (Eq. 1 with h o LN; Appendix A.1, expansion
@@ -69,4 +72,8 @@ from .backward import (  # noqa: F401
 from .single import (  # noqa: F401
     rotary_frequencies, rotary_table, rotation_matrix, positions_of, norm_rotary,
     norm_rotary_backward, attention, attention_backward, adamw, e4m3_values, block_scales,
+)
+from .tokens import (  # noqa: F401
+    embedding, embedding_backward, residual_norm, residual_norm_backward, token_loss, logit_grad,
+    token_loss_backward,
 )

@@ -31,6 +31,12 @@ __all__ = ["NtError", "Partition", "nt_partition_sizes", "nt_make_partition",
            "nt_attention_workspace_bytes", "nt_attention_backward_workspace_bytes",
            "nt_qk_norm_rotary_backward_workspace_bytes",
            "AdamwTensors", "nt_adamw_states", "nt_adamw_tensors", "nt_adamw_step",
+           "nt_token_embedding", "nt_token_embedding_backward",
+           "nt_token_embedding_backward_workspace_bytes", "nt_residual_norm",
+           "nt_residual_norm_8bit", "nt_residual_norm_backward",
+           "nt_residual_norm_backward_workspace_bytes", "nt_token_loss",
+           "nt_token_loss_workspace_bytes", "nt_token_loss_backward",
+           "nt_token_loss_backward_workspace_bytes",
            "nt_last_error", "nt_version",
            "NT_F32", "NT_BF16"]
 
@@ -893,3 +899,10 @@ from ._single import (  # noqa: E402,F401
     nt_attention_backward_workspace_bytes, nt_attention_workspace_bytes, nt_qk_norm_rotary,
     nt_qk_norm_rotary_backward, nt_qk_norm_rotary_backward_workspace_bytes, nt_rotary_table,
     nt_single_attention, nt_single_attention_backward)
+
+# -------------------------------------------------------- tokens and singles
+from ._token import (  # noqa: E402,F401
+    nt_residual_norm, nt_residual_norm_8bit, nt_residual_norm_backward,
+    nt_residual_norm_backward_workspace_bytes, nt_token_embedding, nt_token_embedding_backward,
+    nt_token_embedding_backward_workspace_bytes, nt_token_loss, nt_token_loss_backward,
+    nt_token_loss_backward_workspace_bytes, nt_token_loss_workspace_bytes)

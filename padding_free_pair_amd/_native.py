@@ -30,7 +30,12 @@ EXPORTS = ("nt_partition_sizes", "nt_make_partition", "nt_partition_sizes_rect",
            "nt_rotary_table", "nt_qk_norm_rotary", "nt_qk_norm_rotary_backward_workspace_bytes",
            "nt_qk_norm_rotary_backward", "nt_attention_workspace_bytes", "nt_single_attention",
            "nt_attention_backward_workspace_bytes", "nt_single_attention_backward",
-           "nt_adamw_step", "nt_last_error", "nt_version")
+           "nt_adamw_step", "nt_token_embedding", "nt_token_embedding_backward_workspace_bytes",
+           "nt_token_embedding_backward", "nt_residual_norm", "nt_residual_norm_8bit",
+           "nt_residual_norm_backward_workspace_bytes", "nt_residual_norm_backward",
+           "nt_token_loss_workspace_bytes", "nt_token_loss",
+           "nt_token_loss_backward_workspace_bytes", "nt_token_loss_backward", "nt_last_error",
+           "nt_version")
 
 
 class NtPartition(ctypes.Structure):
@@ -127,6 +132,7 @@ def lib() -> ctypes.CDLL:
     L = ctypes.CDLL(LIB_PATH)
     P = ctypes.POINTER
     i32, i64, sz, vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_void_p
+    f32 = ctypes.c_float
     part = P(NtPartition)
     sig = {
         "nt_partition_sizes": [P(i32), i32, P(i64), P(i64), P(i32), P(sz)],
@@ -185,6 +191,20 @@ def lib() -> ctypes.CDLL:
         "nt_single_attention_backward": [part, P(NtAttention)] + [vp] * 7 +
         [P(NtAttentionGrads), ctypes.c_int, vp, sz, vp],
         "nt_adamw_step": [P(NtAdamwTensor), i32, P(NtAdamw), ctypes.c_int, vp],
+        "nt_token_embedding": [vp, vp, vp, i64, i64, i32, f32, ctypes.c_int, vp],
+        "nt_token_embedding_backward_workspace_bytes": [i64, i64, i32, P(sz)],
+        "nt_token_embedding_backward": [vp, vp, vp, i64, i64, i32, f32, i32, ctypes.c_int, vp, sz,
+                                        vp],
+        "nt_residual_norm": [vp, vp, vp, vp, vp, i64, i32, f32, ctypes.c_int, vp],
+        "nt_residual_norm_8bit": [vp, vp, vp, vp, vp, vp, i64, i32, i32, f32, ctypes.c_int, vp],
+        "nt_residual_norm_backward_workspace_bytes": [i64, i32, P(sz)],
+        "nt_residual_norm_backward": [vp, vp, vp, vp, vp, vp, i64, i32, f32, ctypes.c_int, vp, sz,
+                                      vp],
+        "nt_token_loss_workspace_bytes": [i64, i64, i32, ctypes.c_int, P(sz)],
+        "nt_token_loss": [vp, vp, vp, vp, vp, i64, i64, i32, f32, ctypes.c_int, vp, sz, vp],
+        "nt_token_loss_backward_workspace_bytes": [i64, i64, i32, ctypes.c_int, P(sz)],
+        "nt_token_loss_backward": [vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, i32, f32, i32,
+                                   ctypes.c_int, vp, sz, vp],
     }
     for name, args in sig.items():
         fn = getattr(L, name)

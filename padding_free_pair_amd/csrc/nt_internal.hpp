@@ -283,4 +283,33 @@ constexpr int64_t kAdamwMostElements = int64_t(1) << 35;  // of one tensor (4,09
 hipError_t launch_adamw(const nt_adamw_tensor* tensors, int32_t count, const nt_adamw& h,
                         nt_dtype dtype, hipStream_t stream);
 
+// ---- Tokens and singles (nt_token_embedding.hip, nt_residual_norm.hip,
+// nt_token_loss.hip).
+hipError_t launch_token_embedding(const void* table, const int32_t* tokens, void* out, int64_t T,
+                                  int64_t V, int C, float scale, nt_dtype dtype,
+                                  hipStream_t stream);
+size_t token_embedding_backward_ws_bytes(int64_t T, int64_t V, int C);
+hipError_t launch_token_embedding_backward(const int32_t* tokens, const void* g_out,
+                                           float* g_table, int64_t T, int64_t V, int C,
+                                           float scale, bool accumulate, nt_dtype dtype, void* ws,
+                                           hipStream_t stream);
+// codes given: 8 bits with a scale for each `group` values in y's place.
+hipError_t launch_residual_norm(const void* x, const void* residual, const float* w, void* h,
+                                void* y, uint8_t* codes, float* scales, int64_t rows, int C,
+                                int group, float eps, nt_dtype dtype, hipStream_t stream);
+size_t residual_norm_backward_ws_bytes(int64_t rows, int C);
+hipError_t launch_residual_norm_backward(const void* h, const void* g_y, const void* g_h,
+                                         const float* w, void* g, float* g_w, int64_t rows, int C,
+                                         float eps, nt_dtype dtype, void* ws, hipStream_t stream);
+size_t token_loss_ws_bytes(int64_t tokens, int64_t V, nt_dtype dtype);
+size_t token_loss_backward_ws_bytes(int64_t tokens, int64_t V, int C, nt_dtype dtype);
+hipError_t launch_token_loss(const void* x, const void* W, const int32_t* targets, float* nll,
+                             float* lse, int64_t tokens, int64_t V, int C, float scale,
+                             nt_dtype dtype, void* ws, hipStream_t stream);
+hipError_t launch_token_loss_backward(const void* x, const void* W, const int32_t* targets,
+                                      const float* lse, const float* g_nll, const float* g_lse,
+                                      void* g_x, float* g_W, int64_t tokens, int64_t V, int C,
+                                      float scale, bool accumulate, nt_dtype dtype, void* ws,
+                                      hipStream_t stream);
+
 }  // namespace nt

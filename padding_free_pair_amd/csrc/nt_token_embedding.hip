@@ -1,0 +1,433 @@
+// Embedding of tokens as singles, and its gradient by sorted tokens.
+//
+// Forward: out[t] = scale table[token t], 8 columns a lane; a lookup moves bytes
+// and nothing else. Tokens below zero are absent (zeros), tokens that the table
+// does not hold give NaN.
+//
+// Gradient: g_table[v] = scale sum over the places t of token v of g[t], in the
+// places' order whatever the launch does (no atomics on values). Three kernels:
+// 1. Sort. Each workgroup owns a range of the vocabulary and reads all tokens
+//    (from cache: 4 bytes each): it counts those below its range, which is where
+//    its own go in the sorted order, and lists its own in order, so one launch
+//    sorts without an exchange between workgroups. Its list is then sorted by
+//    token in LDS counters, one set a wave. The rows of absent tokens get
+//    their zeros here.
+// 2. Sums. The sorted places are cut into parts of equal length, so that a token
+//    that is everywhere costs no more than many rare ones. A team of lanes
+//    adds the rows of a part, 8 columns a lane, and writes a token's row at the
+//    end of its run; runs that cross the part's ends go to the workspace.
+// 3. Join. The part where a crossing run begins adds its pieces in order.
+#include <algorithm>
+
+#include "nt_device.hpp"
+#include "nt_internal.hpp"
+
+namespace nt {
+namespace {
+
+constexpr int kTeThreads = 256;
+constexpr int kTeSortThreads = 1024;
+constexpr int kTeSortWaves = kTeSortThreads / 64;
+constexpr int kTeRange = 512;       // most tokens of a workgroup's range
+constexpr int kTeAhead = 8;         // rows in flight
+constexpr int64_t kTeMostGrid = int64_t(1) << 20;
+
+template <typename T> __device__ __forceinline__ void te_load(const T* p, float* f);
+template <> __device__ __forceinline__ void te_load<bf16>(const bf16* p, float* f) {
+  const bf16x8 v = *reinterpret_cast<const bf16x8*>(p);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] = (float)v[i];
+}
+template <> __device__ __forceinline__ void te_load<float>(const float* p, float* f) {
+  const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 4);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[i] = a[i];
+    f[4 + i] = b[i];
+  }
+}
+__device__ __forceinline__ void te_store(bf16* p, const float* f) {
+  bf16x8 v;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = (bf16)f[i];
+  *reinterpret_cast<bf16x8*>(p) = v;
+}
+__device__ __forceinline__ void te_store(float* p, const float* f) {
+  *reinterpret_cast<f32x4*>(p) = f32x4{f[0], f[1], f[2], f[3]};
+  *reinterpret_cast<f32x4*>(p + 4) = f32x4{f[4], f[5], f[6], f[7]};
+}
+
+template <typename T, int LANES>
+__global__ __launch_bounds__(kTeThreads) void k_te_lookup(const T* table, const int32_t* tokens,
+                                                          T* out, int64_t n, int64_t V, int C,
+                                                          float scale) {
+  constexpr int kTeams = kTeThreads / LANES;
+  for (int64_t t = (int64_t)blockIdx.x * kTeams + threadIdx.x / LANES; t < n;
+       t += (int64_t)gridDim.x * kTeams) {
+    const int64_t token = tokens[t];
+    const bool is = token >= 0 && token < V;
+    const float other = token < 0 ? 0.0f : __builtin_nanf("");
+    const T* from = table + (is ? token : 0) * C;
+    for (int c = threadIdx.x % LANES * 8; c < C; c += LANES * 8) {
+      float f[8];
+      te_load(from + c, f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = is ? f[e] * scale : other;
+      te_store(out + t * C + c, f);
+    }
+  }
+}
+
+struct TeSorted {
+  int2* list;       // a range's places and tokens within the range, in order
+  int32_t* place;   // sorted
+  int32_t* token;   // of each sorted place
+  int64_t* count;   // of places that hold a token of the table
+};
+
+__global__ __launch_bounds__(kTeSortThreads) void k_te_sort(const int32_t* tokens, int64_t n,
+                                                            int64_t V, int range, TeSorted s,
+                                                            float* g_table, int C, int zero) {
+  __shared__ int64_t below[kTeSortWaves], inside[kTeSortWaves];
+  __shared__ int32_t counts[kTeSortWaves][kTeRange];
+  __shared__ int32_t sums[kTeSortWaves];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t first = (int64_t)blockIdx.x * range;
+  const uint32_t lo = (uint32_t)first;
+  const uint32_t have = (uint32_t)(V - first < range ? V - first : range);
+  // a wave takes a stretch of the places; absent tokens are large unsigned numbers
+  const int64_t each = ((n + kTeSortWaves - 1) / kTeSortWaves + 63) / 64 * 64;
+  const int64_t begin = std::min<int64_t>(n, wave * each), end = std::min<int64_t>(n, begin + each);
+  int64_t under = 0, mine = 0;
+  for (int64_t i = begin; i < end; i += 512) {
+    uint32_t x[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int64_t at = i + 64 * u + lane;
+      x[u] = at < end ? (uint32_t)tokens[at] : 0xffffffffu;
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      under += __popcll(__ballot(x[u] < lo));
+      mine += __popcll(__ballot(x[u] - lo < have));
+    }
+  }
+  if (lane == 0) {
+    below[wave] = under;
+    inside[wave] = mine;
+  }
+  __syncthreads();
+  int64_t base = 0, total = 0, at = 0;
+  for (int w = 0; w < kTeSortWaves; ++w) {
+    base += below[w];
+    if (w < wave) at += inside[w];
+    total += inside[w];
+  }
+  if (first + range >= V && threadIdx.x == 0) *s.count = base + total;
+  for (int64_t i = begin; mine && i < end; i += 512) {
+    uint32_t x[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int64_t k = i + 64 * u + lane;
+      x[u] = k < end ? (uint32_t)tokens[k] : 0xffffffffu;
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const bool is = x[u] - lo < have;
+      const unsigned long long who = __ballot(is);
+      if (is)
+        s.list[base + at + __popcll(who & ((1ull << lane) - 1))] =
+            make_int2((int)(i + 64 * u + lane), (int)(x[u] - lo));
+      at += __popcll(who);
+    }
+  }
+  for (int k = threadIdx.x; k < kTeSortWaves * kTeRange; k += kTeSortThreads) (&counts[0][0])[k] = 0;
+  __syncthreads();
+  // how often each wave's stretch of the list holds each token
+  const int64_t part = (total + kTeSortWaves - 1) / kTeSortWaves;
+  const int64_t l0 = std::min<int64_t>(total, wave * part), l1 = std::min<int64_t>(total, l0 + part);
+  for (int64_t i = l0 + lane; i < l1; i += 64) atomicAdd(&counts[wave][s.list[base + i].y], 1);
+  __syncthreads();
+  // the first place of each token and wave: a token a thread, then over the tokens
+  int all = 0;
+  if (threadIdx.x < kTeRange)
+    for (int w = 0; w < kTeSortWaves; ++w) all += counts[w][threadIdx.x];
+  int before = all;
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) {
+    const int y = __shfl_up(before, m);
+    if (lane >= m) before += y;
+  }
+  if (lane == 63) sums[wave] = before;
+  __syncthreads();
+  before -= all;
+  for (int w = 0; w < wave; ++w) before += sums[w];
+  if (threadIdx.x < kTeRange)
+    for (int w = 0; w < kTeSortWaves; ++w) {
+      const int x = counts[w][threadIdx.x];
+      counts[w][threadIdx.x] = before;
+      before += x;
+    }
+  // rows of the table that no place holds
+  if (zero) {
+    __shared__ uint8_t held[kTeRange];
+    if (threadIdx.x < kTeRange) held[threadIdx.x] = all != 0;
+    __syncthreads();
+    const int quads = C / 4;
+    for (uint32_t v = wave; v < have; v += kTeSortWaves)
+      if (!held[v])
+        for (int c = lane; c < quads; c += 64)
+          *reinterpret_cast<f32x4*>(g_table + (first + v) * C + 4 * c) =
+              f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  } else {
+    __syncthreads();
+  }
+  // places of equal tokens keep their order: the wave's next place of the token,
+  // and behind it one for each earlier lane with the same token
+  for (int64_t i = l0; i < l1; i += 64) {
+    const bool is = i + lane < l1;
+    const int2 x = is ? s.list[base + i + lane] : make_int2(0, 0);
+    unsigned long long same = __ballot(is);
+#pragma unroll
+    for (int b = 0; b < 9; ++b) {
+      const unsigned long long one = __ballot(x.y >> b & 1);
+      same &= x.y >> b & 1 ? one : ~one;
+    }
+    if (is) {
+      const int rank = __popcll(same & ((1ull << lane) - 1));
+      const int to = counts[wave][x.y] + rank;
+      s.place[base + to] = x.x;
+      s.token[base + to] = x.y + (int)lo;
+    }
+    __builtin_amdgcn_wave_barrier();
+    if (is && same >> lane == 1) counts[wave][x.y] += __popcll(same);
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+template <typename T> struct TeSums {
+  const T* g;
+  float* g_table;
+  float* pieces;          // [2 parts][C]: of the run that a part begins with, and ends with
+  const int32_t* place;
+  const int32_t* token;
+  const int64_t* count;
+  int64_t parts;
+  int part, C, accumulate;
+  float scale;
+};
+
+template <typename T>
+__device__ __forceinline__ void te_row(const TeSums<T>& p, int64_t token, int c, float* f) {
+  float* to = p.g_table + token * p.C + c;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) f[e] *= p.scale;
+  if (p.accumulate) {
+    float old[8];
+    te_load<float>(to, old);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] += old[e];
+  }
+  te_store(to, f);
+}
+
+template <typename T, int LANES>
+__global__ __launch_bounds__(kTeThreads) void k_te_sums(TeSums<T> p) {
+  const int64_t k = (int64_t)blockIdx.x * (kTeThreads / LANES) + threadIdx.x / LANES;
+  const int c = (int)(blockIdx.y * LANES + threadIdx.x % LANES) * 8;
+  const int64_t n = *p.count, begin = k * p.part;
+  if (k >= p.parts || begin >= n || c >= p.C) return;
+  const int64_t end = begin + p.part < n ? begin + p.part : n;
+  const int before = begin ? p.token[begin - 1] : -1, after = end < n ? p.token[end] : -1;
+  float sum[8] = {};
+  int now = p.token[begin];
+  bool first = true;  // the run that the part begins with
+  for (int64_t i = begin; i < end; i += kTeAhead) {
+    float f[kTeAhead][8];
+    int token[kTeAhead];
+#pragma unroll
+    for (int u = 0; u < kTeAhead; ++u) {
+      const int64_t at = i + u < end ? i + u : end - 1;
+      token[u] = p.token[at];
+      te_load<T>(p.g + (int64_t)p.place[at] * p.C + c, f[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < kTeAhead; ++u) {
+      if (i + u >= end) break;
+      if (token[u] != now) {
+        if (first && now == before)
+          te_store(p.pieces + 2 * k * p.C + c, sum);
+        else
+          te_row(p, now, c, sum);
+        first = false;
+        now = token[u];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[e] = 0.0f;
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum[e] += f[u][e];
+    }
+  }
+  if (first && now == before)
+    te_store(p.pieces + 2 * k * p.C + c, sum);
+  else if (now == after)
+    te_store(p.pieces + (2 * k + 1) * p.C + c, sum);
+  else
+    te_row(p, now, c, sum);
+}
+
+// A workgroup for each part: where a run begins in it and goes on behind it, the
+// run's pieces are added, a stretch of them a team, then the teams' sums.
+template <typename T, int LANES>
+__global__ __launch_bounds__(kTeThreads) void k_te_join(TeSums<T> p) {
+  constexpr int kTeams = kTeThreads / LANES;
+  __shared__ float all[kTeams][LANES * 8];
+  const int64_t k = blockIdx.x, n = *p.count, begin = k * p.part, end = begin + p.part;
+  if (end >= n) return;
+  const int now = p.token[end - 1];
+  if (p.token[end] != now || (begin && p.token[begin - 1] == now)) return;
+  int64_t lo = end, hi = n;  // the run's end: the first place in (end, n] of another token
+  while (lo < hi) {
+    const int64_t mid = (lo + hi) / 2;
+    if (p.token[mid] == now) lo = mid + 1; else hi = mid;
+  }
+  const int64_t last = (lo - 1) / p.part, pieces = last - k + 1;
+  const int team = threadIdx.x / LANES, c = (int)(blockIdx.y * LANES + threadIdx.x % LANES) * 8;
+  const int64_t each = (pieces + kTeams - 1) / kTeams;
+  const int64_t from = k + team * each, to = from + each < last + 1 ? from + each : last + 1;
+  float sum[8] = {};
+  if (c < p.C)
+    for (int64_t i = from; i < to; i += kTeAhead) {
+      float f[kTeAhead][8];
+#pragma unroll
+      for (int u = 0; u < kTeAhead; ++u) {
+        const int64_t at = i + u < to ? i + u : to - 1;
+        te_load<float>(p.pieces + (2 * at + (at == k)) * p.C + c, f[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < kTeAhead; ++u)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[e] += i + u < to ? f[u][e] : 0.0f;
+    }
+  te_store(&all[team][threadIdx.x % LANES * 8], sum);
+  __syncthreads();
+  if (team || c >= p.C) return;
+  for (int w = 1; w < kTeams; ++w)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum[e] += all[w][threadIdx.x % LANES * 8 + e];
+  te_row(p, now, c, sum);
+}
+
+__global__ __launch_bounds__(kTeThreads) void k_te_fill(f32x4* p, int64_t n) {
+  for (int64_t i = (int64_t)blockIdx.x * kTeThreads + threadIdx.x; i < n;
+       i += (int64_t)gridDim.x * kTeThreads)
+    p[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+}
+
+template <int LANES> struct TeTeam {
+  static constexpr int lanes = LANES;
+};
+// The team of a row of C columns, at most `MOST` lanes.
+template <int MOST, typename Run> hipError_t te_teams(int C, const Run& run) {
+  if (C <= 64) return run(TeTeam<8>());
+  if (C <= 128) return run(TeTeam<16>());
+  if (C <= 256) return run(TeTeam<32>());
+  if (MOST == 64 || C <= 512) return run(TeTeam<64>());
+  if (C <= 1024) return run(TeTeam<MOST < 128 ? MOST : 128>());
+  return run(TeTeam<MOST>());
+}
+
+struct Plan {
+  int64_t parts;
+  int part, range;
+  size_t list, place, token, count, pieces, total;
+};
+
+Plan plan_of(int64_t T, int64_t V, int C) {
+  Plan p = {};
+  // 16 places a part, more of them where that would be over 2,048 parts
+  p.part = (int)std::max<int64_t>(16, (T + 2047) / 2048);
+  p.parts = (T + p.part - 1) / p.part;
+  // two workgroups for each compute unit, or more where a range would be too long
+  p.range = (int)std::min<int64_t>(kTeRange, (V + 511) / 512);
+  size_t at = 0;
+  p.list = at; at = align256(at + sizeof(int2) * T);
+  p.place = at; at = align256(at + sizeof(int32_t) * T);
+  p.token = at; at = align256(at + sizeof(int32_t) * T);
+  p.count = at; at = align256(at + sizeof(int64_t));
+  p.pieces = at; at = align256(at + sizeof(float) * 2 * p.parts * C);
+  p.total = at;
+  return p;
+}
+
+template <typename T>
+hipError_t lookup(const void* table, const int32_t* tokens, void* out, int64_t n, int64_t V, int C,
+                  float scale, hipStream_t s) {
+  return te_teams<256>(C, [&](auto team) {
+    constexpr int L = decltype(team)::lanes;
+    const int64_t rows = kTeThreads / L;
+    const uint32_t grid = (uint32_t)std::min<int64_t>((n + rows - 1) / rows, kTeMostGrid);
+    k_te_lookup<T, L><<<grid, kTeThreads, 0, s>>>(
+        static_cast<const T*>(table), tokens, static_cast<T*>(out), n, V, C, scale);
+    return hipGetLastError();
+  });
+}
+
+template <typename T>
+hipError_t backward(const int32_t* tokens, const void* g, float* g_table, int64_t n, int64_t V,
+                    int C, float scale, bool accumulate, char* ws, hipStream_t s) {
+  const Plan p = plan_of(n, V, C);
+  const TeSorted sorted = {reinterpret_cast<int2*>(ws + p.list),
+                           reinterpret_cast<int32_t*>(ws + p.place),
+                           reinterpret_cast<int32_t*>(ws + p.token),
+                           reinterpret_cast<int64_t*>(ws + p.count)};
+  k_te_sort<<<(uint32_t)((V + p.range - 1) / p.range), kTeSortThreads, 0, s>>>(
+      tokens, n, V, p.range, sorted, g_table, C, !accumulate);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const TeSums<T> a = {static_cast<const T*>(g), g_table, reinterpret_cast<float*>(ws + p.pieces),
+                       sorted.place, sorted.token, sorted.count, p.parts, p.part, C, accumulate,
+                       scale};
+  return te_teams<64>(C, [&](auto team) {
+    constexpr int L = decltype(team)::lanes;
+    const int64_t rows = kTeThreads / L;
+    const uint32_t slices = (uint32_t)((C / 8 + L - 1) / L);
+    k_te_sums<T, L><<<dim3((uint32_t)((p.parts + rows - 1) / rows), slices), kTeThreads, 0, s>>>(a);
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess || p.parts < 2) return err;
+    k_te_join<T, L><<<dim3((uint32_t)(p.parts - 1), slices), kTeThreads, 0, s>>>(a);
+    return hipGetLastError();
+  });
+}
+
+}  // namespace
+
+hipError_t launch_token_embedding(const void* table, const int32_t* tokens, void* out, int64_t T,
+                                  int64_t V, int C, float scale, nt_dtype dtype, hipStream_t s) {
+  if (T == 0) return hipSuccess;
+  return dtype == NT_BF16 ? lookup<bf16>(table, tokens, out, T, V, C, scale, s)
+                          : lookup<float>(table, tokens, out, T, V, C, scale, s);
+}
+
+size_t token_embedding_backward_ws_bytes(int64_t T, int64_t V, int C) {
+  return T ? plan_of(T, V, C).total : 0;
+}
+
+hipError_t launch_token_embedding_backward(const int32_t* tokens, const void* g_out,
+                                           float* g_table, int64_t T, int64_t V, int C,
+                                           float scale, bool accumulate, nt_dtype dtype, void* ws,
+                                           hipStream_t s) {
+  if (T == 0) {  // nothing to add
+    if (accumulate) return hipSuccess;
+    const int64_t n = V * C / 4;
+    k_te_fill<<<(uint32_t)std::min<int64_t>((n + kTeThreads - 1) / kTeThreads, 4096), kTeThreads, 0,
+                s>>>(reinterpret_cast<f32x4*>(g_table), n);
+    return hipGetLastError();
+  }
+  char* w = static_cast<char*>(ws);
+  return dtype == NT_BF16
+             ? backward<bf16>(tokens, g_out, g_table, T, V, C, scale, accumulate, w, s)
+             : backward<float>(tokens, g_out, g_table, T, V, C, scale, accumulate, w, s);
+}
+
+}  // namespace nt
