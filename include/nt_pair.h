@@ -878,18 +878,17 @@ nt_status nt_residual_norm_backward(const void* h, const void* g_y, const void* 
                                     float eps, nt_dtype dtype, void* workspace,
                                     size_t workspace_bytes, void* stream);
 
-/* Workspace bytes nt_token_loss needs: a few numbers for each token and 128
- * rows of the vocabulary. */
+/* Workspace bytes nt_token_loss needs: two numbers for each token and 128 rows of the
+ * vocabulary, of at most 65,536 tokens (more of them come in passes). */
 nt_status nt_token_loss_workspace_bytes(int64_t T, int64_t V, int32_t C, nt_dtype dtype,
                                         size_t* bytes);
 
 /*
  * Cross entropy of singles over a vocabulary, for each token:
  *   z[t, v] = scale x_t . W_v,  lse[t] = log sum_v exp z[t, v],  nll[t] = lse[t] - z[t, target_t].
- * x: [T, C], W: [V, C] of `dtype`, targets: [T]; nll, lse: fp32 [T]. Logits are
- * fp32 and are not kept. A token whose target is below zero takes no part: nll
+ * x: [T, C], W: [V, C] of `dtype`, targets: [T]; nll, lse: fp32 [T]; scale is
+ * finite and not zero. Logits are fp32 and are not kept. A token whose target is below zero takes no part: nll
  * = lse = 0, whatever its row holds. A target of V or more has nll NaN.
- * NT_ERR_OVERFLOW: more than 2^22 tiles of 128 rows of W x 128 tokens.
  * workspace: device, 16-byte aligned, of one call at a time.
  */
 nt_status nt_token_loss(const void* x, const void* W, const int32_t* targets, float* nll,
@@ -897,7 +896,8 @@ nt_status nt_token_loss(const void* x, const void* W, const int32_t* targets, fl
                         void* workspace, size_t workspace_bytes, void* stream);
 
 /* Workspace bytes nt_token_loss_backward needs: the gradients of the logits of
- * a piece of the vocabulary (at most 512 MiB, or of 256 rows), sums of g_x, a copy of x. */
+ * a piece of the vocabulary (at most 512 MiB, or of 256 rows), sums of g_x, two copies of
+ * x and one of the piece's rows of W, for at most 65,536 tokens. */
 nt_status nt_token_loss_backward_workspace_bytes(int64_t T, int64_t V, int32_t C, nt_dtype dtype,
                                                  size_t* bytes);
 

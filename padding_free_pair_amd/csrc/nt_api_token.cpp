@@ -13,7 +13,6 @@ namespace {
 using namespace nt::host;
 
 constexpr int64_t kMaxVocabulary = int64_t(1) << 26;
-constexpr int64_t kMaxTiles = int64_t(1) << 22;  // a grid holds fewer than 2^32 threads
 
 struct Array {
   const char* name;
@@ -62,6 +61,12 @@ nt_status check_scale(float scale) {
   return NT_OK;
 }
 
+nt_status check_logit_scale(float scale) {
+  if (!std::isfinite(scale) || scale == 0.0f)
+    return fail(NT_ERR_INVALID, "scale must be finite and not zero");
+  return NT_OK;
+}
+
 nt_status check_workspace(const void* workspace, size_t have, size_t need) {
   if (have < need)
     return fail(NT_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", have, need);
@@ -90,10 +95,6 @@ nt_status check_apart(const Array (&written)[W], const Array (&read)[R], const i
 nt_status check_loss(int64_t T, int64_t V, int32_t C, nt_dtype dtype) {
   NT_TRY(check_sizes(T, V, C));
   NT_TRY(check_dtype(dtype));
-  if ((T + 127) / 128 * ((V + 127) / 128) > kMaxTiles ||
-      ((int64_t)C + 127) / 128 * ((T > V ? T : V) + 127) / 128 > kMaxTiles)
-    return fail(NT_ERR_OVERFLOW, "%lld tokens over a vocabulary of %lld exceed one launch",
-                (long long)T, (long long)V);
   return NT_OK;
 }
 
@@ -232,7 +233,7 @@ nt_status nt_token_loss_workspace_bytes(int64_t T, int64_t V, int32_t C, nt_dtyp
                                         size_t* bytes) {
   NT_TRY(check_loss(T, V, C, dtype));
   if (!bytes) return fail(NT_ERR_NULL, "bytes is NULL");
-  *bytes = nt::token_loss_ws_bytes(T, V, dtype);
+  *bytes = nt::token_loss_ws_bytes(T, V, C, dtype);
   return ok();
 }
 
@@ -240,8 +241,8 @@ nt_status nt_token_loss(const void* x, const void* W, const int32_t* targets, fl
                         float* lse, int64_t T, int64_t V, int32_t C, float scale, nt_dtype dtype,
                         void* workspace, size_t workspace_bytes, void* stream) {
   NT_TRY(check_loss(T, V, C, dtype));
-  NT_TRY(check_scale(scale));
-  const size_t es = esize(dtype), need = nt::token_loss_ws_bytes(T, V, dtype);
+  NT_TRY(check_logit_scale(scale));
+  const size_t es = esize(dtype), need = nt::token_loss_ws_bytes(T, V, C, dtype);
   const uint64_t numbers = (uint64_t)T * sizeof(float);
   const Array in[3] = {{"x", x, (uint64_t)T * C * es},
                        {"W", W, (uint64_t)V * C * es},
@@ -274,7 +275,7 @@ nt_status nt_token_loss_backward(const void* x, const void* W, const int32_t* ta
                                  float scale, int32_t accumulate, nt_dtype dtype, void* workspace,
                                  size_t workspace_bytes, void* stream) {
   NT_TRY(check_loss(T, V, C, dtype));
-  NT_TRY(check_scale(scale));
+  NT_TRY(check_logit_scale(scale));
   NT_TRY(check_flag("accumulate", accumulate));
   const size_t es = esize(dtype), need = nt::token_loss_backward_ws_bytes(T, V, C, dtype);
   const uint64_t numbers = (uint64_t)T * sizeof(float);

@@ -301,7 +301,7 @@ size_t residual_norm_backward_ws_bytes(int64_t rows, int C);
 hipError_t launch_residual_norm_backward(const void* h, const void* g_y, const void* g_h,
                                          const float* w, void* g, float* g_w, int64_t rows, int C,
                                          float eps, nt_dtype dtype, void* ws, hipStream_t stream);
-size_t token_loss_ws_bytes(int64_t tokens, int64_t V, nt_dtype dtype);
+size_t token_loss_ws_bytes(int64_t tokens, int64_t V, int C, nt_dtype dtype);
 size_t token_loss_backward_ws_bytes(int64_t tokens, int64_t V, int C, nt_dtype dtype);
 hipError_t launch_token_loss(const void* x, const void* W, const int32_t* targets, float* nll,
                              float* lse, int64_t tokens, int64_t V, int C, float scale,

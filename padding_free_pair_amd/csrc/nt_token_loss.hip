@@ -68,24 +68,48 @@ __global__ __launch_bounds__(kTlListThreads) void k_tl_list(const int32_t* targe
   if (blockIdx.x == gridDim.x - 1 && threadIdx.x == 0) *live = at;
 }
 
-// The listed rows of x, one after another, zeros behind them up to a whole tile.
+// Rows of an array [rows, C] transposed, to [C][ld], and (copy given) as they are,
+// to [..][C]: the rows of a list (list given), or the rows from `first` on. Columns of the
+// result from `*live` (or `rows`) on are zeros up to a whole tile of 256. Tiles of 64
+// x 64 pass through LDS, so both sides are whole lines.
+template <typename T> struct TlTranspose {
+  const T* from;
+  T* to;
+  T* copy;
+  const int32_t* list;
+  const int64_t* live;
+  int64_t rows, ld;
+  int C;
+};
 template <typename T>
-__global__ __launch_bounds__(256) void k_tl_gather(const T* x, const int32_t* rows,
-                                                   const int64_t* live, T* out, int64_t chunks,
-                                                   int64_t padded) {
-  constexpr int V = 16 / (int)sizeof(T);
-  const int64_t n = *live, most = (n + 255) / 256 * 256;
-  const int64_t end = (most < padded ? most : padded) * chunks;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < end; i += (int64_t)gridDim.x * 256) {
-    const int64_t r = i / chunks, c = i - r * chunks;
-    Vec16<T> v;
-    if (r < n) {
-      v = load16(x + ((int64_t)rows[r] * chunks + c) * V);
-    } else {
+__global__ __launch_bounds__(256) void k_tl_transpose(TlTranspose<T> p) {
+  constexpr int V = 16 / (int)sizeof(T), kChunks = 64 / V;  // of a tile's row
+  __shared__ T tile[64][64 + V];
+  const int64_t rows = p.live ? *p.live : p.rows;
+  const int64_t r0 = (int64_t)blockIdx.x * 64;
+  const int c0 = (int)blockIdx.y * 64;
+  if (r0 >= (rows + 255) / 256 * 256) return;
 #pragma unroll
-      for (int e = 0; e < V; ++e) v.set(e, 0.0f);
+  for (int i = threadIdx.x; i < 64 * kChunks; i += 256) {
+    const int r = i / kChunks, c = i % kChunks * V;
+    Vec16<T> v;
+#pragma unroll
+    for (int e = 0; e < V; ++e) v.set(e, 0.0f);
+    if (c0 + c < p.C) {
+      if (r0 + r < rows) v = load16(p.from + (p.list ? p.list[r0 + r] : r0 + r) * p.C + c0 + c);
+      if (p.copy) store16(p.copy + (r0 + r) * p.C + c0 + c, v);
     }
-    store16(out + i * V, v);
+    store16(&tile[r][c], v);
+  }
+  __syncthreads();
+  if (!p.to) return;
+#pragma unroll
+  for (int i = threadIdx.x; i < 64 * kChunks; i += 256) {
+    const int c = i / kChunks, r = i % kChunks * V;
+    Vec16<T> v;
+#pragma unroll
+    for (int e = 0; e < V; ++e) v.v[e] = tile[r + e][c];
+    if (c0 + c < p.C) store16(p.to + (c0 + c) * p.ld + r0 + r, v);
   }
 }
 
@@ -95,18 +119,22 @@ template <typename T> struct TlForward {
   const int32_t* targets;
   const int32_t* rows;
   const int64_t* live;
-  float2* part;   // [tiles of the vocabulary][T]: maximum (in powers of 2) and sum
-  float* at;      // [T] the target's logit, in powers of 2
+  float2* part;   // [tiles of the vocabulary][T]: base (in powers of 2) and sum of the powers
+  float* at;      // [T] the target's logit before its scale
   int64_t tokens, V;
   int C;
   float scale2;   // scale log2(e)
   uint32_t tiles_m, tiles_n;
 };
 
-__device__ __forceinline__ float tl_halves_sum(float x) {
-  const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, x),
-                                                  __builtin_bit_cast(uint32_t, x), false, false);
-  return __builtin_bit_cast(float, (uint32_t)r[0]) + __builtin_bit_cast(float, (uint32_t)r[1]);
+// A value of the four lanes that hold a token joined.
+__device__ __forceinline__ float tl_max4(float x) {
+  x = fmaxf(x, __shfl_xor(x, 16));
+  return fmaxf(x, __shfl_xor(x, 32));
+}
+__device__ __forceinline__ float tl_sum4(float x) {
+  x += __shfl_xor(x, 16);
+  return x + __shfl_xor(x, 32);
 }
 
 template <typename S>
@@ -114,55 +142,51 @@ __global__ __launch_bounds__(S::threads) void k_tl_forward(TlForward<typename S:
   typedef typename S::type T;
   typedef PtAlong<T, S::m, S::threads> A;
   typedef PtAlong<T, S::n, S::threads> B;
-  __shared__ __attribute__((aligned(16))) char smem[2 * S::bytes];
+  __shared__ __attribute__((aligned(256))) char smem[S::lds];
   uint32_t tm, tn;
   if (!pt_tile(blockIdx.x, p.tiles_m, p.tiles_n, &tm, &tn)) return;
   const int64_t v0 = (int64_t)tm * S::m, t0 = (int64_t)tn * S::n, live = *p.live;
   if (t0 >= live) return;
-  const A la([&](int r) { return p.W + (v0 + r < p.V ? v0 + r : p.V - 1) * p.C; });
-  const B lb([&](int r) {
-    return p.x + (int64_t)p.rows[t0 + r < live ? t0 + r : live - 1] * p.C;
+  const A la(p.W + v0 * p.C, p.C, [&](int r) { return v0 + r < p.V ? r : p.V - 1 - v0; });
+  const B lb(p.x, p.C, [&](int r) {
+    return (int64_t)p.rows[t0 + r < live ? t0 + r : live - 1];
   });
-  f32x16 z[S::mt][S::nt];
-  pt_product<S, A, B>(z, smem, (p.C + S::bk - 1) / S::bk, [&](int64_t j, uint32_t to) {
-    la.start(j * S::bk, p.C, to);
-    lb.start(j * S::bk, p.C, to + S::m * 128);
-  });
+  PtSums<S> z;
+  pt_product<true, S, A, B>(
+      z, smem, (p.C + S::bk - 1) / S::bk,
+      [&](int64_t j, uint32_t to) { la.start(j * S::bk, p.C, to); },
+      [&](int64_t j, uint32_t to) { lb.start(j * S::bk, p.C, to); });
 
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, h = lane >> 5;
-  const int m0 = wave / S::wn * 32 * S::mt, n0 = wave % S::wn * 32 * S::nt;
-  const int64_t past = p.V - v0 - m0 - 4 * h;  // the vocabulary's end from the lane's rows on
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4;
+  const int m0 = z.first_m(), n0 = z.first_n();
+  const int64_t past = p.V - v0 - m0 - 4 * g;  // the vocabulary's end from the lane's rows on
   const int left = past < 0 ? 0 : past < S::m ? (int)past : S::m;
   float2* stats = reinterpret_cast<float2*>(smem);  // [wm][n]
+  const float factor = fabsf(p.scale2);
   __syncthreads();
 #pragma unroll
   for (int j = 0; j < S::nt; ++j) {
-    const int64_t t = t0 + n0 + 32 * j + (lane & 31);
+    const int64_t t = t0 + n0 + 16 * j + (lane & 15);
     int target = -1;  // from the lane's rows on, where it is among them
     if (t < live) {
-      const int64_t from = p.targets[p.rows[t]] - v0 - m0 - 4 * h;
-      // the other half of the wave holds every other four rows
-      if (from >= 0 && from < 32 * S::mt && !(from & 4)) target = (int)from;
+      const int64_t from = p.targets[p.rows[t]] - v0 - m0 - 4 * g;
+      if (from >= 0 && from < 16 * S::mt && from % 16 < 4) target = (int)from;
     }
-    float most = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < S::mt; ++i)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        z[i][j][e] *= p.scale2;
-        most = fmaxf(most, z[i][j][e]);
-      }
-    if (v0 + S::m > p.V) {  // the last tile of the vocabulary
-      int end = left;
-      asm volatile("" : "+v"(end)::"memory");  // not compared ahead for every j
-      most = -INFINITY;
+    if (p.scale2 < 0.0f) {  // then all logits the other way round
+      at_rare();
 #pragma unroll
       for (int i = 0; i < S::mt; ++i)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          if (32 * i + 8 * (e >> 2) + (e & 3) >= end) z[i][j][e] = -INFINITY;
-          most = fmaxf(most, z[i][j][e]);
-        }
+        for (int e = 0; e < 4; ++e) z.d[i][j][e] = -z.d[i][j][e];
+    }
+    if (v0 + S::m > p.V) {  // the last tile of the vocabulary
+      int end = left;
+      asm volatile("" : "+v"(end)::"memory");  // not compared ahead for every j
+#pragma unroll
+      for (int i = 0; i < S::mt; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (16 * i + e >= end) z.d[i][j][e] = -INFINITY;
     }
     if (__ballot(target >= 0)) {
       at_rare();
@@ -170,19 +194,28 @@ __global__ __launch_bounds__(S::threads) void k_tl_forward(TlForward<typename S:
 #pragma unroll
       for (int i = 0; i < S::mt; ++i)
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          found = 32 * i + 8 * (e >> 2) + (e & 3) == target ? z[i][j][e] : found;
+        for (int e = 0; e < 4; ++e) found = 16 * i + e == target ? z.d[i][j][e] : found;
       if (target >= 0) p.at[t] = found;
     }
-    most = at_halves_max(most);
+    float most = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < S::mt; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) most = fmaxf(most, z.d[i][j][e]);
+    // The powers count from the base as it is rounded here, the join as well, and the
+    // target's logit is taken from it unrounded (a product and a sum in one rounding), so
+    // that what the base lost cancels in nll. (-inf times a factor of 0 would be NaN.)
+    most = tl_max4(most);
+    most = most == -INFINITY ? most : most * factor;
     const float base = most == -INFINITY ? 0.0f : most;
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < S::mt; ++i)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) sum += __builtin_amdgcn_exp2f(z[i][j][e] - base);
-    sum = tl_halves_sum(sum);
-    if (h == 0) stats[wave / S::wn * S::n + n0 + 32 * j + lane] = make_float2(most, sum);
+      for (int e = 0; e < 4; ++e)
+        sum += __builtin_amdgcn_exp2f(__builtin_fmaf(z.d[i][j][e], factor, -base));
+    sum = tl_sum4(sum);
+    if (g == 0) stats[wave / S::wn * S::n + n0 + 16 * j + lane] = make_float2(most, sum);
   }
   __syncthreads();
   for (int c = threadIdx.x; c < S::n; c += S::threads) {
@@ -204,7 +237,8 @@ __global__ __launch_bounds__(S::threads) void k_tl_forward(TlForward<typename S:
 __global__ __launch_bounds__(256) void k_tl_join(const float2* part, const float* at,
                                                  const int32_t* targets, const int32_t* rows,
                                                  const int64_t* live, float* nll, float* lse,
-                                                 int64_t tokens, int64_t V, uint32_t tiles) {
+                                                 int64_t tokens, int64_t V, uint32_t tiles,
+                                                 float factor) {
   __shared__ float2 stats[16][17];
   const int c = threadIdx.x & 15, k = threadIdx.x >> 4;
   const int64_t n = *live;
@@ -230,89 +264,194 @@ __global__ __launch_bounds__(256) void k_tl_join(const float2* part, const float
     const int64_t row = rows[t];
     lse[row] = (most + rest) * kLn2;
     // a target that the vocabulary does not hold
-    nll[row] = targets[row] < V ? ((most - at[t]) + rest) * kLn2 : __builtin_nanf("");
+    nll[row] = targets[row] < V ? (rest - __builtin_fmaf(at[t], factor, -most)) * kLn2
+                                : __builtin_nanf("");
   }
 }
 
 template <typename T> struct TlGrad {
   const T* x;     // the listed rows, one after another
+  const T* xT;    // transposed, [C][ldt]
   const T* W;
+  const T* WT;    // the piece transposed, [C][ldv]
   const int32_t* targets;
   const int32_t* rows;
   const int64_t* live;
   const float* lse;
   const float* g_nll;
   const float* g_lse;
-  T* d;           // [padded tokens][piece], in bf16 hi, then lo behind `plane` elements
-  int64_t plane, piece;
+  T* d;           // [piece][ldt], in bf16 hi, then lo `plane` elements on
+  int64_t plane, piece, ldv, ldt;
   int64_t v_first, V;  // the piece's first row of W, and all rows
   float* sums;    // products: [splits][...] fp32
   float* out;     // g_W
-  int64_t tokens; // capacity of the lists
+  int64_t tokens; // of the copies, a multiple of 256
   int C, splits, accumulate;
   float scale, scale2;
   uint32_t tiles_m, tiles_n;
 };
 
-// d of a tile: rows of W (m) x tokens (n).
+// A wave's results in the operands' type, to memory by way of LDS, so that rows are
+// stored as whole lines (stores of the four consecutive m that a lane holds took a
+// quarter of the kernel). In LDS a row is an n; its 16-byte chunks are turned by the
+// row, which spreads the accesses over the banks. A wave's part of LDS is its own.
+template <typename S> struct TlTurn {
+  typedef typename S::type T;
+  static constexpr int width = 16 * S::mt, rows = 16 * S::nt;  // of the wave
+  static constexpr int vec = 16 / (int)sizeof(T), chunks = width / vec;
+  static_assert(S::wm * S::wn * rows * width * (int)sizeof(T) <= S::lds, "fits the tiles' LDS");
+  static __device__ __forceinline__ int at(int r, int c) {
+    return r * width + ((c / vec) ^ (r & (chunks - 1))) * vec + c % vec;
+  }
+  static __device__ __forceinline__ T* tile(char* smem) {
+    return reinterpret_cast<T*>(smem) + (threadIdx.x >> 6) * (rows * width);
+  }
+  static __device__ __forceinline__ void put(const PtSums<S>& x, T* tile) {
+    const int lane = threadIdx.x & 63, g = lane >> 4;
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int j = 0; j < S::nt; ++j)
+#pragma unroll
+      for (int i = 0; i < S::mt; ++i)
+        at_store4(tile + at(16 * j + (lane & 15), 16 * i + 4 * g), x.d[i][j][0], x.d[i][j][1],
+                  x.d[i][j][2], x.d[i][j][3]);
+    __builtin_amdgcn_wave_barrier();
+  }
+  // Rows of m, n contiguous: a lane takes 16 bytes of a row, the 4 quarters of a wave
+  // 64 of 16 rows. In bf16 by the transposing read (lane i's address is that of row
+  // i / 4 and columns 4 (i % 4) .. of its quarter).
+  static __device__ __forceinline__ void store(const T* tile, T* to, int64_t pitch) {
+    const int lane = threadIdx.x & 63, g = lane >> 4, i = lane & 15;
+#pragma unroll
+    for (int b = 0; b < S::mt; ++b)
+#pragma unroll
+      for (int k = 0; k < rows / (4 * vec); ++k) {
+        const int n = k * 4 * vec + vec * g;
+        Vec16<T> v;
+        if constexpr (sizeof(T) == 2) {
+          const at_bf16x4 x = at_read_tr(tile + at(n + (i >> 2), 16 * b + 4 * (i & 3)));
+          const at_bf16x4 y = at_read_tr(tile + at(n + 4 + (i >> 2), 16 * b + 4 * (i & 3)));
+          v.v = bf16x8{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+        } else {
+#pragma unroll
+          for (int e = 0; e < vec; ++e) v.v[e] = tile[at(n + e, 16 * b + i)];
+        }
+        store16(to + (16 * b + i) * pitch + n, v);
+      }
+  }
+};
+
+// d of a tile, rows of W (m) x tokens (n), to d[v][t], in bf16 hi and, for the gradient of
+// W, lo. (The order that both products would read along k, [t][v] of hi for the
+// gradient of x, costs more to store than its product gains from it: workgroups come to
+// their stores at the same time, so every byte is paid.)
 template <typename S>
 __global__ __launch_bounds__(S::threads) void k_tl_logit_grad(TlGrad<typename S::type> p) {
   typedef typename S::type T;
   typedef PtAlong<T, S::m, S::threads> A;
   typedef PtAlong<T, S::n, S::threads> B;
-  __shared__ __attribute__((aligned(16))) char smem[2 * S::bytes];
+  __shared__ __attribute__((aligned(256))) char smem[S::lds];
   uint32_t tm, tn;
   if (!pt_tile(blockIdx.x, p.tiles_m, p.tiles_n, &tm, &tn)) return;
   const int64_t c0 = (int64_t)tm * S::m, v0 = p.v_first + c0, t0 = (int64_t)tn * S::n;
   const int64_t live = *p.live;
   if (t0 >= live) return;
-  const A la([&](int r) { return p.W + (v0 + r < p.V ? v0 + r : p.V - 1) * p.C; });
-  const B lb([&](int r) { return p.x + (t0 + r) * p.C; });
-  f32x16 z[S::mt][S::nt];
-  pt_product<S, A, B>(z, smem, (p.C + S::bk - 1) / S::bk, [&](int64_t j, uint32_t to) {
-    la.start(j * S::bk, p.C, to);
-    lb.start(j * S::bk, p.C, to + S::m * 128);
-  });
+  // a tile may begin behind the vocabulary: d is whole tiles of 256
+  const int64_t from = v0 < p.V ? v0 : p.V - 1;
+  const A la(p.W + from * p.C, p.C, [&](int r) { return from + r < p.V ? r : p.V - 1 - from; });
+  const B lb(p.x + t0 * p.C, p.C, [](int r) { return (int64_t)r; });
+  PtSums<S> z;
+  pt_product<true, S, A, B>(
+      z, smem, (p.C + S::bk - 1) / S::bk,
+      [&](int64_t j, uint32_t to) { la.start(j * S::bk, p.C, to); },
+      [&](int64_t j, uint32_t to) { lb.start(j * S::bk, p.C, to); });
 
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, h = lane >> 5;
-  const int m0 = wave / S::wn * 32 * S::mt, n0 = wave % S::wn * 32 * S::nt;
+  const int lane = threadIdx.x & 63, g = lane >> 4, m0 = z.first_m(), n0 = z.first_n();
 #pragma unroll
   for (int j = 0; j < S::nt; ++j) {
-    const int64_t t = t0 + n0 + 32 * j + (lane & 31);
+    const int64_t t = t0 + n0 + 16 * j + (lane & 15), first = v0 + m0 + 4 * g;
     float both = 0.0f, one = 0.0f, base = 0.0f;
-    int target = -1, left = 0;  // from the lane's rows of W on
+    int target = -1;  // from the lane's rows of W on, where it is among them
     if (t < live) {
-      const int64_t row = p.rows[t], past = p.V - v0 - m0 - 4 * h;
-      const int64_t from = p.targets[row] - v0 - m0 - 4 * h;
-      if (from >= 0 && from < 32 * S::mt) target = (int)from;
-      left = past < 0 ? 0 : past < S::m ? (int)past : S::m;
+      const int64_t row = p.rows[t], place = p.targets[row] - first;
+      if (place >= 0 && place < 16 * S::mt && place % 16 < 4) target = (int)place;
       one = p.g_nll[row];
       both = (p.g_lse ? one + p.g_lse[row] : one) * p.scale;
       one *= p.scale;
       base = p.lse[row] * kLog2e;
       if (p.targets[row] >= p.V) both = __builtin_nanf("");
     }
-    T* to = p.d + t * p.piece + c0 + m0 + 4 * h;
 #pragma unroll
     for (int i = 0; i < S::mt; ++i)
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        float f[4];
+      for (int e = 0; e < 4; ++e)
+        z.d[i][j][e] =
+            both * __builtin_amdgcn_exp2f(__builtin_fmaf(z.d[i][j][e], p.scale2, -base));
+    if (__ballot(target >= 0)) {
+      at_rare();
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int v = 32 * i + 8 * g + e;
-          f[e] = both * __builtin_amdgcn_exp2f(z[i][j][4 * g + e] * p.scale2 - base);
-          if (v == target) f[e] -= one;
-          // rows of W that are not there, and tokens behind the last one
-          if (v >= left) f[e] = 0.0f;
-        }
-        at_store4(to + 32 * i + 8 * g, f[0], f[1], f[2], f[3]);
-        if constexpr (sizeof(T) == 2) {
+      for (int i = 0; i < S::mt; ++i)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) f[e] -= (float)(T)f[e];
-          at_store4(to + p.plane + 32 * i + 8 * g, f[0], f[1], f[2], f[3]);
-        }
-      }
+        for (int e = 0; e < 4; ++e) z.d[i][j][e] -= 16 * i + e == target ? one : 0.0f;
+    }
+    if (v0 + S::m > p.V || t0 + S::n > live) {
+      // zeros for rows of W that are not there and for tokens behind the last one
+      const int64_t past = p.V - first;
+      int left = t >= live || past < 0 ? 0 : past < S::m ? (int)past : S::m;
+      asm volatile("" : "+v"(left)::"memory");  // not compared ahead for every j
+#pragma unroll
+      for (int i = 0; i < S::mt; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (16 * i + e >= left) z.d[i][j][e] = 0.0f;
+    }
+  }
+  __syncthreads();  // the tiles have been read
+  T* tile = TlTurn<S>::tile(smem);
+  TlTurn<S>::put(z, tile);
+  T* to = p.d + (c0 + m0) * p.ldt + t0 + n0;
+  TlTurn<S>::store(tile, to, p.ldt);
+  if constexpr (sizeof(T) == 2) {
+    if (!p.out) return;
+#pragma unroll
+    for (int j = 0; j < S::nt; ++j)
+#pragma unroll
+      for (int i = 0; i < S::mt; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) z.d[i][j][e] -= (float)(T)z.d[i][j][e];
+    TlTurn<S>::put(z, tile);
+    TlTurn<S>::store(tile, to + p.plane, p.ldt);
+  }
+}
+
+// Of a product's tiles of k, the ones of a split.
+struct TlSplit {
+  int64_t begin, n;
+  __device__ __forceinline__ TlSplit(int64_t tiles, int splits) {
+    const int64_t each = (tiles + splits - 1) / splits;
+    begin = blockIdx.y * each;
+    n = (begin + each < tiles ? begin + each : tiles) - begin;
+  }
+};
+
+// A wave's results to rows of n in fp32, m contiguous: columns below `columns` of rows below
+// `rows`, added to what is there with `add`.
+template <typename S>
+__device__ __forceinline__ void tl_store(const PtSums<S>& acc, float* to, int64_t pitch,
+                                         int64_t first, int64_t rows, int64_t column,
+                                         int64_t columns, bool add) {
+  const int lane = threadIdx.x & 63, g = lane >> 4;
+#pragma unroll
+  for (int j = 0; j < S::nt; ++j) {
+    const int64_t r = first + acc.first_n() + 16 * j + (lane & 15);
+    if (r >= rows) continue;
+#pragma unroll
+    for (int i = 0; i < S::mt; ++i) {
+      const int64_t c = column + acc.first_m() + 16 * i + 4 * g;
+      if (c >= columns) continue;
+      f32x4* at = reinterpret_cast<f32x4*>(to + r * pitch + c);
+      *at = add ? acc.d[i][j] + *at : acc.d[i][j];
+    }
   }
 }
 
@@ -320,42 +459,23 @@ __global__ __launch_bounds__(S::threads) void k_tl_logit_grad(TlGrad<typename S:
 template <typename S>
 __global__ __launch_bounds__(S::threads) void k_tl_x_grad(TlGrad<typename S::type> p) {
   typedef typename S::type T;
-  typedef PtAcross<T, S::m, S::threads> A;
-  typedef PtAlong<T, S::n, S::threads> B;
-  __shared__ __attribute__((aligned(16))) char smem[2 * S::bytes];
+  typedef PtAlong<T, S::m, S::threads> A;
+  typedef PtAcross<T, S::n, S::threads> B;
+  __shared__ __attribute__((aligned(256))) char smem[S::lds];
   uint32_t tm, tn;
   if (!pt_tile(blockIdx.x, p.tiles_m, p.tiles_n, &tm, &tn)) return;
   const int64_t c0 = (int64_t)tm * S::m, t0 = (int64_t)tn * S::n, live = *p.live;
   if (t0 >= live) return;
   const int64_t K = p.V - p.v_first < p.piece ? p.V - p.v_first : p.piece;
-  const int64_t tiles = (K + S::bk - 1) / S::bk, each = (tiles + p.splits - 1) / p.splits;
-  const int64_t begin = blockIdx.y * each, end = begin + each < tiles ? begin + each : tiles;
-  const A la(p.W + p.v_first * p.C + c0, p.C - c0, p.C);
-  const B lb([&](int r) { return p.d + (t0 + r) * p.piece; });
-  f32x16 acc[S::mt][S::nt];
-  pt_product<S, A, B>(acc, smem, end - begin, [&](int64_t j, uint32_t to) {
-    la.start((begin + j) * S::bk, K, to);
-    lb.start((begin + j) * S::bk, p.piece, to + S::m * 128);
-  });
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, h = lane >> 5;
-  const int m0 = wave / S::wn * 32 * S::mt, n0 = wave % S::wn * 32 * S::nt;
-#pragma unroll
-  for (int j = 0; j < S::nt; ++j) {
-    const int64_t t = t0 + n0 + 32 * j + (lane & 31);
-    if (t >= live) continue;
-    float* to = p.sums + ((int64_t)blockIdx.y * p.tokens + t) * p.C;
-#pragma unroll
-    for (int i = 0; i < S::mt; ++i)
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int64_t c = c0 + m0 + 32 * i + 8 * g + 4 * h;
-        if (c >= p.C) continue;
-        f32x4 f = {acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2],
-                   acc[i][j][4 * g + 3]};
-        if (p.accumulate) f += *reinterpret_cast<const f32x4*>(to + c);
-        *reinterpret_cast<f32x4*>(to + c) = f;
-      }
-  }
+  const TlSplit split((K + S::bk - 1) / S::bk, p.splits);
+  const A la(p.WT + c0 * p.ldv, p.ldv, [&](int r) { return c0 + r < p.C ? r : p.C - 1 - c0; });
+  const B lb(p.d + t0, p.ldt);
+  PtSums<S> acc;
+  pt_product<false, S, A, B>(
+      acc, smem, split.n,
+      [&](int64_t j, uint32_t to) { la.start((split.begin + j) * S::bk, p.piece, to); },
+      [&](int64_t j, uint32_t to) { lb.start((split.begin + j) * S::bk, to); });
+  tl_store(acc, p.sums + blockIdx.y * p.tokens * p.C, p.C, t0, live, c0, p.C, p.accumulate);
 }
 
 // g_W[v][c] (+)= sum over tokens of d[t, v] x[t, c], d as hi and lo in turn; with
@@ -363,47 +483,33 @@ __global__ __launch_bounds__(S::threads) void k_tl_x_grad(TlGrad<typename S::typ
 template <typename S>
 __global__ __launch_bounds__(S::threads) void k_tl_w_grad(TlGrad<typename S::type> p) {
   typedef typename S::type T;
-  typedef PtAcross<T, S::m, S::threads> A;
-  typedef PtAcross<T, S::n, S::threads> B;
-  __shared__ __attribute__((aligned(16))) char smem[2 * S::bytes];
+  typedef PtAlong<T, S::m, S::threads> A;
+  typedef PtAlong<T, S::n, S::threads> B;
+  __shared__ __attribute__((aligned(256))) char smem[S::lds];
   uint32_t tm, tn;
   if (!pt_tile(blockIdx.x, p.tiles_m, p.tiles_n, &tm, &tn)) return;
-  const int64_t c0 = (int64_t)tm * S::m, n_first = (int64_t)tn * S::n, live = *p.live;
-  const int64_t one = (live + S::bk - 1) / S::bk;
-  const int64_t tiles = sizeof(T) == 2 ? 2 * one : one, each = (tiles + p.splits - 1) / p.splits;
-  const int64_t begin = blockIdx.y * each, end = begin + each < tiles ? begin + each : tiles;
-  const A la(p.x + c0, p.C - c0, p.C);
-  const B lb(p.d + n_first, p.piece - n_first, p.piece);
-  B lo = lb;
-  lo.base += p.plane;
-  f32x16 acc[S::mt][S::nt];
-  pt_product<S, A, B>(acc, smem, end - begin, [&](int64_t j, uint32_t to) {
-    const bool low = begin + j >= one;
-    const int64_t k0 = (begin + j - (low ? one : 0)) * S::bk;
-    la.start(k0, p.tokens, to);
-    (low ? lo : lb).start(k0, p.tokens, to + S::m * 128);
-  });
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, h = lane >> 5;
-  const int m0 = wave / S::wn * 32 * S::mt, n0 = wave % S::wn * 32 * S::nt;
+  const int64_t c0 = (int64_t)tm * S::m, n0 = (int64_t)tn * S::n;
+  const int64_t one = (*p.live + S::bk - 1) / S::bk;
+  const TlSplit split(sizeof(T) == 2 ? 2 * one : one, p.splits);
+  const A la(p.xT + c0 * p.ldt, p.ldt,
+             [&](int r) { return c0 + r < p.C ? r : p.C - 1 - c0; });
+  const B lb(p.d + n0 * p.ldt, p.ldt, [](int r) { return (int64_t)r; });
+  PtSums<S> acc;
+  pt_product<false, S, A, B>(
+      acc, smem, split.n,
+      [&](int64_t j, uint32_t to) {
+        const int64_t k = split.begin + j;
+        la.start((k < one ? k : k - one) * S::bk, p.tokens, to);
+      },
+      [&](int64_t j, uint32_t to) {
+        const int64_t k = split.begin + j;
+        lb.start((k < one ? k : k - one) * S::bk, p.tokens, to, k < one ? 0 : p.plane);
+      });
   const int64_t rows = p.V - p.v_first < p.piece ? p.V - p.v_first : p.piece;
-#pragma unroll
-  for (int j = 0; j < S::nt; ++j) {
-    const int64_t v = n_first + n0 + 32 * j + (lane & 31);
-    if (v >= rows) continue;
-    float* to = p.splits > 1 ? p.sums + ((int64_t)blockIdx.y * p.piece + v) * p.C
-                             : p.out + (p.v_first + v) * p.C;
-#pragma unroll
-    for (int i = 0; i < S::mt; ++i)
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int64_t c = c0 + m0 + 32 * i + 8 * g + 4 * h;
-        if (c >= p.C) continue;
-        f32x4 f = {acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2],
-                   acc[i][j][4 * g + 3]};
-        if (p.splits == 1 && p.accumulate) f += *reinterpret_cast<const f32x4*>(to + c);
-        *reinterpret_cast<f32x4*>(to + c) = f;
-      }
-  }
+  if (p.splits > 1)
+    tl_store(acc, p.sums + blockIdx.y * p.piece * p.C, p.C, n0, rows, c0, p.C, false);
+  else
+    tl_store(acc, p.out + p.v_first * p.C, p.C, n0, rows, c0, p.C, p.accumulate);
 }
 
 // The splits of g_x joined and rounded, each listed row at its token's place, zeros at the others.
@@ -450,113 +556,170 @@ uint32_t blocks_of(int64_t x, int64_t each) {
   return (uint32_t)std::min<int64_t>(tiles_of(x, each), 1 << 16);
 }
 
-typedef PtShape<bf16, 4, 2, 2, 4> Big;                       // 256 x 256, 8 waves
-template <typename T> using Mid = PtShape<T, 2, 2, 2, 2>;   // 128 x 128, 4 waves
-template <typename T> using Thin = PtShape<T, 1, 1, 4, 1>;  // 128 x 32, 4 waves
+typedef PtShape<bf16, 8, 4, 2, 4> Big;                      // 256 x 256, 8 waves
+template <typename T> using Mid = PtShape<T, 4, 4, 2, 2>;   // 128 x 128, 4 waves
+template <typename T> using Thin = PtShape<T, 2, 2, 4, 1>;  // 128 x 32, 4 waves
 
 constexpr int64_t kCus = 256;
+constexpr int64_t kThinTokens = 32;
 constexpr int64_t kPieceBytes = int64_t(512) << 20;  // of d
 constexpr int kMostSplits = 16;
 
-struct Plan {
-  int64_t padded, piece, planes;
-  int x_splits, w_splits;
-  // the workspace
-  size_t rows, live, part, at, x, d, x_sums, w_sums, total;
+// Tokens of a pass: an array of them spans 4 GiB at most, and the statistics of 128
+// rows of the vocabulary each 512 MiB (or those of 256 tokens).
+int64_t pass_of(int64_t T, int64_t V) {
+  const int64_t most = (int64_t(1) << 26) / tiles_of(V, 128) / 256 * 256;
+  return std::min(T, std::max<int64_t>(256, std::min<int64_t>(most, 1 << 16)));
+}
+
+// How a product of m x n results over k is cut: into tiles of 256 x 256 or 128 x
+// 128, and k into parts.
+struct Cut {
+  bool big;
+  int splits;
+  double cost;
 };
 
-// Tiles of 256 x 256 where they fill the card once. Only in bf16: fp32 products
-// take sixteen times as long, and a tile of 128 x 128 keeps up with its loads.
-bool big_tiles(int64_t m, int64_t n, bool narrow) {
-  return narrow && tiles_of(m, 256) * tiles_of(n, 256) >= kCus;
+// The cheapest cut, counted in steps of k that a compute unit spends on 128 x
+// 128 results: whole rounds of all units, 4 for a large tile and 1.3 for a small one
+// (measured: 1,430 and 1,115 TFLOP/s where the rounds are full), a tile's beginning and end as
+// 300 steps more (fp32: 20), and the results' way through memory, `bytes` each (8 for each part
+// where there are several) at 4 TB/s. fp32 has the small tile only: its products take sixteen times as long, which
+// hides the loads of either.
+Cut cut_of(int64_t m, int64_t n, int64_t k, double bytes, bool narrow, bool split) {
+  Cut best = {false, 1, 0.0};
+  const double step = narrow ? 5.9e-9 : 5.6e-8;  // seconds
+  const int64_t bk = narrow ? 64 : 32;
+  for (int big = 0; big <= (narrow ? 1 : 0); ++big)
+    for (int s = 1; s <= (split ? kMostSplits : 1); ++s) {
+      if (s > 1 && k < 8 * bk * s) break;
+      const int64_t tile = big ? 256 : 128;
+      const int64_t rounds = tiles_of(tiles_of(m, tile) * tiles_of(n, tile) * s, kCus);
+      const double cost = (double)rounds * (big ? 4.0 : 1.3) *
+                              ((double)tiles_of(k, s) + (narrow ? 300.0 : 20.0)) +
+                          (double)m * (double)n * ((s > 1 ? s * 8.0 : 0.0) + bytes) / 4e12 / step;
+      if ((!big && s == 1) || cost < best.cost) best = {big != 0, s, cost};
+    }
+  return best;
 }
 
-int splits_of(int64_t tiles, int64_t steps) {
-  // about one workgroup for each compute unit and half as many again, eight steps each at least
-  int64_t s = tiles >= kCus ? 1 : (kCus + kCus / 2) / tiles;
-  if (s > steps / 8) s = steps / 8;
-  if (s > kMostSplits) s = kMostSplits;
-  return s < 1 ? 1 : (int)s;
-}
+struct Plan {
+  int64_t tokens, padded, piece, planes, ldv, ldt;
+  Cut logits, singles, weights;
+  // the workspace
+  size_t rows, live, part, at, x, xT, WT, d, x_sums, w_sums, total;
+};
 
-int64_t forward_m(int64_t T, int64_t V, bool narrow) {
-  return T > 32 && big_tiles(V, T, narrow) ? 256 : 128;
-}
+bool thin(int64_t T) { return T <= kThinTokens; }
 
-Plan forward_plan(int64_t T, int64_t V, nt_dtype dtype) {
+Plan forward_plan(int64_t T, int64_t V, int64_t C, nt_dtype dtype) {
   Plan p = {};
+  p.tokens = pass_of(T, V);
+  p.logits = cut_of(V, p.tokens, C, 0.0, dtype == NT_BF16, false);
+  if (thin(p.tokens)) p.logits.big = false;
   size_t at = 0;
-  p.rows = at; at = align256(at + sizeof(int32_t) * T);
+  p.rows = at; at = align256(at + sizeof(int32_t) * p.tokens);
   p.live = at; at = align256(at + sizeof(int64_t));
-  p.at = at; at = align256(at + sizeof(float) * T);
-  p.part = at; at = align256(at + sizeof(float2) * T * tiles_of(V, forward_m(T, V, dtype == NT_BF16)));
+  p.at = at; at = align256(at + sizeof(float) * p.tokens);
+  p.part = at; at = align256(at + sizeof(float2) * p.tokens * tiles_of(V, p.logits.big ? 256 : 128));
   p.total = at;
   return p;
 }
 
 Plan backward_plan(int64_t T, int64_t V, int64_t C, nt_dtype dtype) {
   Plan p = {};
-  const int64_t es = dtype == NT_BF16 ? 2 : 4;
-  p.planes = dtype == NT_BF16 ? 2 : 1;
-  p.padded = up(T, 256);
-  const int64_t most = std::max<int64_t>(256, kPieceBytes / (p.padded * es * p.planes) / 256 * 256);
-  const int64_t pieces = tiles_of(V, most);
-  p.piece = up(tiles_of(V, pieces), 256);
-  const int64_t bk = 128 / es;
-  const bool bx = big_tiles(C, T, p.planes == 2), bw = big_tiles(C, p.piece, p.planes == 2);
-  const int64_t x_tiles = bx ? tiles_of(C, 256) * tiles_of(T, 256) : tiles_of(C, 128) * tiles_of(T, 128);
-  const int64_t w_tiles = bw ? tiles_of(C, 256) * tiles_of(p.piece, 256)
-                             : tiles_of(C, 128) * tiles_of(std::min(p.piece, up(V, 128)), 128);
-  p.x_splits = splits_of(x_tiles, p.piece / bk);
-  p.w_splits = splits_of(w_tiles, p.planes * p.padded / bk);
+  const bool narrow = dtype == NT_BF16;
+  const int64_t es = narrow ? 2 : 4;
+  p.tokens = pass_of(T, V);
+  p.padded = up(p.tokens, 256);
+  p.planes = narrow ? 2 : 1;  // of d
+  const int64_t most =
+      std::max<int64_t>(256, kPieceBytes / (p.padded * es * p.planes) / 256 * 256);
+  // the number of pieces, from the least one on, that fills whole rounds best
+  double best = 0.0;
+  for (int64_t pieces = tiles_of(V, most), last = pieces + 8; pieces < last; ++pieces) {
+    const int64_t piece = up(tiles_of(V, pieces), 256);
+    const Cut l = cut_of(piece, p.tokens, C, (double)(es * p.planes), narrow, false);
+    const Cut x = cut_of(C, p.tokens, piece, 8.0, narrow, true);
+    const Cut w = cut_of(C, piece, p.planes * p.tokens, 4.0, narrow, true);
+    const double cost = (double)tiles_of(V, piece) * (l.cost + x.cost + w.cost);
+    if (!p.piece || cost < best) {
+      best = cost;
+      p.piece = piece;
+      p.logits = l;
+      p.singles = x;
+      p.weights = w;
+    }
+  }
+  // Rows of a power of two of bytes would put the same values of k of all rows in one
+  // channel of the cache: a line more
+  p.ldv = p.piece + 128 / es;
+  p.ldt = p.padded + 128 / es;
   size_t at = 0;
-  p.rows = at; at = align256(at + sizeof(int32_t) * T);
+  p.rows = at; at = align256(at + sizeof(int32_t) * p.tokens);
   p.live = at; at = align256(at + sizeof(int64_t));
   p.x = at; at = align256(at + es * p.padded * C);
-  p.d = at; at = align256(at + es * p.planes * p.padded * p.piece);
-  p.x_sums = at; at = align256(at + sizeof(float) * p.x_splits * p.padded * C);
+  p.xT = at; at = align256(at + es * p.ldt * C);
+  p.WT = at; at = align256(at + es * p.ldv * C);
+  p.d = at; at = align256(at + es * p.planes * p.ldt * p.piece);
+  p.x_sums = at; at = align256(at + sizeof(float) * p.singles.splits * p.padded * C);
   p.w_sums = at;
-  if (p.w_splits > 1) at = align256(at + sizeof(float) * p.w_splits * p.piece * C);
+  if (p.weights.splits > 1) at = align256(at + sizeof(float) * p.weights.splits * p.piece * C);
   p.total = at;
   return p;
 }
 
+hipError_t list(const int32_t* targets, int64_t tokens, int32_t* rows, int64_t* live, float* nll,
+                float* lse, hipStream_t s) {
+  k_tl_list<<<(uint32_t)tiles_of(tokens, kTlListChunk), kTlListThreads, 0, s>>>(
+      targets, tokens, rows, live, nll, lse);
+  return hipGetLastError();
+}
+
 template <typename S>
-hipError_t run_forward(TlForward<typename S::type> a, hipStream_t s) {
+hipError_t run_forward(TlForward<typename S::type> a, float* nll, float* lse, hipStream_t s) {
   a.tiles_m = (uint32_t)tiles_of(a.V, S::m);
   a.tiles_n = (uint32_t)tiles_of(a.tokens, S::n);
-  k_tl_forward<S><<<dim3((uint32_t)pt_grid((int64_t)a.tiles_m * a.tiles_n)), S::threads, 0, s>>>(a);
+  k_tl_forward<S><<<(uint32_t)pt_grid((int64_t)a.tiles_m * a.tiles_n), S::threads, 0, s>>>(a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  k_tl_join<<<blocks_of(a.tokens, 16), 256, 0, s>>>(a.part, a.at, a.targets, a.rows, a.live, nll,
+                                                    lse, a.tokens, a.V, a.tiles_m,
+                                                    fabsf(a.scale2));
   return hipGetLastError();
 }
 
 template <typename T>
-hipError_t forward(const void* x, const void* W, const int32_t* targets, float* nll, float* lse,
-                   int64_t tokens, int64_t V, int C, float scale, char* ws, nt_dtype dtype, hipStream_t s) {
-  const Plan p = forward_plan(tokens, V, dtype);
+hipError_t forward(const T* x, const T* W, const int32_t* targets, float* nll, float* lse,
+                   int64_t T_, int64_t V, int C, float scale, char* ws, nt_dtype dtype,
+                   hipStream_t s) {
+  const Plan p = forward_plan(T_, V, C, dtype);
   int32_t* rows = reinterpret_cast<int32_t*>(ws + p.rows);
   int64_t* live = reinterpret_cast<int64_t*>(ws + p.live);
-  k_tl_list<<<(uint32_t)tiles_of(tokens, kTlListChunk), kTlListThreads, 0, s>>>(targets, tokens,
-                                                                               rows, live, nll, lse);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  TlForward<T> a = {static_cast<const T*>(x), static_cast<const T*>(W), targets, rows, live,
-                    reinterpret_cast<float2*>(ws + p.part), reinterpret_cast<float*>(ws + p.at),
-                    tokens, V, C, scale * kLog2e, 0, 0};
-  const int64_t m = forward_m(tokens, V, dtype == NT_BF16);
-  if constexpr (sizeof(T) == 2)
-    e = m == 256 ? run_forward<Big>(a, s)
-                 : tokens <= 32 ? run_forward<Thin<T>>(a, s) : run_forward<Mid<T>>(a, s);
-  else
-    e = tokens <= 32 ? run_forward<Thin<T>>(a, s) : run_forward<Mid<T>>(a, s);
-  if (e != hipSuccess) return e;
-  k_tl_join<<<blocks_of(tokens, 16), 256, 0, s>>>(
-      a.part, a.at, targets, rows, live, nll, lse, tokens, V, (uint32_t)tiles_of(V, m));
-  return hipGetLastError();
+  for (int64_t t = 0; t < T_; t += p.tokens) {
+    const int64_t n = std::min(p.tokens, T_ - t);
+    hipError_t e = list(targets + t, n, rows, live, nll + t, lse + t, s);
+    if (e != hipSuccess) return e;
+    const TlForward<T> a = {x + t * C, W, targets + t, rows, live,
+                            reinterpret_cast<float2*>(ws + p.part),
+                            reinterpret_cast<float*>(ws + p.at), n, V, C, scale * kLog2e, 0, 0};
+    if constexpr (sizeof(T) == 2) {
+      e = p.logits.big        ? run_forward<Big>(a, nll + t, lse + t, s)
+          : thin(p.tokens) ? run_forward<Thin<T>>(a, nll + t, lse + t, s)
+                           : run_forward<Mid<T>>(a, nll + t, lse + t, s);
+    } else {
+      e = thin(p.tokens) ? run_forward<Thin<T>>(a, nll + t, lse + t, s)
+                         : run_forward<Mid<T>>(a, nll + t, lse + t, s);
+    }
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
-// One of the gradient's products, m x n results, in tiles of the size that fits.
+// One of the gradient's products, m x n results.
 enum Product { kLogits, kSingles, kWeights };
-template <typename S, Product P> hipError_t run_tiles(TlGrad<typename S::type> a, int64_t m, int64_t n, hipStream_t s) {
+template <typename S, Product P>
+hipError_t run_tiles(TlGrad<typename S::type> a, int64_t m, int64_t n, hipStream_t s) {
   a.tiles_m = (uint32_t)tiles_of(m, S::m);
   a.tiles_n = (uint32_t)tiles_of(n, S::n);
   const dim3 grid((uint32_t)pt_grid((int64_t)a.tiles_m * a.tiles_n), a.splits);
@@ -566,61 +729,60 @@ template <typename S, Product P> hipError_t run_tiles(TlGrad<typename S::type> a
   return hipGetLastError();
 }
 template <Product P, typename T>
-hipError_t run_product(const TlGrad<T>& a, bool big, int64_t m, int64_t n, hipStream_t s) {
+hipError_t run_product(TlGrad<T> a, const Cut& cut, int64_t m, int64_t n, hipStream_t s) {
+  a.splits = cut.splits;
   if constexpr (sizeof(T) == 2)
-    if (big) return run_tiles<Big, P>(a, m, n, s);
+    if (cut.big) return run_tiles<Big, P>(a, m, n, s);
   return run_tiles<Mid<T>, P>(a, m, n, s);
 }
 
+template <typename T> hipError_t transpose(const TlTranspose<T>& a, int64_t rows, hipStream_t s) {
+  k_tl_transpose<T><<<dim3((uint32_t)(up(rows, 256) / 64), (uint32_t)tiles_of(a.C, 64)), 256, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+// A pass.
 template <typename T>
-hipError_t backward(const void* x, const void* W, const int32_t* targets, const float* lse,
-                    const float* g_nll, const float* g_lse, void* g_x, float* g_W, int64_t tokens,
-                    int64_t V, int C, float scale, bool accumulate, char* ws, nt_dtype dtype,
-                    hipStream_t s) {
-  const Plan p = backward_plan(tokens, V, C, dtype);
-  const bool narrow = dtype == NT_BF16;
+hipError_t backward(const Plan& p, const T* x, const T* W, const int32_t* targets, const float* lse,
+                    const float* g_nll, const float* g_lse, T* g_x, float* g_W, int64_t tokens,
+                    int64_t V, int C, float scale, bool accumulate, char* ws, hipStream_t s) {
   int32_t* rows = reinterpret_cast<int32_t*>(ws + p.rows);
   int64_t* live = reinterpret_cast<int64_t*>(ws + p.live);
   T* xs = reinterpret_cast<T*>(ws + p.x);
-  k_tl_list<<<(uint32_t)tiles_of(tokens, kTlListChunk), kTlListThreads, 0, s>>>(
-      targets, tokens, rows, live, nullptr, nullptr);
-  hipError_t e = hipGetLastError();
+  T* xT = reinterpret_cast<T*>(ws + p.xT);
+  T* WT = reinterpret_cast<T*>(ws + p.WT);
+  hipError_t e = list(targets, tokens, rows, live, nullptr, nullptr, s);
   if (e != hipSuccess) return e;
-  const int64_t chunks = C * (int64_t)sizeof(T) / 16;
-  k_tl_gather<T><<<blocks_of(p.padded * chunks, 256), 256, 0, s>>>(
-      static_cast<const T*>(x), rows, live, xs, chunks, p.padded);
-  e = hipGetLastError();
+  e = transpose(TlTranspose<T>{x, g_W ? xT : nullptr, xs, rows, live, tokens, p.ldt, C}, tokens, s);
   if (e != hipSuccess) return e;
-  TlGrad<T> a = {xs, static_cast<const T*>(W), targets, rows, live, lse, g_nll, g_lse,
-                 reinterpret_cast<T*>(ws + p.d), p.padded * p.piece, p.piece, 0, V,
-                 reinterpret_cast<float*>(ws + p.x_sums), g_W, p.padded, C, 1, 0, scale,
-                 scale * kLog2e, 0, 0};
+  TlGrad<T> a = {xs, xT, W, WT, targets, rows, live, lse, g_nll, g_lse,
+                 reinterpret_cast<T*>(ws + p.d), p.ldt * p.piece, p.piece, p.ldv, p.ldt, 0, V,
+                 nullptr, g_W, p.padded, C, 1, 0, scale, scale * kLog2e, 0, 0};
+  float* x_sums = reinterpret_cast<float*>(ws + p.x_sums);
+  float* w_sums = reinterpret_cast<float*>(ws + p.w_sums);
   for (int64_t v = 0; v < V; v += p.piece) {
     const int64_t n = std::min(p.piece, V - v);
     a.v_first = v;
-    a.accumulate = 0;
-    a.splits = 1;
     // whole tiles of d: the products read up to the next multiple of a step of k
-    const int64_t m = std::min(p.piece, up(n, 256));
-    e = run_product<kLogits>(a, big_tiles(m, tokens, narrow), m, tokens, s);
+    e = run_product<kLogits>(a, p.logits, up(n, 256), tokens, s);
     if (e != hipSuccess) return e;
     if (g_x) {
+      e = transpose(TlTranspose<T>{W + v * C, WT, nullptr, nullptr, nullptr, n, p.ldv, C}, n, s);
+      if (e != hipSuccess) return e;
+      a.sums = x_sums;
       a.accumulate = v > 0;
-      a.splits = p.x_splits;
-      e = run_product<kSingles>(a, big_tiles(C, tokens, narrow), C, tokens, s);
+      e = run_product<kSingles>(a, p.singles, C, tokens, s);
       if (e != hipSuccess) return e;
     }
     if (g_W) {
-      TlGrad<T> b = a;
-      b.accumulate = accumulate;
-      b.splits = p.w_splits;
-      b.sums = reinterpret_cast<float*>(ws + p.w_sums);
-      e = run_product<kWeights>(b, big_tiles(C, p.piece, narrow), C, n, s);
+      a.sums = w_sums;
+      a.accumulate = accumulate;
+      e = run_product<kWeights>(a, p.weights, C, n, s);
       if (e != hipSuccess) return e;
-      if (p.w_splits > 1) {
+      if (p.weights.splits > 1) {
         const int64_t quads = n * C / 4;
-        k_tl_w_join<<<blocks_of(quads, 256), 256, 0, s>>>(
-            b.sums, g_W + v * C, quads, p.piece * C, p.w_splits, accumulate);
+        k_tl_w_join<<<blocks_of(quads, 256), 256, 0, s>>>(w_sums, g_W + v * C, quads, p.piece * C,
+                                                          p.weights.splits, accumulate);
         e = hipGetLastError();
         if (e != hipSuccess) return e;
       }
@@ -628,14 +790,30 @@ hipError_t backward(const void* x, const void* W, const int32_t* targets, const 
   }
   if (!g_x) return hipSuccess;
   k_tl_x_join<T><<<blocks_of(tokens * (C / 4), 256), 256, 0, s>>>(
-      a.sums, targets, rows, live, static_cast<T*>(g_x), tokens, p.padded, C, p.x_splits);
+      x_sums, targets, rows, live, g_x, tokens, p.padded, C, p.singles.splits);
   return hipGetLastError();
+}
+
+template <typename T>
+hipError_t backward(const void* x, const void* W, const int32_t* targets, const float* lse,
+                    const float* g_nll, const float* g_lse, void* g_x, float* g_W, int64_t tokens,
+                    int64_t V, int C, float scale, bool accumulate, void* ws, nt_dtype dtype,
+                    hipStream_t s) {
+  const Plan p = backward_plan(tokens, V, C, dtype);
+  for (int64_t t = 0; t < tokens; t += p.tokens) {
+    const hipError_t e = backward<T>(
+        p, static_cast<const T*>(x) + t * C, static_cast<const T*>(W), targets + t, lse + t,
+        g_nll + t, g_lse ? g_lse + t : nullptr, g_x ? static_cast<T*>(g_x) + t * C : nullptr, g_W,
+        std::min(p.tokens, tokens - t), V, C, scale, accumulate || t > 0, static_cast<char*>(ws), s);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace
 
-size_t token_loss_ws_bytes(int64_t tokens, int64_t V, nt_dtype dtype) {
-  return tokens ? forward_plan(tokens, V, dtype).total : 0;
+size_t token_loss_ws_bytes(int64_t tokens, int64_t V, int C, nt_dtype dtype) {
+  return tokens ? forward_plan(tokens, V, C, dtype).total : 0;
 }
 
 size_t token_loss_backward_ws_bytes(int64_t tokens, int64_t V, int C, nt_dtype dtype) {
@@ -647,8 +825,11 @@ hipError_t launch_token_loss(const void* x, const void* W, const int32_t* target
                              nt_dtype dtype, void* ws, hipStream_t s) {
   if (tokens == 0) return hipSuccess;
   char* w = static_cast<char*>(ws);
-  return dtype == NT_BF16 ? forward<bf16>(x, W, targets, nll, lse, tokens, V, C, scale, w, dtype, s)
-                          : forward<float>(x, W, targets, nll, lse, tokens, V, C, scale, w, dtype, s);
+  if (dtype == NT_BF16)
+    return forward(static_cast<const bf16*>(x), static_cast<const bf16*>(W), targets, nll, lse,
+                   tokens, V, C, scale, w, dtype, s);
+  return forward(static_cast<const float*>(x), static_cast<const float*>(W), targets, nll, lse,
+                 tokens, V, C, scale, w, dtype, s);
 }
 
 hipError_t launch_token_loss_backward(const void* x, const void* W, const int32_t* targets,
@@ -662,11 +843,10 @@ hipError_t launch_token_loss_backward(const void* x, const void* W, const int32_
     k_tl_fill<<<blocks_of(n, 256), 256, 0, s>>>(g_W, n);
     return hipGetLastError();
   }
-  char* w = static_cast<char*>(ws);
   return dtype == NT_BF16 ? backward<bf16>(x, W, targets, lse, g_nll, g_lse, g_x, g_W, tokens, V, C,
-                                           scale, accumulate, w, dtype, s)
+                                           scale, accumulate, ws, dtype, s)
                           : backward<float>(x, W, targets, lse, g_nll, g_lse, g_x, g_W, tokens, V,
-                                            C, scale, accumulate, w, dtype, s);
+                                            C, scale, accumulate, ws, dtype, s);
 }
 
 }  // namespace nt

@@ -85,8 +85,8 @@ ROWS = [{"rows": -1}, {"rows": 2 ** 31}, {"C": 0}, {"C": 12}, {"C": 16392}, {"ep
     (norm_8bit, ROWS + [{"group": 4}, {"group": 24}, {"group": 256}, {"group": -8}, {"group": 1024},
                         {"group": 640, "C": 640}]),
     (norm_backward, ROWS),
-    (loss, SIZES + [{"scale": math.inf}]),
-    (loss_backward, SIZES + [{"scale": math.inf}, {"accumulate": 3}])])
+    (loss, SIZES + [{"scale": math.inf}, {"scale": 0.0}, {"scale": -0.0}]),
+    (loss_backward, SIZES + [{"scale": math.inf}, {"scale": 0.0}, {"accumulate": 3}])])
 def test_sizes(lib, call, changes):
     for change in changes:
         assert call(lib, **change) == E.NT_ERR_INVALID, change
@@ -141,14 +141,6 @@ def test_overlaps(lib, call, pairs):
         assert call(lib, x=at(30), h=at(30), y=at(30)) == E.NT_ERR_INVALID
 
 
-def test_loss_overflow(lib):
-    b = ctypes.c_size_t()
-    assert lib.nt_token_loss_workspace_bytes(2 ** 20, 2 ** 20, 64, 1, ctypes.byref(b)) == \
-        E.NT_ERR_OVERFLOW
-    assert loss(lib, T=2 ** 20, V=2 ** 20) == E.NT_ERR_OVERFLOW
-    assert loss_backward(lib, T=2 ** 20, V=2 ** 20) == E.NT_ERR_OVERFLOW
-
-
 def test_workspace_sizes(lib):
     """Bounded whatever the vocabulary: the logits' gradients come in pieces."""
     b = ctypes.c_size_t()
@@ -158,10 +150,14 @@ def test_workspace_sizes(lib):
         return b.value
 
     T, C = 8192, 2048
-    copies = T * C * (2 + 4)  # x, and the sums of g_x
+    d = 512 << 20  # in two forms, of T x piece values each
     for V in (32003, 131072, 2 ** 20):
-        assert of(T, V, C) <= (512 << 20) + copies + (1 << 20)
-        assert of(T, V, C, 0) <= (512 << 20) + T * C * (4 + 4 * 16) + (1 << 20)
+        # x twice, the sums of g_x, and a piece of W: as large as d at C = T
+        assert of(T, V, C) <= d + T * C * (2 + 2 + 4) + d + (1 << 20)
+        assert of(T, V, C, 0) <= d + T * C * (4 + 4 + 4 * 16) + d + (1 << 20)
+    assert of(T, 2 ** 20, C) < T * 2 ** 20 * 2  # less than the logits would take
+    # more tokens come in passes
+    assert of(2 ** 24, 32003, C) == of(2 ** 16, 32003, C)
     assert of(0, 5, 8) == 0
     assert lib.nt_token_loss_backward_workspace_bytes(5, 9, 16, 1, None) == E.NT_ERR_NULL
     assert lib.nt_token_loss_workspace_bytes(5, 9, 16, 1, None) == E.NT_ERR_NULL
