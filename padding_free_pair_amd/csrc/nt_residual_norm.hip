@@ -59,6 +59,24 @@ template <> __device__ __forceinline__ void rn_store<float>(float* p, const floa
   *reinterpret_cast<f32x4*>(p + 4) = f32x4{f[4], f[5], f[6], f[7]};
 }
 
+// Eight columns of a row as they lie in memory.
+template <typename T> struct RnRaw {
+  uint4 v[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) v[i] = reinterpret_cast<const uint4*>(p)[i];
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) v[i] = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ float get(int e) const {
+    T t[8];
+    __builtin_memcpy(t, v, sizeof(t));
+    return (float)t[e];
+  }
+};
+
 struct RnSum {
   __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
 };
@@ -218,10 +236,30 @@ template <typename T> struct RnBackward {
   float eps;
 };
 
+// Two values of every lane of a team summed in one exchange.
+template <int LANES> __device__ __forceinline__ float2 rn_sum2(float2 v, float2* scratch) {
+#pragma unroll
+  for (int m = 1; m < (LANES < 64 ? LANES : 64); m <<= 1) {
+    v.x += __shfl_xor(v.x, m);
+    v.y += __shfl_xor(v.y, m);
+  }
+  if (LANES > 64) {
+    if ((threadIdx.x & 63) == 0) scratch[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = scratch[0];
+#pragma unroll
+    for (int w = 1; w < LANES / 64; ++w) {
+      v.x += scratch[w].x;
+      v.y += scratch[w].y;
+    }
+  }
+  return v;
+}
+
 template <typename T, int LANES, int NV>
 __global__ __launch_bounds__(kRnThreads) void k_rn_backward(RnBackward<T> p) {
   constexpr int kTeams = kRnThreads / LANES;
-  __shared__ float scratch[kRnThreads / 64];
+  __shared__ float2 scratch[2][kRnThreads / 64];  // in turn, so that one barrier a row is enough
   const int lane = threadIdx.x % LANES, team = threadIdx.x / LANES;
   float w[NV][8], sums[NV][8];
 #pragma unroll
@@ -235,45 +273,59 @@ __global__ __launch_bounds__(kRnThreads) void k_rn_backward(RnBackward<T> p) {
     if (p.w && c < p.C) rn_load<float>(p.w + c, w[u]);
   }
   const int64_t step = (int64_t)gridDim.x * kTeams;
-  for (int64_t first = (int64_t)blockIdx.x * kTeams; first < p.rows; first += step) {
+  // the next row is loaded while this one is worked on (rows of up to 8,192 columns: the
+  // wider ones have no registers left)
+  constexpr bool kAhead = NV <= 4;
+  RnRaw<T> h[NV], g[NV], more[NV];
+  const auto load = [&](int64_t first) {
     const int64_t row = first + team;
-    const bool is = row < p.rows;  // the others keep the lane exchanges whole
-    const int64_t at = (is ? row : p.rows - 1) * p.C;
-    float h[NV][8], g[NV][8], squares = 0.0f, dots = 0.0f;
+    const int64_t at = (row < p.rows ? row : p.rows - 1) * p.C;
 #pragma unroll
     for (int u = 0; u < NV; ++u) {
       const int c = (lane + u * LANES) * 8;
+      more[u].zero();
       if (c < p.C) {
-        rn_load<T>(p.h + at + c, h[u]);
-        rn_load<T>(p.g_y + at + c, g[u]);
+        h[u].load(p.h + at + c);
+        g[u].load(p.g_y + at + c);
+        if (p.g_h) more[u].load(p.g_h + at + c);
       } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) h[u][e] = g[u][e] = 0.0f;
+        h[u].zero();
+        g[u].zero();
       }
     }
+  };
+  int turn = 0;
+  if (kAhead) load((int64_t)blockIdx.x * kTeams);
+  for (int64_t first = (int64_t)blockIdx.x * kTeams; first < p.rows; first += step, turn ^= 1) {
+    const int64_t row = first + team;
+    const bool is = row < p.rows;  // the others keep the lane exchanges whole
+    if (!kAhead) load(first);
+    const int64_t at = row * p.C;
+    float2 s = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int u = 0; u < NV; ++u)
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        squares += h[u][e] * h[u][e];
-        dots += h[u][e] * (g[u][e] * w[u][e]);
+        s.x += h[u].get(e) * h[u].get(e);
+        s.y += h[u].get(e) * (g[u].get(e) * w[u][e]);
       }
-    squares = rn_join<LANES>(squares, LANES, RnSum(), scratch);
-    dots = rn_join<LANES>(dots, LANES, RnSum(), scratch);
-    const float r = 1.0f / sqrtf(squares / (float)p.C + p.eps);
-    const float mean = r * dots / (float)p.C;  // of g_y w xhat
+    s = rn_sum2<LANES>(s, scratch[turn]);
+    const float r = 1.0f / sqrtf(s.x / (float)p.C + p.eps);
+    const float mean = r * s.y / (float)p.C;  // of g_y w xhat
+    float out[NV][8];
+#pragma unroll
+    for (int u = 0; u < NV; ++u)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float xhat = h[u].get(e) * r;
+        out[u][e] = r * (g[u].get(e) * w[u][e] - xhat * mean) + more[u].get(e);
+        if (is) sums[u][e] += g[u].get(e) * xhat;
+      }
+    if (kAhead && first + step < p.rows) load(first + step);
 #pragma unroll
     for (int u = 0; u < NV; ++u) {
       const int c = (lane + u * LANES) * 8;
-      float out[8], more[8] = {};
-      if (p.g_h && c < p.C) rn_load<T>(p.g_h + at + c, more);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float xhat = h[u][e] * r;
-        out[e] = r * (g[u][e] * w[u][e] - xhat * mean) + more[e];
-        if (is) sums[u][e] += g[u][e] * xhat;
-      }
-      if (is && c < p.C) rn_store<T>(p.g + at + c, out);
+      if (is && c < p.C) rn_store<T>(p.g + at + c, out[u]);
     }
   }
   if (!p.part) return;
@@ -298,18 +350,27 @@ __global__ __launch_bounds__(kRnThreads) void k_rn_backward(RnBackward<T> p) {
   }
 }
 
-// g_w[c] = the workgroups' sums added: 32 columns x 8 stretches of workgroups.
-__global__ __launch_bounds__(kRnThreads) void k_rn_weights(const float* part, float* g_w,
-                                                           int blocks, int C) {
-  __shared__ double all[8][33];
-  const int c = blockIdx.x * 32 + (threadIdx.x & 31), k = threadIdx.x >> 5;
+// g_w[c] = the workgroups' sums added: 32 columns x 32 stretches of workgroups, 8 loads
+// of a thread in flight (8 stretches and one load after the other: 17 us).
+constexpr int kRnWeightThreads = 1024;
+__global__ __launch_bounds__(kRnWeightThreads) void k_rn_weights(const float* part, float* g_w,
+                                                                 int blocks, int C) {
+  __shared__ double all[32][33];
+  const int lane = threadIdx.x & 31, c = blockIdx.x * 32 + lane, k = threadIdx.x >> 5;
   double s = 0.0;
   if (c < C)
-    for (int b = k; b < blocks; b += 8) s += (double)part[(int64_t)b * C + c];
-  all[k][threadIdx.x & 31] = s;
+    for (int b = k; b < blocks; b += 256) {
+      float f[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) f[u] = b + 32 * u < blocks ? part[(int64_t)(b + 32 * u) * C + c] : 0.0f;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) s += (double)f[u];
+    }
+  all[k][lane] = s;
   __syncthreads();
   if (k || c >= C) return;
-  for (int i = 1; i < 8; ++i) s += all[i][threadIdx.x & 31];
+#pragma unroll
+  for (int i = 1; i < 32; ++i) s += all[i][lane];
   g_w[c] = (float)s;
 }
 
@@ -364,7 +425,7 @@ hipError_t backward(const RnBackward<T>& p, float* g_w, hipStream_t s) {  // g_w
     if (e != hipSuccess) return e;
   }
   if (!p.w) return hipSuccess;
-  k_rn_weights<<<(p.C + 31) / 32, kRnThreads, 0, s>>>(p.part, g_w, blocks, p.C);
+  k_rn_weights<<<(p.C + 31) / 32, kRnWeightThreads, 0, s>>>(p.part, g_w, blocks, p.C);
   return hipGetLastError();
 }
 

@@ -30,8 +30,8 @@ def embedding(lib, **change):
 
 
 def embedding_backward(lib, **change):
-    a = dict(tokens=at(0), g=at(1), table=at(2), T=5, V=9, C=16, scale=1.0, accumulate=0, dtype=1,
-             ws=at(3), bytes=1 << 20, stream=None)
+    a = dict(tokens=at(0), g=at(1), table=at(2), T=5000, V=9, C=16, scale=1.0, accumulate=0,
+             dtype=1, ws=at(3), bytes=1 << 20, stream=None)
     a.update(change)
     return lib.nt_token_embedding_backward(*a.values())
 

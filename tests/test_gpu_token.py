@@ -69,7 +69,10 @@ def test_embedding(nt, T, V, C, scale, dtype):
 
 BACK = [(1, 1, 8, 1), (1, 5000, 8, 1), (64, 1, 16, 1), (17, 3, 72, 2), (700, 33, 384, 1),
         (1000, 511, 64, 1), (1000, 513, 128, 1), (2500, 1500, 264, 1), (300, 100000, 40, 1),
-        (5000, 7, 520, 3), (40000, 4, 32, 1)]
+        (5000, 7, 520, 3), (40000, 4, 32, 1),
+        # either side of the rule for one launch
+        (4096, 5, 72, 3), (4097, 5, 72, 3), (40, 4096, 64, 1), (40, 4097, 64, 1), (4096, 2, 8, 2),
+        (4100, 2, 8, 2), (4100, 3, 72, 2)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
