@@ -294,7 +294,7 @@ def _loss_inputs(rng, T, V, C, dtype, absent=0.2, spread=2.0):
     return x, x64, W, W64, ids
 
 
-LOSS = [(1, 1, 8), (1, 2, 64), (2, 127, 72), (5, 128, 136), (32, 129, 40), (31, 1000, 384),
+LOSS = [(1, 1, 8), (1, 2, 64), (2, 127, 72), (5, 128, 136), (32, 129, 40), (17, 70001, 24), (16, 65, 264), (31, 1000, 384),
         (33, 33, 8), (64, 257, 64), (130, 300, 200), (257, 128, 1032), (300, 1301, 128)]
 
 
