@@ -43,6 +43,27 @@ __device__ __forceinline__ f32x4 pt_mma(const f32x8& a, const f32x8& b, f32x4 c)
   for (int j = 0; j < 8; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[j], b[j], c, 0, 0, 0);
   return c;
 }
+// The products of all blocks, in fp32 one value of k of all blocks after the other, so
+// that none waits for the one before it.
+template <int MT, int NT>
+__device__ __forceinline__ void pt_mma(const bf16x8 (&a)[MT], const bf16x8 (&b)[NT],
+                                       f32x4 (&c)[MT][NT]) {
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) c[i][j] = pt_mma(a[i], b[j], c[i][j]);
+}
+template <int MT, int NT>
+__device__ __forceinline__ void pt_mma(const f32x8 (&a)[MT], const f32x8 (&b)[NT],
+                                       f32x4 (&c)[MT][NT]) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+        c[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[i][k], b[j][k], c[i][j], 0, 0, 0);
+}
 
 // The thread's index where few tiles need it: nothing that follows from it is kept in
 // registers over the walk.
@@ -95,9 +116,11 @@ template <typename T, int ROWS, int THREADS> struct PtAlong : PtRows<T, ROWS, TH
   template <typename Place>
   __device__ __forceinline__ PtAlong(const T* b, int64_t ld, const Place& place) : base(b) {
 #pragma unroll
-    for (int u = 0; u < pieces; ++u)
+    for (int u = 0; u < pieces; ++u) {
       off[u] = (uint32_t)((place(Base::row(threadIdx.x, u)) * ld + Base::col(threadIdx.x, u)) *
                           (int64_t)sizeof(T));
+      asm volatile("" : "+v"(off[u]));  // one register, not the 64 bits it comes from
+    }
   }
   // Values k0 .. of all rows to LDS address `tile`, zeros from K on, of the array that lies
   // `plane` elements on.
@@ -111,10 +134,13 @@ template <typename T, int ROWS, int THREADS> struct PtAlong : PtRows<T, ROWS, TH
     } else {
       const int thread = pt_thread();
 #pragma unroll
-      for (int u = 0; u < pieces; ++u)
-        at_load_lds<16>(k0 + Base::col(thread, u) < K ? (const void*)(from + off[u])
-                                              : (const void*)&kAtZeros,
+      for (int u = 0; u < pieces; ++u) {
+        uint32_t o = off[u];
+        asm volatile("" : "+v"(o));
+        at_load_lds<16>(k0 + Base::col(thread, u) < K ? (const void*)(from + o)
+                                                      : (const void*)&kAtZeros,
                         to + u * THREADS * 16);
+      }
     }
   }
 };
@@ -137,6 +163,7 @@ template <typename T, int COLS, int THREADS> struct PtAcross {
       const int i = threadIdx.x + u * THREADS, row = i / 16 % bk;
       const int col = i / (16 * bk) * sub + (i % 16 ^ L::turn(row)) * L::vec;
       off[u] = (uint32_t)((row * ld + col) * (int64_t)sizeof(T));
+      asm volatile("" : "+v"(off[u]));
     }
   }
   // Rows k0 .. to LDS address `tile`.
@@ -204,10 +231,7 @@ template <typename S> struct PtFrags {
   }
   __device__ __forceinline__ void multiply(PtSums<S>& acc) const {
     __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int i = 0; i < S::mt; ++i)
-#pragma unroll
-      for (int j = 0; j < S::nt; ++j) acc.d[i][j] = pt_mma(a[i], b[j], acc.d[i][j]);
+    pt_mma(a, b, acc.d);
     __builtin_amdgcn_sched_barrier(0);
   }
 };
@@ -282,7 +306,8 @@ __device__ __forceinline__ void pt_product(PtSums<S>& acc, char* smem, int64_t n
 // Tiles over the eight dies: workgroups go to the dies in turn, so each die
 // takes a stretch of the tiles' order, and in that order four tiles of m stay
 // together over all tiles of n: what the 32 workgroups of a die read at a time
-// is 4 + 8 strips of the operands, which its cache holds.
+// is 4 + 8 strips of the operands, which its cache holds. A launch has the tiles' number
+// rounded up to whole eights of workgroups.
 constexpr int kPtGroup = 4;
 __device__ __forceinline__ bool pt_tile(uint32_t id, uint32_t tiles_m, uint32_t tiles_n, uint32_t* m,
                                         uint32_t* n) {
@@ -296,6 +321,5 @@ __device__ __forceinline__ bool pt_tile(uint32_t id, uint32_t tiles_m, uint32_t 
   *n = in / have;
   return true;
 }
-inline int64_t pt_grid(int64_t tiles) { return (tiles + 7) / 8 * 8; }
 
 }  // namespace nt

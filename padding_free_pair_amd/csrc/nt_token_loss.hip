@@ -25,6 +25,7 @@
 namespace nt {
 namespace {
 
+constexpr int kMostSplits = 16;
 constexpr int kTlListThreads = 1024;
 constexpr int64_t kTlListChunk = 4 * kTlListThreads;  // targets of a workgroup of the list
 
@@ -81,8 +82,10 @@ template <typename T> struct TlTranspose {
   int64_t rows, ld;
   int C;
 };
+// Two arrays in one launch, the second one (blockIdx.z 1) where there is one.
 template <typename T>
-__global__ __launch_bounds__(256) void k_tl_transpose(TlTranspose<T> p) {
+__global__ __launch_bounds__(256) void k_tl_transpose(TlTranspose<T> p, TlTranspose<T> second) {
+  if (blockIdx.z) p = second;
   constexpr int V = 16 / (int)sizeof(T), kChunks = 64 / V;  // of a tile's row
   __shared__ T tile[64][64 + V];
   const int64_t rows = p.live ? *p.live : p.rows;
@@ -124,7 +127,7 @@ template <typename T> struct TlForward {
   int64_t tokens, V;
   int C;
   float scale2;   // scale log2(e)
-  uint32_t tiles_m, tiles_n;
+  uint32_t tiles_m;
 };
 
 // A value of the four lanes that hold a token joined.
@@ -144,9 +147,9 @@ __global__ __launch_bounds__(S::threads) void k_tl_forward(TlForward<typename S:
   typedef PtAlong<T, S::n, S::threads> B;
   __shared__ __attribute__((aligned(256))) char smem[S::lds];
   uint32_t tm, tn;
-  if (!pt_tile(blockIdx.x, p.tiles_m, p.tiles_n, &tm, &tn)) return;
-  const int64_t v0 = (int64_t)tm * S::m, t0 = (int64_t)tn * S::n, live = *p.live;
-  if (t0 >= live) return;
+  const int64_t live = *p.live;
+  if (!pt_tile(blockIdx.x, p.tiles_m, (uint32_t)((live + S::n - 1) / S::n), &tm, &tn)) return;
+  const int64_t v0 = (int64_t)tm * S::m, t0 = (int64_t)tn * S::n;
   const A la(p.W + v0 * p.C, p.C, [&](int r) { return v0 + r < p.V ? r : p.V - 1 - v0; });
   const B lb(p.x, p.C, [&](int r) {
     return (int64_t)p.rows[t0 + r < live ? t0 + r : live - 1];
@@ -275,8 +278,8 @@ __global__ __launch_bounds__(256) void k_tl_join(const float2* part, const float
 // and all waves of the card at it. A wave keeps each token's
 // maximum and sum over the rows that it takes. The list of tokens is a ballot. x lies in
 // LDS, 64 KiB of it at a time: fragments of x from the cache would be as many loads again
-// as those of W (40 us where these are @). Measured at 16 tokens, 32,000 words of 2,048
-// (131 MB): @ us, @ TB/s.
+// as those of W (40 us where this takes 34). Measured at 16 tokens, 32,000 words of 2,048
+// (131 MB): 28 us, 4.6 TB/s, and the join 5; 131,072 words of 4,096 200 us, 5.3 TB/s.
 constexpr int kThinTokens = 32;
 constexpr int kThinWaves = 4;
 constexpr int kThinBlocks = 1024;  // of a launch, four for each compute unit
@@ -524,7 +527,8 @@ template <typename T> struct TlGrad {
   float* sums;    // products: [splits][...] fp32
   float* out;     // g_W
   int64_t tokens; // of the copies, a multiple of 256
-  int C, splits, accumulate;
+  int64_t x_budget;  // numbers in the sums of g_x
+  int C, w_most, accumulate;
   float scale, scale2;
   uint32_t tiles_m, tiles_n;
 };
@@ -590,10 +594,9 @@ __global__ __launch_bounds__(S::threads) void k_tl_logit_grad(TlGrad<typename S:
   typedef PtAlong<T, S::n, S::threads> B;
   __shared__ __attribute__((aligned(256))) char smem[S::lds];
   uint32_t tm, tn;
-  if (!pt_tile(blockIdx.x, p.tiles_m, p.tiles_n, &tm, &tn)) return;
-  const int64_t c0 = (int64_t)tm * S::m, v0 = p.v_first + c0, t0 = (int64_t)tn * S::n;
   const int64_t live = *p.live;
-  if (t0 >= live) return;
+  if (!pt_tile(blockIdx.x, p.tiles_m, (uint32_t)((live + S::n - 1) / S::n), &tm, &tn)) return;
+  const int64_t c0 = (int64_t)tm * S::m, v0 = p.v_first + c0, t0 = (int64_t)tn * S::n;
   // a tile may begin behind the vocabulary: d is whole tiles of 256
   const int64_t from = v0 < p.V ? v0 : p.V - 1;
   const A la(p.W + from * p.C, p.C, [&](int r) { return from + r < p.V ? r : p.V - 1 - from; });
@@ -662,13 +665,39 @@ __global__ __launch_bounds__(S::threads) void k_tl_logit_grad(TlGrad<typename S:
   }
 }
 
-// Of a product's tiles of k, the ones of a split.
-struct TlSplit {
-  int64_t begin, n;
-  __device__ __forceinline__ TlSplit(int64_t tiles, int splits) {
-    const int64_t each = (tiles + splits - 1) / splits;
-    begin = blockIdx.y * each;
-    n = (begin + each < tiles ? begin + each : tiles) - begin;
+// How many parts k is cut into: as many as the launched workgroups allow for this many tiles
+// of results (how many tokens have a target is known here only), up to `most`, each of
+// eight tiles of k at least.
+__device__ __forceinline__ int tl_splits(int64_t tiles, int64_t steps, int64_t launched,
+                                         int64_t most) {
+  int64_t s = launched / ((tiles + 7) / 8 * 8);
+  if (s > steps / 8) s = steps / 8;
+  if (s > most) s = most;
+  return s < 1 ? 1 : (int)s;
+}
+
+// The parts of g_x that `budget` fp32 numbers hold.
+__device__ __forceinline__ int64_t tl_most(int64_t budget, int64_t live, int C) {
+  const int64_t most = live ? budget / (live * C) : 1;
+  return most < kMostSplits ? most : kMostSplits;
+}
+
+// A workgroup's tile of results and its part of the tiles of k.
+struct TlPart {
+  uint32_t m, n;
+  int split, splits;
+  int64_t begin, count;
+  __device__ __forceinline__ bool take(uint32_t tiles_m, uint32_t tiles_n, int64_t steps,
+                                       int64_t most) {
+    const int64_t tiles = (int64_t)tiles_m * tiles_n, each = (tiles + 7) / 8 * 8;
+    if (tiles == 0) return false;
+    splits = tl_splits(tiles, steps, gridDim.x, most);
+    split = (int)(blockIdx.x / each);
+    if (split >= splits) return false;
+    const int64_t length = (steps + splits - 1) / splits;
+    begin = split * length;
+    count = (begin + length < steps ? begin + length : steps) - begin;
+    return pt_tile((uint32_t)(blockIdx.x - split * each), tiles_m, tiles_n, &m, &n);
   }
 };
 
@@ -693,27 +722,36 @@ __device__ __forceinline__ void tl_store(const PtSums<S>& acc, float* to, int64_
   }
 }
 
-// sums[split][t][c] (+)= sum over the split's rows v of the piece of d[t, v] W[v, c].
+// The product of g_x, sums[split][t][c] (+)= sum over the split's rows v of the piece of
+// d[t, v] W[v, c], and that of g_W: both sides of a launch and of its join count alike.
+template <int TILE> __device__ __forceinline__ int64_t tl_tokens(int64_t live) {
+  return (live + TILE - 1) / TILE;
+}
+
 template <typename S>
 __global__ __launch_bounds__(S::threads) void k_tl_x_grad(TlGrad<typename S::type> p) {
   typedef typename S::type T;
   typedef PtAlong<T, S::m, S::threads> A;
   typedef PtAcross<T, S::n, S::threads> B;
   __shared__ __attribute__((aligned(256))) char smem[S::lds];
-  uint32_t tm, tn;
-  if (!pt_tile(blockIdx.x, p.tiles_m, p.tiles_n, &tm, &tn)) return;
-  const int64_t c0 = (int64_t)tm * S::m, t0 = (int64_t)tn * S::n, live = *p.live;
-  if (t0 >= live) return;
+  const int64_t live = *p.live;
   const int64_t K = p.V - p.v_first < p.piece ? p.V - p.v_first : p.piece;
-  const TlSplit split((K + S::bk - 1) / S::bk, p.splits);
+  TlPart part;
+  // parts of the first piece, which may be cut finer than a shorter last one could
+  if (!part.take(p.tiles_m, (uint32_t)tl_tokens<S::n>(live), p.piece / S::bk,
+                 tl_most(p.x_budget, live, p.C)))
+    return;
+  const int64_t steps = (K + S::bk - 1) / S::bk;
+  const int64_t count = part.begin + part.count < steps ? part.count : steps - part.begin;
+  const int64_t c0 = (int64_t)part.m * S::m, t0 = (int64_t)part.n * S::n;
   const A la(p.WT + c0 * p.ldv, p.ldv, [&](int r) { return c0 + r < p.C ? r : p.C - 1 - c0; });
   const B lb(p.d + t0, p.ldt);
   PtSums<S> acc;
   pt_product<false, S, A, B>(
-      acc, smem, split.n,
-      [&](int64_t j, uint32_t to) { la.start((split.begin + j) * S::bk, p.piece, to); },
-      [&](int64_t j, uint32_t to) { lb.start((split.begin + j) * S::bk, to); });
-  tl_store(acc, p.sums + blockIdx.y * p.tokens * p.C, p.C, t0, live, c0, p.C, p.accumulate);
+      acc, smem, count,
+      [&](int64_t j, uint32_t to) { la.start((part.begin + j) * S::bk, p.piece, to); },
+      [&](int64_t j, uint32_t to) { lb.start((part.begin + j) * S::bk, to); });
+  tl_store(acc, p.sums + part.split * live * p.C, p.C, t0, live, c0, p.C, p.accumulate);
 }
 
 // g_W[v][c] (+)= sum over tokens of d[t, v] x[t, c], d as hi and lo in turn; with
@@ -724,59 +762,75 @@ __global__ __launch_bounds__(S::threads) void k_tl_w_grad(TlGrad<typename S::typ
   typedef PtAlong<T, S::m, S::threads> A;
   typedef PtAlong<T, S::n, S::threads> B;
   __shared__ __attribute__((aligned(256))) char smem[S::lds];
-  uint32_t tm, tn;
-  if (!pt_tile(blockIdx.x, p.tiles_m, p.tiles_n, &tm, &tn)) return;
-  const int64_t c0 = (int64_t)tm * S::m, n0 = (int64_t)tn * S::n;
   const int64_t one = (*p.live + S::bk - 1) / S::bk;
-  const TlSplit split(sizeof(T) == 2 ? 2 * one : one, p.splits);
+  TlPart part;
+  if (!part.take(p.tiles_m, p.tiles_n, sizeof(T) == 2 ? 2 * one : one, p.w_most)) return;
+  const int64_t c0 = (int64_t)part.m * S::m, n0 = (int64_t)part.n * S::n;
   const A la(p.xT + c0 * p.ldt, p.ldt,
              [&](int r) { return c0 + r < p.C ? r : p.C - 1 - c0; });
   const B lb(p.d + n0 * p.ldt, p.ldt, [](int r) { return (int64_t)r; });
   PtSums<S> acc;
   pt_product<false, S, A, B>(
-      acc, smem, split.n,
+      acc, smem, part.count,
       [&](int64_t j, uint32_t to) {
-        const int64_t k = split.begin + j;
+        const int64_t k = part.begin + j;
         la.start((k < one ? k : k - one) * S::bk, p.tokens, to);
       },
       [&](int64_t j, uint32_t to) {
-        const int64_t k = split.begin + j;
+        const int64_t k = part.begin + j;
         lb.start((k < one ? k : k - one) * S::bk, p.tokens, to, k < one ? 0 : p.plane);
       });
   const int64_t rows = p.V - p.v_first < p.piece ? p.V - p.v_first : p.piece;
-  if (p.splits > 1)
-    tl_store(acc, p.sums + blockIdx.y * p.piece * p.C, p.C, n0, rows, c0, p.C, false);
+  if (part.splits > 1)
+    tl_store(acc, p.sums + part.split * rows * p.C, p.C, n0, rows, c0, p.C, false);
   else
     tl_store(acc, p.out + p.v_first * p.C, p.C, n0, rows, c0, p.C, p.accumulate);
 }
+
+// How a product was cut, for its join.
+struct TlCut {
+  int tile_m, tile_n, bk, planes;
+  int64_t launched;
+};
 
 // The splits of g_x joined and rounded, each listed row at its token's place, zeros at the others.
 template <typename T>
 __global__ __launch_bounds__(256) void k_tl_x_join(const float* sums, const int32_t* targets,
                                                    const int32_t* rows, const int64_t* live,
-                                                   T* g_x, int64_t tokens, int64_t capacity,
-                                                   int C, int splits) {
-  // one thread takes 4 columns
-  const int64_t quads = C / 4, n = *live;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < tokens * quads;
-       i += (int64_t)gridDim.x * 256) {
-    const int64_t r = i / quads, c = (i - r * quads) * 4;
-    if (r < n) {
-      f32x4 f = *reinterpret_cast<const f32x4*>(sums + r * C + c);
-      for (int s = 1; s < splits; ++s)
-        f += *reinterpret_cast<const f32x4*>(sums + ((int64_t)s * capacity + r) * C + c);
-      at_store4(g_x + (int64_t)rows[r] * C + c, f[0], f[1], f[2], f[3]);
+                                                   T* g_x, int64_t tokens, int64_t piece,
+                                                   int64_t budget, int C, TlCut cut) {
+  const int64_t n = *live;
+  const int64_t tiles = (int64_t)((C + cut.tile_m - 1) / cut.tile_m) *
+                        ((n + cut.tile_n - 1) / cut.tile_n);
+  const int splits = n ? tl_splits(tiles, piece / cut.bk, cut.launched, tl_most(budget, n, C)) : 1;
+  for (int64_t r = blockIdx.x; r < tokens; r += gridDim.x) {
+    T* to = g_x + (r < n ? rows[r] : 0) * (int64_t)C;
+    const bool absent = targets[r] < 0;
+    for (int c = 4 * threadIdx.x; c < C; c += 4 * 256) {
+      if (r < n) {
+        f32x4 f = *reinterpret_cast<const f32x4*>(sums + r * C + c);
+        for (int s = 1; s < splits; ++s)
+          f += *reinterpret_cast<const f32x4*>(sums + (s * n + r) * C + c);
+        at_store4(to + c, f[0], f[1], f[2], f[3]);
+      }
+      if (absent) at_store4(g_x + r * C + c, 0.0f, 0.0f, 0.0f, 0.0f);
     }
-    if (targets[r] < 0) at_store4(g_x + r * C + c, 0.0f, 0.0f, 0.0f, 0.0f);
   }
 }
 
-// The splits of a piece of g_W joined.
-__global__ __launch_bounds__(256) void k_tl_w_join(const float* sums, float* out, int64_t quads,
-                                                   int64_t each, int splits, int accumulate) {
+// The splits of a piece of g_W (`rows` rows) joined, where there are several.
+__global__ __launch_bounds__(256) void k_tl_w_join(const float* sums, const int64_t* live,
+                                                   float* out, int64_t rows, int C, int64_t most,
+                                                   int accumulate, TlCut cut) {
+  const int64_t tiles = (int64_t)((C + cut.tile_m - 1) / cut.tile_m) *
+                        ((rows + cut.tile_n - 1) / cut.tile_n);
+  const int64_t steps = cut.planes * ((*live + cut.bk - 1) / cut.bk), quads = rows * C / 4;
+  const int splits = tl_splits(tiles, steps, cut.launched, most);
+  if (splits == 1) return;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < quads; i += (int64_t)gridDim.x * 256) {
     f32x4 f = *reinterpret_cast<const f32x4*>(sums + 4 * i);
-    for (int s = 1; s < splits; ++s) f += *reinterpret_cast<const f32x4*>(sums + s * each + 4 * i);
+    for (int s = 1; s < splits; ++s)
+      f += *reinterpret_cast<const f32x4*>(sums + s * rows * C + 4 * i);
     if (accumulate) f += *reinterpret_cast<const f32x4*>(out + 4 * i);
     *reinterpret_cast<f32x4*>(out + 4 * i) = f;
   }
@@ -794,12 +848,67 @@ uint32_t blocks_of(int64_t x, int64_t each) {
   return (uint32_t)std::min<int64_t>(tiles_of(x, each), 1 << 16);
 }
 
-typedef PtShape<bf16, 8, 4, 2, 4> Big;                      // 256 x 256, 8 waves
-template <typename T> using Mid = PtShape<T, 4, 4, 2, 2>;   // 128 x 128, 4 waves
+// Two tiles for each type. fp32 products take sixteen times as long as bf16's, so smaller
+// tiles keep up with their loads.
+template <typename T> struct Tiles;
+template <> struct Tiles<bf16> {
+  typedef PtShape<bf16, 8, 4, 2, 4> Large;  // 256 x 256, 8 waves, one workgroup a compute unit
+  typedef PtShape<bf16, 4, 4, 2, 2> Small;  // 128 x 128, 4 waves, two of them
+};
+template <> struct Tiles<float> {
+  typedef PtShape<float, 4, 4, 2, 2> Large;  // 128 x 128, 4 waves, two of them
+  typedef PtShape<float, 2, 2, 2, 2> Small;  // 64 x 64, 4 waves, four of them
+};
 
 constexpr int64_t kCus = 256;
 constexpr int64_t kPieceBytes = int64_t(512) << 20;  // of d
-constexpr int kMostSplits = 16;
+constexpr int64_t kSumsBytes = int64_t(256) << 20;   // of the parts of g_x or g_W, where there are
+
+// How a product of m x n results over k is cut: its tile, and the workgroups launched,
+// which cut k into parts where there are more of them than tiles.
+struct Cut {
+  bool large;
+  int tile;
+  int64_t launched;
+  double cost;
+};
+
+// The cheaper tile, counted in steps of k that a compute unit spends on a small tile:
+// whole rounds of all units (in fp32 and half a one: tokens without a target leave the last
+// one fuller or emptier, and the small tile costs little more), 4 for a large tile and 1.3
+// for a small one (measured in bf16: 1,430 and 1,115 TFLOP/s where the rounds are full;
+// fp32: 129 and 122, 1.07), a tile's beginning and end as 300 steps more (fp32: 40), and the results' way through memory, `bytes` each
+// and 8 more for each part where there are several, at 4 TB/s. fp32, 1,866 tokens, half of
+// them without a target, over 4,099 words of 384, gradient: 140 us by this rule, 196 in
+// large tiles.
+Cut cut_of(int64_t m, int64_t n, int64_t k, double bytes, bool narrow, bool split) {
+  Cut best = {};
+  const double step = narrow ? 5.9e-9 : 1.4e-8;  // seconds
+  const int64_t bk = narrow ? 64 : 32;
+  for (int large = 0; large < 2; ++large) {
+    const int64_t tile = (narrow ? 128 : 64) << large;
+    const int64_t tiles = tiles_of(m, tile) * tiles_of(n, tile);
+    // as many workgroups as there is room for at a time
+    const int64_t room = kCus * (large ? (narrow ? 1 : 2) : (narrow ? 2 : 4));
+    const int64_t launched = split ? std::max(up(tiles, 8), room) : up(tiles, 8);
+    int64_t s = std::min<int64_t>(launched / up(tiles, 8), std::min<int64_t>(kMostSplits, k / (8 * bk)));
+    if (s < 1) s = 1;
+    const double cost = ((double)tiles_of(tiles * s, kCus) + (narrow ? 0.0 : 0.5)) *
+                            (large ? 4.0 : narrow ? 1.3 : 1.07) *
+                            ((double)tiles_of(k, s) + (narrow ? 300.0 : 40.0)) +
+                        (double)m * (double)n * ((s > 1 ? (double)s * 8.0 : 0.0) + bytes) / 4e12 / step;
+    if (!large || cost < best.cost) best = {large != 0, (int)tile, launched, cost};
+  }
+  return best;
+}
+
+struct Plan {
+  int64_t tokens, padded, piece, planes, ldv, ldt, x_budget;
+  int w_most;
+  Cut logits, singles, weights;
+  // the workspace
+  size_t rows, live, part, at, x, xT, WT, d, x_sums, w_sums, total;
+};
 
 // Tokens of a pass: an array of them spans 4 GiB at most, and the statistics of 128
 // rows of the vocabulary each 512 MiB (or those of 256 tokens).
@@ -807,44 +916,6 @@ int64_t pass_of(int64_t T, int64_t V) {
   const int64_t most = (int64_t(1) << 26) / tiles_of(V, 128) / 256 * 256;
   return std::min(T, std::max<int64_t>(256, std::min<int64_t>(most, 1 << 16)));
 }
-
-// How a product of m x n results over k is cut: into tiles of 256 x 256 or 128 x
-// 128, and k into parts.
-struct Cut {
-  bool big;
-  int splits;
-  double cost;
-};
-
-// The cheapest cut, counted in steps of k that a compute unit spends on 128 x
-// 128 results: whole rounds of all units, 4 for a large tile and 1.3 for a small one
-// (measured: 1,430 and 1,115 TFLOP/s where the rounds are full), a tile's beginning and end as
-// 300 steps more (fp32: 20), and the results' way through memory, `bytes` each (8 for each part
-// where there are several) at 4 TB/s. fp32 has the small tile only: its products take sixteen times as long, which
-// hides the loads of either.
-Cut cut_of(int64_t m, int64_t n, int64_t k, double bytes, bool narrow, bool split) {
-  Cut best = {false, 1, 0.0};
-  const double step = narrow ? 5.9e-9 : 5.6e-8;  // seconds
-  const int64_t bk = narrow ? 64 : 32;
-  for (int big = 0; big <= (narrow ? 1 : 0); ++big)
-    for (int s = 1; s <= (split ? kMostSplits : 1); ++s) {
-      if (s > 1 && k < 8 * bk * s) break;
-      const int64_t tile = big ? 256 : 128;
-      const int64_t rounds = tiles_of(tiles_of(m, tile) * tiles_of(n, tile) * s, kCus);
-      const double cost = (double)rounds * (big ? 4.0 : 1.3) *
-                              ((double)tiles_of(k, s) + (narrow ? 300.0 : 20.0)) +
-                          (double)m * (double)n * ((s > 1 ? s * 8.0 : 0.0) + bytes) / 4e12 / step;
-      if ((!big && s == 1) || cost < best.cost) best = {big != 0, s, cost};
-    }
-  return best;
-}
-
-struct Plan {
-  int64_t tokens, padded, piece, planes, ldv, ldt;
-  Cut logits, singles, weights;
-  // the workspace
-  size_t rows, live, part, at, x, xT, WT, d, x_sums, w_sums, total;
-};
 
 bool thin(int64_t T) { return T <= kThinTokens; }
 int thin_blocks(int64_t V) { return (int)std::min<int64_t>(tiles_of(V, 16 * kThinWaves), kThinBlocks); }
@@ -863,7 +934,7 @@ Plan forward_plan(int64_t T, int64_t V, int64_t C, nt_dtype dtype) {
   p.rows = at; at = align256(at + sizeof(int32_t) * p.tokens);
   p.live = at; at = align256(at + sizeof(int64_t));
   p.at = at; at = align256(at + sizeof(float) * p.tokens);
-  p.part = at; at = align256(at + sizeof(float2) * p.tokens * tiles_of(V, p.logits.big ? 256 : 128));
+  p.part = at; at = align256(at + sizeof(float2) * p.tokens * tiles_of(V, p.logits.tile));
   p.total = at;
   return p;
 }
@@ -880,10 +951,10 @@ Plan backward_plan(int64_t T, int64_t V, int64_t C, nt_dtype dtype) {
   // the number of pieces, from the least one on, that fills whole rounds best
   double best = 0.0;
   for (int64_t pieces = tiles_of(V, most), last = pieces + 8; pieces < last; ++pieces) {
-    const int64_t piece = up(tiles_of(V, pieces), 256);
-    const Cut l = cut_of(piece, p.tokens, C, (double)(es * p.planes), narrow, false);
-    const Cut x = cut_of(C, p.tokens, piece, 8.0, narrow, true);
-    const Cut w = cut_of(C, piece, p.planes * p.tokens, 4.0, narrow, true);
+    const int64_t piece = up(tiles_of(V, pieces), 256), n = std::min(piece, V);
+    const Cut l = cut_of(n, p.tokens, C, (double)(es * p.planes), narrow, false);
+    const Cut x = cut_of(C, p.tokens, n, 8.0, narrow, true);
+    const Cut w = cut_of(C, n, p.planes * p.tokens, 4.0, narrow, true);
     const double cost = (double)tiles_of(V, piece) * (l.cost + x.cost + w.cost);
     if (!p.piece || cost < best) {
       best = cost;
@@ -897,6 +968,16 @@ Plan backward_plan(int64_t T, int64_t V, int64_t C, nt_dtype dtype) {
   // channel of the cache: a line more
   p.ldv = p.piece + 128 / es;
   p.ldt = p.padded + 128 / es;
+  const int64_t numbers = kSumsBytes / (int64_t)sizeof(float);
+  // room for all parts that the workgroups allow, or for 256 MiB of them (fewer tokens with
+  // a target allow more parts of fewer rows, which take no more room)
+  const int64_t x_tiles = tiles_of(C, p.singles.tile) * tiles_of(p.tokens, p.singles.tile);
+  const int64_t x_parts = std::min<int64_t>(kMostSplits, p.singles.launched / up(x_tiles, 8));
+  p.x_budget = std::max(p.padded * C, std::min(x_parts * p.padded * C, numbers));
+  const int64_t w_tiles = tiles_of(C, p.weights.tile) * tiles_of(std::min(p.piece, V), p.weights.tile);
+  const int64_t w_rows = std::min(p.piece, V) * C;
+  p.w_most = (int)std::max<int64_t>(
+      1, std::min(std::min<int64_t>(kMostSplits, p.weights.launched / up(w_tiles, 8)), numbers / w_rows));
   size_t at = 0;
   p.rows = at; at = align256(at + sizeof(int32_t) * p.tokens);
   p.live = at; at = align256(at + sizeof(int64_t));
@@ -904,9 +985,9 @@ Plan backward_plan(int64_t T, int64_t V, int64_t C, nt_dtype dtype) {
   p.xT = at; at = align256(at + es * p.ldt * C);
   p.WT = at; at = align256(at + es * p.ldv * C);
   p.d = at; at = align256(at + es * p.planes * p.ldt * p.piece);
-  p.x_sums = at; at = align256(at + sizeof(float) * p.singles.splits * p.padded * C);
+  p.x_sums = at; at = align256(at + sizeof(float) * p.x_budget);
   p.w_sums = at;
-  if (p.weights.splits > 1) at = align256(at + sizeof(float) * p.weights.splits * p.piece * C);
+  if (p.w_most > 1) at = align256(at + sizeof(float) * p.w_most * w_rows);
   p.total = at;
   return p;
 }
@@ -921,8 +1002,7 @@ hipError_t list(const int32_t* targets, int64_t tokens, int32_t* rows, int64_t* 
 template <typename S>
 hipError_t run_forward(TlForward<typename S::type> a, float* nll, float* lse, hipStream_t s) {
   a.tiles_m = (uint32_t)tiles_of(a.V, S::m);
-  a.tiles_n = (uint32_t)tiles_of(a.tokens, S::n);
-  k_tl_forward<S><<<(uint32_t)pt_grid((int64_t)a.tiles_m * a.tiles_n), S::threads, 0, s>>>(a);
+  k_tl_forward<S><<<(uint32_t)up(a.tiles_m * tiles_of(a.tokens, S::n), 8), S::threads, 0, s>>>(a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   k_tl_join<<<blocks_of(a.tokens, 16), 256, 0, s>>>(a.part, a.at, a.targets, a.rows, a.live, nll,
@@ -963,12 +1043,9 @@ hipError_t forward(const T* x, const T* W, const int32_t* targets, float* nll, f
     if (e != hipSuccess) return e;
     const TlForward<T> a = {x + t * C, W, targets + t, rows, live,
                             reinterpret_cast<float2*>(ws + p.part),
-                            reinterpret_cast<float*>(ws + p.at), n, V, C, scale * kLog2e, 0, 0};
-    if constexpr (sizeof(T) == 2)
-      e = p.logits.big ? run_forward<Big>(a, nll + t, lse + t, s)
-                       : run_forward<Mid<T>>(a, nll + t, lse + t, s);
-    else
-      e = run_forward<Mid<T>>(a, nll + t, lse + t, s);
+                            reinterpret_cast<float*>(ws + p.at), n, V, C, scale * kLog2e, 0};
+    e = p.logits.large ? run_forward<typename Tiles<T>::Large>(a, nll + t, lse + t, s)
+                       : run_forward<typename Tiles<T>::Small>(a, nll + t, lse + t, s);
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
@@ -977,25 +1054,29 @@ hipError_t forward(const T* x, const T* W, const int32_t* targets, float* nll, f
 // One of the gradient's products, m x n results.
 enum Product { kLogits, kSingles, kWeights };
 template <typename S, Product P>
-hipError_t run_tiles(TlGrad<typename S::type> a, int64_t m, int64_t n, hipStream_t s) {
+hipError_t run_tiles(TlGrad<typename S::type> a, const Cut& cut, int64_t m, int64_t n,
+                     hipStream_t s) {
   a.tiles_m = (uint32_t)tiles_of(m, S::m);
   a.tiles_n = (uint32_t)tiles_of(n, S::n);
-  const dim3 grid((uint32_t)pt_grid((int64_t)a.tiles_m * a.tiles_n), a.splits);
+  const uint32_t grid = (uint32_t)std::max(cut.launched, up((int64_t)a.tiles_m * a.tiles_n, 8));
   if constexpr (P == kLogits) k_tl_logit_grad<S><<<grid, S::threads, 0, s>>>(a);
   if constexpr (P == kSingles) k_tl_x_grad<S><<<grid, S::threads, 0, s>>>(a);
   if constexpr (P == kWeights) k_tl_w_grad<S><<<grid, S::threads, 0, s>>>(a);
   return hipGetLastError();
 }
 template <Product P, typename T>
-hipError_t run_product(TlGrad<T> a, const Cut& cut, int64_t m, int64_t n, hipStream_t s) {
-  a.splits = cut.splits;
-  if constexpr (sizeof(T) == 2)
-    if (cut.big) return run_tiles<Big, P>(a, m, n, s);
-  return run_tiles<Mid<T>, P>(a, m, n, s);
+hipError_t run_product(const TlGrad<T>& a, const Cut& cut, int64_t m, int64_t n, hipStream_t s) {
+  if (cut.large) return run_tiles<typename Tiles<T>::Large, P>(a, cut, m, n, s);
+  return run_tiles<typename Tiles<T>::Small, P>(a, cut, m, n, s);
 }
 
-template <typename T> hipError_t transpose(const TlTranspose<T>& a, int64_t rows, hipStream_t s) {
-  k_tl_transpose<T><<<dim3((uint32_t)(up(rows, 256) / 64), (uint32_t)tiles_of(a.C, 64)), 256, 0, s>>>(a);
+// b: with `b_rows` rows, or none of them.
+template <typename T>
+hipError_t transpose(const TlTranspose<T>& a, int64_t a_rows, const TlTranspose<T>& b,
+                     int64_t b_rows, hipStream_t s) {
+  const int64_t rows = std::max(a_rows, b_rows);
+  const dim3 grid((uint32_t)(up(rows, 256) / 64), (uint32_t)tiles_of(a.C, 64), b_rows ? 2 : 1);
+  k_tl_transpose<T><<<grid, 256, 0, s>>>(a, b);
   return hipGetLastError();
 }
 
@@ -1011,13 +1092,20 @@ hipError_t backward(const Plan& p, const T* x, const T* W, const int32_t* target
   T* WT = reinterpret_cast<T*>(ws + p.WT);
   hipError_t e = list(targets, tokens, rows, live, nullptr, nullptr, s);
   if (e != hipSuccess) return e;
-  e = transpose(TlTranspose<T>{x, g_W ? xT : nullptr, xs, rows, live, tokens, p.ldt, C}, tokens, s);
+  // x, and the first piece of W
+  const auto piece = [&](int64_t v, int64_t n) {
+    return TlTranspose<T>{W + v * C, WT, nullptr, nullptr, nullptr, n, p.ldv, C};
+  };
+  const int64_t first = std::min(p.piece, V);
+  e = transpose(TlTranspose<T>{x, g_W ? xT : nullptr, xs, rows, live, tokens, p.ldt, C}, tokens,
+                piece(0, first), g_x ? first : 0, s);
   if (e != hipSuccess) return e;
   TlGrad<T> a = {xs, xT, W, WT, targets, rows, live, lse, g_nll, g_lse,
                  reinterpret_cast<T*>(ws + p.d), p.ldt * p.piece, p.piece, p.ldv, p.ldt, 0, V,
-                 nullptr, g_W, p.padded, C, 1, 0, scale, scale * kLog2e, 0, 0};
+                 nullptr, g_W, p.padded, p.x_budget, C, p.w_most, 0, scale, scale * kLog2e, 0, 0};
   float* x_sums = reinterpret_cast<float*>(ws + p.x_sums);
   float* w_sums = reinterpret_cast<float*>(ws + p.w_sums);
+  const int bk = 128 / (int)sizeof(T);
   for (int64_t v = 0; v < V; v += p.piece) {
     const int64_t n = std::min(p.piece, V - v);
     a.v_first = v;
@@ -1025,7 +1113,7 @@ hipError_t backward(const Plan& p, const T* x, const T* W, const int32_t* target
     e = run_product<kLogits>(a, p.logits, up(n, 256), tokens, s);
     if (e != hipSuccess) return e;
     if (g_x) {
-      e = transpose(TlTranspose<T>{W + v * C, WT, nullptr, nullptr, nullptr, n, p.ldv, C}, n, s);
+      if (v) e = transpose(piece(v, n), n, piece(v, n), 0, s);
       if (e != hipSuccess) return e;
       a.sums = x_sums;
       a.accumulate = v > 0;
@@ -1037,18 +1125,24 @@ hipError_t backward(const Plan& p, const T* x, const T* W, const int32_t* target
       a.accumulate = accumulate;
       e = run_product<kWeights>(a, p.weights, C, n, s);
       if (e != hipSuccess) return e;
-      if (p.weights.splits > 1) {
-        const int64_t quads = n * C / 4;
-        k_tl_w_join<<<blocks_of(quads, 256), 256, 0, s>>>(w_sums, g_W + v * C, quads, p.piece * C,
-                                                          p.weights.splits, accumulate);
+      if (p.w_most > 1) {
+        const int t = p.weights.tile;
+        const int64_t launched =
+            std::max(p.weights.launched, up(tiles_of(C, t) * tiles_of(n, t), 8));
+        k_tl_w_join<<<blocks_of(n * C / 4, 256), 256, 0, s>>>(
+            w_sums, live, g_W + v * C, n, C, p.w_most, accumulate,
+            TlCut{t, t, bk, (int)p.planes, launched});
         e = hipGetLastError();
         if (e != hipSuccess) return e;
       }
     }
   }
   if (!g_x) return hipSuccess;
-  k_tl_x_join<T><<<blocks_of(tokens * (C / 4), 256), 256, 0, s>>>(
-      x_sums, targets, rows, live, g_x, tokens, p.padded, C, p.singles.splits);
+  const int t = p.singles.tile;
+  const int64_t launched = std::max(p.singles.launched, up(tiles_of(C, t) * tiles_of(tokens, t), 8));
+  k_tl_x_join<T><<<blocks_of(tokens, 1), 256, 0, s>>>(
+      x_sums, targets, rows, live, g_x, tokens, p.piece, p.x_budget, C,
+      TlCut{t, t, bk, (int)p.planes, launched});
   return hipGetLastError();
 }
 
