@@ -8,6 +8,7 @@ marshal pointers, and the library computes.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 from . import _check, _code, _dtype_code, _native
 from ._native import NT_OK
@@ -45,9 +46,11 @@ def _tokens(torch, device, name, t, count) -> None:
     _expect(device, name, t, (count,), torch.int32)
 
 
-def _bytes(entry, *args) -> int:
+@functools.lru_cache(maxsize=256)
+def _bytes(name, *args) -> int:
+    """Workspace bytes, which the sizes alone decide."""
     b = ctypes.c_size_t()
-    status = entry(*args, ctypes.byref(b))
+    status = getattr(_native.lib(), name)(*args, ctypes.byref(b))
     if status != NT_OK:
         _check(status)
     return b.value
@@ -64,7 +67,7 @@ def nt_token_embedding(table, tokens, scale: float = 1.0, out=None, stream=None)
     T = tokens.shape[0]
     with _on(torch, dev, stream) as s:
         if out is None:
-            out = torch.empty((T, C), dtype=table.dtype, device=dev)
+            out = table.new_empty((T, C))
         else:
             _expect(dev, "out", out, (T, C), table.dtype)
         status = lib.nt_token_embedding(_at(table), _at(tokens), _at(out), T, V, C, scale, code, s)
@@ -74,7 +77,7 @@ def nt_token_embedding(table, tokens, scale: float = 1.0, out=None, stream=None)
 
 
 def nt_token_embedding_backward_workspace_bytes(tokens: int, vocabulary: int, width: int) -> int:
-    return _bytes(_native.lib().nt_token_embedding_backward_workspace_bytes, tokens, vocabulary,
+    return _bytes("nt_token_embedding_backward_workspace_bytes", tokens, vocabulary,
                   width)
 
 
@@ -89,7 +92,7 @@ def nt_token_embedding_backward(tokens, g_out, vocabulary: int, scale: float = 1
     if accumulate and g_table is None:
         raise ValueError("accumulate needs g_table")
     with _on(torch, dev, stream) as s:
-        need = _bytes(lib.nt_token_embedding_backward_workspace_bytes, T, vocabulary, C)
+        need = _bytes("nt_token_embedding_backward_workspace_bytes", T, vocabulary, C)
         if g_table is None:
             g_table = torch.empty((vocabulary, C), dtype=torch.float32, device=dev)
         else:
@@ -111,7 +114,7 @@ def _sum_of(torch, dev, x, residual, h):
         return x
     _expect(dev, "residual", residual, x.shape, x.dtype)
     if h is None:
-        return torch.empty(x.shape, dtype=x.dtype, device=dev)
+        return torch.empty_like(x)
     _expect(dev, "h", h, x.shape, x.dtype)
     return h
 
@@ -127,7 +130,7 @@ def nt_residual_norm(x, w=None, residual=None, eps: float = 1e-6, y=None, h=None
     with _on(torch, dev, stream) as s:
         h = _sum_of(torch, dev, x, residual, h)
         if y is None:
-            y = torch.empty((T, C), dtype=x.dtype, device=dev)
+            y = torch.empty_like(x)
         else:
             _expect(dev, "y", y, (T, C), x.dtype)
         status = lib.nt_residual_norm(_at(x), _at(residual), _at(w),
@@ -153,11 +156,11 @@ def nt_residual_norm_8bit(x, w=None, residual=None, eps: float = 1e-6, group: in
     with _on(torch, dev, stream) as s:
         h = _sum_of(torch, dev, x, residual, h)
         if codes is None:
-            codes = torch.empty((T, C), dtype=torch.float8_e4m3fn, device=dev)
+            codes = torch.empty_like(x, dtype=torch.float8_e4m3fn)
         else:
             _expect(dev, "codes", codes, (T, C), torch.float8_e4m3fn)
         if scales is None:
-            scales = torch.empty(shape, dtype=torch.float32, device=dev)
+            scales = x.new_empty(shape, dtype=torch.float32)
         else:
             _expect(dev, "scales", scales, shape, torch.float32)
         status = lib.nt_residual_norm_8bit(_at(x), _at(residual), _at(w),
@@ -169,7 +172,7 @@ def nt_residual_norm_8bit(x, w=None, residual=None, eps: float = 1e-6, group: in
 
 
 def nt_residual_norm_backward_workspace_bytes(tokens: int, width: int) -> int:
-    return _bytes(_native.lib().nt_residual_norm_backward_workspace_bytes, tokens, width)
+    return _bytes("nt_residual_norm_backward_workspace_bytes", tokens, width)
 
 
 def nt_residual_norm_backward(h, g_y, w=None, g_h=None, eps: float = 1e-6, g=None, g_w=None,
@@ -185,16 +188,16 @@ def nt_residual_norm_backward(h, g_y, w=None, g_h=None, eps: float = 1e-6, g=Non
     _expect(dev, "w", w, (C,), torch.float32)
     with _on(torch, dev, stream) as s:
         if g is None:
-            g = torch.empty((T, C), dtype=dt, device=dev)
+            g = torch.empty_like(h)
         else:
             _expect(dev, "g", g, shape, dt)
         need = 0
         if w is None:
             g_w = None
         else:
-            need = _bytes(lib.nt_residual_norm_backward_workspace_bytes, T, C)
+            need = _bytes("nt_residual_norm_backward_workspace_bytes", T, C)
             if g_w is None:
-                g_w = torch.empty((C,), dtype=torch.float32, device=dev)
+                g_w = torch.empty_like(w)
             else:
                 _expect(dev, "g_w", g_w, (C,), torch.float32)
         ws, have, workspace = _workspace(torch, dev, workspace, need)
@@ -206,13 +209,13 @@ def nt_residual_norm_backward(h, g_y, w=None, g_h=None, eps: float = 1e-6, g=Non
 
 
 def nt_token_loss_workspace_bytes(tokens: int, vocabulary: int, width: int, dtype) -> int:
-    return _bytes(_native.lib().nt_token_loss_workspace_bytes, tokens, vocabulary, width,
+    return _bytes("nt_token_loss_workspace_bytes", tokens, vocabulary, width,
                   _code(dtype))
 
 
 def nt_token_loss_backward_workspace_bytes(tokens: int, vocabulary: int, width: int,
                                            dtype) -> int:
-    return _bytes(_native.lib().nt_token_loss_backward_workspace_bytes, tokens, vocabulary, width,
+    return _bytes("nt_token_loss_backward_workspace_bytes", tokens, vocabulary, width,
                   _code(dtype))
 
 
@@ -234,7 +237,7 @@ def nt_token_loss(x, W, targets, scale: float = 1.0, nll=None, lse=None, workspa
     code, dev, f32 = _dtype_code(x), x.device, torch.float32
     T, V, C = _loss_inputs(torch, dev, x, W, targets)
     with _on(torch, dev, stream) as s:
-        need = _bytes(lib.nt_token_loss_workspace_bytes, T, V, C, code)
+        need = _bytes("nt_token_loss_workspace_bytes", T, V, C, code)
         if nll is None:
             nll = torch.empty((T,), dtype=f32, device=dev)
         else:
@@ -268,9 +271,9 @@ def nt_token_loss_backward(x, W, targets, lse, g_nll, g_lse=None, scale: float =
     if g_W is not None and not weight_grad:
         raise ValueError("g_W without weight_grad")
     with _on(torch, dev, stream) as s:
-        need = _bytes(lib.nt_token_loss_backward_workspace_bytes, T, V, C, code)
+        need = _bytes("nt_token_loss_backward_workspace_bytes", T, V, C, code)
         if g_x is None:
-            g_x = torch.empty((T, C), dtype=x.dtype, device=dev)
+            g_x = torch.empty_like(x)
         else:
             _expect(dev, "g_x", g_x, (T, C), x.dtype)
         if g_W is not None:

@@ -6,16 +6,19 @@
 //
 // Gradient: g_table[v] = scale sum over the places t of token v of g[t], in the
 // places' order whatever the launch does (no atomics on values). Three kernels:
-// 1. Sort. Each workgroup owns a range of the vocabulary and reads all tokens
-//    (from cache: 4 bytes each): it counts those below its range, which is where
-//    its own go in the sorted order, and lists its own in order, so one launch
-//    sorts without an exchange between workgroups. Its list is then sorted by
-//    token in LDS counters, one set a wave. The rows of absent tokens get
-//    their zeros here.
+// 1. Sort. Each workgroup owns every W-th token of the vocabulary (W a power of two:
+//    the frequent ones, which often stand together, are spread) and reads all
+//    tokens (from cache: 4 bytes each): it counts those of the workgroups before it,
+//    which is where its own go in the sorted order, and lists its own in order, so
+//    one launch sorts without an exchange between workgroups. Its list is then
+//    sorted by token in LDS counters, one set a wave.
 // 2. Sums. The sorted places are cut into parts of equal length, so that a token
 //    that is everywhere costs no more than many rare ones. A team of lanes
 //    adds the rows of a part, 8 columns a lane, and writes a token's row at the
-//    end of its run; runs that cross the part's ends go to the workspace.
+//    end of its run; runs that cross the part's ends go to the workspace. Workgroups
+//    behind the parts' write the zeros of the tokens that no place holds, which is most
+//    of what a large vocabulary moves (in the first kernel they kept the sums waiting:
+//    67 us where this takes @, 16,384 places over 50,021 tokens of 1,024).
 // 3. Join. The part where a crossing run begins adds its pieces in order.
 // Few places over a small vocabulary (an alphabet) take one launch instead: a workgroup
 // for each token and 64 columns lists the token's places and adds their rows.
@@ -30,9 +33,10 @@ namespace {
 constexpr int kTeThreads = 256;
 constexpr int kTeSortThreads = 1024;
 constexpr int kTeSortWaves = kTeSortThreads / 64;
-constexpr int kTeRange = 512;       // most tokens of a workgroup's range
+constexpr int kTeRange = 512;       // most tokens of a workgroup
 constexpr int kTeAhead = 8;         // rows in flight
 constexpr int64_t kTeMostGrid = int64_t(1) << 20;
+constexpr int64_t kTeZeroBlocks = 1024;  // four for each compute unit
 
 template <typename T> __device__ __forceinline__ void te_load(const T* p, float* f);
 template <> __device__ __forceinline__ void te_load<bf16>(const bf16* p, float* f) {
@@ -81,42 +85,56 @@ __global__ __launch_bounds__(kTeThreads) void k_te_lookup(const T* table, const 
 }
 
 struct TeSorted {
-  int2* list;       // a range's places and tokens within the range, in order
+  int2* list;       // a workgroup's places and its number of their tokens, in order
   int32_t* place;   // sorted
   int32_t* token;   // of each sorted place
   int64_t* count;   // of places that hold a token of the table
+  uint8_t* held;    // whether a place holds each token
 };
 
 __global__ __launch_bounds__(kTeSortThreads) void k_te_sort(const int32_t* tokens, int64_t n,
-                                                            int64_t V, int range, TeSorted s,
-                                                            float* g_table, int C, int zero) {
+                                                            int64_t V, int shift, TeSorted s) {
   __shared__ int64_t below[kTeSortWaves], inside[kTeSortWaves];
   __shared__ int32_t counts[kTeSortWaves][kTeRange];
   __shared__ int32_t sums[kTeSortWaves];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t first = (int64_t)blockIdx.x * range;
-  const uint32_t lo = (uint32_t)first;
-  const uint32_t have = (uint32_t)(V - first < range ? V - first : range);
-  // a wave takes a stretch of the places; absent tokens are large unsigned numbers
-  const int64_t each = ((n + kTeSortWaves - 1) / kTeSortWaves + 63) / 64 * 64;
+  // its tokens are blockIdx.x + (k << shift), k below `have`
+  const uint32_t mask = (1u << shift) - 1, mine = blockIdx.x, all_tokens = (uint32_t)V;
+  const uint32_t have = (all_tokens - mine + mask) >> shift;
+  for (int k = threadIdx.x; k < kTeSortWaves * kTeRange; k += kTeSortThreads) (&counts[0][0])[k] = 0;
+  // A wave takes a stretch of the places, 4 neighbouring ones a lane at a time; absent
+  // tokens are large unsigned numbers.
+  const int64_t each = ((n + kTeSortWaves - 1) / kTeSortWaves + 255) / 256 * 256;
   const int64_t begin = std::min<int64_t>(n, wave * each), end = std::min<int64_t>(n, begin + each);
-  int64_t under = 0, mine = 0;
-  for (int64_t i = begin; i < end; i += 512) {
-    uint32_t x[8];
+  const auto load = [&](int64_t i, uint32_t (&x)[4]) {
+    if (i + 4 <= end) {
+      __builtin_memcpy(x, tokens + i, 16);
+    } else {
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const int64_t at = i + 64 * u + lane;
-      x[u] = at < end ? (uint32_t)tokens[at] : 0xffffffffu;
+      for (int e = 0; e < 4; ++e) x[e] = i + e < end ? (uint32_t)tokens[i + e] : 0xffffffffu;
     }
+  };
+  int under = 0, own = 0;
+  for (int64_t i = begin + 4 * lane; i < end; i += 1024) {
+    uint32_t x[4][4];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      under += __popcll(__ballot(x[u] < lo));
-      mine += __popcll(__ballot(x[u] - lo < have));
-    }
+    for (int u = 0; u < 4; ++u) load(i + 256 * u, x[u]);
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        under += x[u][e] < all_tokens && (x[u][e] & mask) < mine;
+        own += x[u][e] < all_tokens && (x[u][e] & mask) == mine;
+      }
+  }
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) {
+    under += __shfl_xor(under, m);
+    own += __shfl_xor(own, m);
   }
   if (lane == 0) {
     below[wave] = under;
-    inside[wave] = mine;
+    inside[wave] = own;
   }
   __syncthreads();
   int64_t base = 0, total = 0, at = 0;
@@ -125,30 +143,44 @@ __global__ __launch_bounds__(kTeSortThreads) void k_te_sort(const int32_t* token
     if (w < wave) at += inside[w];
     total += inside[w];
   }
-  if (first + range >= V && threadIdx.x == 0) *s.count = base + total;
-  for (int64_t i = begin; mine && i < end; i += 512) {
-    uint32_t x[8];
+  if (blockIdx.x == gridDim.x - 1 && threadIdx.x == 0) *s.count = base + total;
+  for (int64_t i0 = begin; own && i0 < end; i0 += 1024) {
+    const int64_t i = i0 + 4 * lane;
+    uint32_t x[4][4];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const int64_t k = i + 64 * u + lane;
-      x[u] = k < end ? (uint32_t)tokens[k] : 0xffffffffu;
-    }
+    for (int u = 0; u < 4; ++u) load(i + 256 * u, x[u]);
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const bool is = x[u] - lo < have;
-      const unsigned long long who = __ballot(is);
-      if (is)
-        s.list[base + at + __popcll(who & ((1ull << lane) - 1))] =
-            make_int2((int)(i + 64 * u + lane), (int)(x[u] - lo));
-      at += __popcll(who);
+    for (int u = 0; u < 4; ++u) {
+      // behind the matches of the lanes before this one, then its own in order
+      int place = 0, all = 0;
+      bool is[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        is[e] = x[u][e] < all_tokens && (x[u][e] & mask) == mine;
+        const unsigned long long who = __ballot(is[e]);
+        place += __popcll(who & ((1ull << lane) - 1));
+        all += __popcll(who);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (is[e])
+          s.list[base + at + place++] =
+              make_int2((int)(i + 256 * u + e), (int)(x[u][e] >> shift));
+      at += all;
     }
   }
-  for (int k = threadIdx.x; k < kTeSortWaves * kTeRange; k += kTeSortThreads) (&counts[0][0])[k] = 0;
   __syncthreads();
   // how often each wave's stretch of the list holds each token
   const int64_t part = (total + kTeSortWaves - 1) / kTeSortWaves;
   const int64_t l0 = std::min<int64_t>(total, wave * part), l1 = std::min<int64_t>(total, l0 + part);
-  for (int64_t i = l0 + lane; i < l1; i += 64) atomicAdd(&counts[wave][s.list[base + i].y], 1);
+  for (int64_t i = l0 + lane; i < l1; i += 64 * kTeAhead) {
+    int x[kTeAhead];
+#pragma unroll
+    for (int u = 0; u < kTeAhead; ++u) x[u] = i + 64 * u < l1 ? s.list[base + i + 64 * u].y : 0;
+#pragma unroll
+    for (int u = 0; u < kTeAhead; ++u)
+      if (i + 64 * u < l1) atomicAdd(&counts[wave][x[u]], 1);
+  }
   __syncthreads();
   // the first place of each token and wave: a token a thread, then over the tokens
   int all = 0;
@@ -170,40 +202,36 @@ __global__ __launch_bounds__(kTeSortThreads) void k_te_sort(const int32_t* token
       counts[w][threadIdx.x] = before;
       before += x;
     }
-  // rows of the table that no place holds
-  if (zero) {
-    __shared__ uint8_t held[kTeRange];
-    if (threadIdx.x < kTeRange) held[threadIdx.x] = all != 0;
-    __syncthreads();
-    const int quads = C / 4;
-    for (uint32_t v = wave; v < have; v += kTeSortWaves)
-      if (!held[v])
-        for (int c = lane; c < quads; c += 64)
-          *reinterpret_cast<f32x4*>(g_table + (first + v) * C + 4 * c) =
-              f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  } else {
-    __syncthreads();
-  }
+  if (threadIdx.x < have) s.held[mine + ((int64_t)threadIdx.x << shift)] = all != 0;
+  __syncthreads();
   // places of equal tokens keep their order: the wave's next place of the token,
   // and behind it one for each earlier lane with the same token
-  for (int64_t i = l0; i < l1; i += 64) {
-    const bool is = i + lane < l1;
-    const int2 x = is ? s.list[base + i + lane] : make_int2(0, 0);
-    unsigned long long same = __ballot(is);
+  for (int64_t i = l0; i < l1; i += 64 * kTeAhead) {
+    int2 ahead[kTeAhead];
 #pragma unroll
-    for (int b = 0; b < 9; ++b) {
-      const unsigned long long one = __ballot(x.y >> b & 1);
-      same &= x.y >> b & 1 ? one : ~one;
+    for (int u = 0; u < kTeAhead; ++u)
+      ahead[u] = i + 64 * u + lane < l1 ? s.list[base + i + 64 * u + lane] : make_int2(0, 0);
+#pragma unroll
+    for (int u = 0; u < kTeAhead; ++u) {
+      if (i + 64 * u >= l1) break;
+      const bool is = i + 64 * u + lane < l1;
+      const int2 x = ahead[u];
+      unsigned long long same = __ballot(is);
+#pragma unroll
+      for (int b = 0; b < 9; ++b) {
+        const unsigned long long one = __ballot(x.y >> b & 1);
+        same &= x.y >> b & 1 ? one : ~one;
+      }
+      if (is) {
+        const int rank = __popcll(same & ((1ull << lane) - 1));
+        const int to = counts[wave][x.y] + rank;
+        s.place[base + to] = x.x;
+        s.token[base + to] = (int)(mine + ((uint32_t)x.y << shift));
+      }
+      __builtin_amdgcn_wave_barrier();
+      if (is && same >> lane == 1) counts[wave][x.y] += __popcll(same);
+      __builtin_amdgcn_wave_barrier();
     }
-    if (is) {
-      const int rank = __popcll(same & ((1ull << lane) - 1));
-      const int to = counts[wave][x.y] + rank;
-      s.place[base + to] = x.x;
-      s.token[base + to] = x.y + (int)lo;
-    }
-    __builtin_amdgcn_wave_barrier();
-    if (is && same >> lane == 1) counts[wave][x.y] += __popcll(same);
-    __builtin_amdgcn_wave_barrier();
   }
 }
 
@@ -214,8 +242,10 @@ template <typename T> struct TeSums {
   const int32_t* place;
   const int32_t* token;
   const int64_t* count;
-  int64_t parts;
+  const uint8_t* held;
+  int64_t parts, V;
   int part, C, accumulate;
+  int blocks;             // workgroups of the sums; the ones behind them write zeros
   float scale;
 };
 
@@ -233,8 +263,22 @@ __device__ __forceinline__ void te_row(const TeSums<T>& p, int64_t token, int c,
   te_store(to, f);
 }
 
+// Zeros in the rows of tokens that no place holds, a wave a row.
+template <typename T> __device__ __forceinline__ void te_zeros(const TeSums<T>& p) {
+  const int64_t step = (int64_t)(gridDim.x - p.blocks) * (kTeThreads / 64);
+  for (int64_t v = (int64_t)(blockIdx.x - p.blocks) * (kTeThreads / 64) + threadIdx.x / 64; v < p.V;
+       v += step)
+    if (!p.held[v])
+      for (int c = (threadIdx.x & 63) * 4; c < p.C; c += 256)
+        *reinterpret_cast<f32x4*>(p.g_table + v * p.C + c) = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+}
+
 template <typename T, int LANES>
 __global__ __launch_bounds__(kTeThreads) void k_te_sums(TeSums<T> p) {
+  if ((int)blockIdx.x >= p.blocks) {
+    if (blockIdx.y == 0) te_zeros(p);
+    return;
+  }
   const int64_t k = (int64_t)blockIdx.x * (kTeThreads / LANES) + threadIdx.x / LANES;
   const int c = (int)(blockIdx.y * LANES + threadIdx.x % LANES) * 8;
   const int64_t n = *p.count, begin = k * p.part;
@@ -288,12 +332,16 @@ __global__ __launch_bounds__(kTeThreads) void k_te_join(TeSums<T> p) {
   if (end >= n) return;
   const int now = p.token[end - 1];
   if (p.token[end] != now || (begin && p.token[begin - 1] == now)) return;
-  int64_t lo = end, hi = n;  // the run's end: the first place in (end, n] of another token
-  while (lo < hi) {
-    const int64_t mid = (lo + hi) / 2;
-    if (p.token[mid] == now) lo = mid + 1; else hi = mid;
+  // the last part that begins with the run's token, 64 parts looked at at once
+  int64_t last = k + 1;
+  for (;;) {
+    const int64_t next = last + 1 + (threadIdx.x & 63);
+    const bool on = next < p.parts && next * p.part < n && p.token[next * p.part] == now;
+    const int more = __popcll(__ballot(on));
+    last += more;
+    if (more < 64) break;
   }
-  const int64_t last = (lo - 1) / p.part, pieces = last - k + 1;
+  const int64_t pieces = last - k + 1;
   const int team = threadIdx.x / LANES, c = (int)(blockIdx.y * LANES + threadIdx.x % LANES) * 8;
   const int64_t each = (pieces + kTeams - 1) / kTeams;
   const int64_t from = k + team * each, to = from + each < last + 1 ? from + each : last + 1;
@@ -417,8 +465,8 @@ template <int MOST, typename Run> hipError_t te_teams(int C, const Run& run) {
 
 struct Plan {
   int64_t parts;
-  int part, range;
-  size_t list, place, token, count, pieces, total;
+  int part, shift;
+  size_t list, place, token, count, held, pieces, total;
 };
 
 Plan plan_of(int64_t T, int64_t V, int C) {
@@ -426,13 +474,15 @@ Plan plan_of(int64_t T, int64_t V, int C) {
   // 16 places a part, more of them where that would be over 2,048 parts
   p.part = (int)std::max<int64_t>(16, (T + 2047) / 2048);
   p.parts = (T + p.part - 1) / p.part;
-  // two workgroups for each compute unit, or more where a range would be too long
-  p.range = (int)std::min<int64_t>(kTeRange, (V + 511) / 512);
+  // a workgroup for each compute unit, or more where one would have too many tokens
+  p.shift = 8;
+  while ((V >> p.shift) >= kTeRange) ++p.shift;
   size_t at = 0;
   p.list = at; at = align256(at + sizeof(int2) * T);
   p.place = at; at = align256(at + sizeof(int32_t) * T);
   p.token = at; at = align256(at + sizeof(int32_t) * T);
   p.count = at; at = align256(at + sizeof(int64_t));
+  p.held = at; at = align256(at + V);
   p.pieces = at; at = align256(at + sizeof(float) * 2 * p.parts * C);
   p.total = at;
   return p;
@@ -463,19 +513,22 @@ hipError_t backward(const int32_t* tokens, const void* g, float* g_table, int64_
   const TeSorted sorted = {reinterpret_cast<int2*>(ws + p.list),
                            reinterpret_cast<int32_t*>(ws + p.place),
                            reinterpret_cast<int32_t*>(ws + p.token),
-                           reinterpret_cast<int64_t*>(ws + p.count)};
-  k_te_sort<<<(uint32_t)((V + p.range - 1) / p.range), kTeSortThreads, 0, s>>>(
-      tokens, n, V, p.range, sorted, g_table, C, !accumulate);
+                           reinterpret_cast<int64_t*>(ws + p.count),
+                           reinterpret_cast<uint8_t*>(ws + p.held)};
+  k_te_sort<<<(uint32_t)std::min<int64_t>(V, int64_t(1) << p.shift), kTeSortThreads, 0, s>>>(
+      tokens, n, V, p.shift, sorted);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const TeSums<T> a = {static_cast<const T*>(g), g_table, reinterpret_cast<float*>(ws + p.pieces),
-                       sorted.place, sorted.token, sorted.count, p.parts, p.part, C, accumulate,
-                       scale};
+  TeSums<T> a = {static_cast<const T*>(g), g_table, reinterpret_cast<float*>(ws + p.pieces),
+                 sorted.place, sorted.token, sorted.count, sorted.held, p.parts, V, p.part, C,
+                 accumulate, 0, scale};
   return te_teams<64>(C, [&](auto team) {
     constexpr int L = decltype(team)::lanes;
     const int64_t rows = kTeThreads / L;
     const uint32_t slices = (uint32_t)((C / 8 + L - 1) / L);
-    k_te_sums<T, L><<<dim3((uint32_t)((p.parts + rows - 1) / rows), slices), kTeThreads, 0, s>>>(a);
+    a.blocks = (int)((p.parts + rows - 1) / rows);
+    const int64_t zeros = accumulate ? 0 : std::min<int64_t>((V + 3) / 4, kTeZeroBlocks);
+    k_te_sums<T, L><<<dim3((uint32_t)(a.blocks + zeros), slices), kTeThreads, 0, s>>>(a);
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess || p.parts < 2) return err;
     k_te_join<T, L><<<dim3((uint32_t)(p.parts - 1), slices), kTeThreads, 0, s>>>(a);
