@@ -886,9 +886,10 @@ nt_status nt_token_loss_workspace_bytes(int64_t T, int64_t V, int32_t C, nt_dtyp
 /*
  * Cross entropy of singles over a vocabulary, for each token:
  *   z[t, v] = scale x_t . W_v,  lse[t] = log sum_v exp z[t, v],  nll[t] = lse[t] - z[t, target_t].
- * x: [T, C], W: [V, C] of `dtype`, targets: [T]; nll, lse: fp32 [T]; scale is
- * finite and not zero. Logits are fp32 and are not kept. A token whose target is below zero takes no part: nll
- * = lse = 0, whatever its row holds. A target of V or more has nll NaN.
+ * x: [T, C], W: [V, C] of `dtype`, targets: [T]; nll, lse: fp32 [T]; scale is not
+ * zero, and at most 2^100 either way. Logits are fp32 and are not kept. A token whose
+ * target is below zero takes no part: nll = lse = 0, whatever its row holds. A target of
+ * V or more has nll NaN.
  * workspace: device, 16-byte aligned, of one call at a time.
  */
 nt_status nt_token_loss(const void* x, const void* W, const int32_t* targets, float* nll,
@@ -909,8 +910,8 @@ nt_status nt_token_loss_backward_workspace_bytes(int64_t T, int64_t V, int32_t C
  *   g_x = scale d W,   g_W (+)= scale d^T x.
  * g_x: [T, C] of `dtype`, zero for tokens without a target; g_W: fp32 [V, C].
  * Either may be NULL. With NT_BF16 g_x takes d rounded to bf16 (at the target
- * unrounded) and g_W takes it as a pair of bf16, hi + lo (to 2^-17). A target of V or more makes its
- * gradients NaN. workspace: device, 16-byte aligned, of one call at a time.
+ * unrounded) and g_W takes it as a pair of bf16, hi + lo (to 2^-17). A target of V or
+ * more makes its gradients NaN. workspace: device, 16-byte aligned, of one call at a time.
  */
 nt_status nt_token_loss_backward(const void* x, const void* W, const int32_t* targets,
                                  const float* lse, const float* g_nll, const float* g_lse,

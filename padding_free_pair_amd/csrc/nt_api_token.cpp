@@ -61,9 +61,10 @@ nt_status check_scale(float scale) {
   return NT_OK;
 }
 
+// The kernels take it times log2(e), which has to be finite as well.
 nt_status check_logit_scale(float scale) {
-  if (!std::isfinite(scale) || scale == 0.0f)
-    return fail(NT_ERR_INVALID, "scale must be finite and not zero");
+  if (!(std::fabs(scale) <= 0x1p100f) || scale == 0.0f)
+    return fail(NT_ERR_INVALID, "scale must not be zero, and at most 2^100 either way");
   return NT_OK;
 }
 

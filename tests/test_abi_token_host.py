@@ -94,6 +94,14 @@ def test_sizes(lib, call, changes):
     assert call(lib, dtype=7) == E.NT_ERR_DTYPE
 
 
+@pytest.mark.parametrize("call", [loss, loss_backward])
+def test_scales_without_a_product(lib, call):
+    """Finite scales whose product with log2(e) may not be, and their neighbours."""
+    for scale in (3.4e38, -3.4e38, 2.0 ** 101, math.nan, -math.inf):
+        assert call(lib, scale=scale) == E.NT_ERR_INVALID, scale
+    assert call(lib, scale=2.0 ** 100, bytes=0) == E.NT_ERR_WORKSPACE
+
+
 @pytest.mark.parametrize("call,needed,free", [
     (embedding, ["table", "tokens", "out"], []),
     (embedding_backward, ["tokens", "g", "table", "ws"], []),
