@@ -114,6 +114,25 @@ def test_embedding_backward_nothing(nt):
         assert bool((out == 0.0).all())
 
 
+def test_embedding_far_rows(nt):
+    """Rows of the table and of the singles past 4 GiB."""
+    announce("embedding of 4.6 GB")
+    V, C = 140000, 16384
+    table = torch.zeros((V, C), dtype=torch.bfloat16, device="cuda")
+    table[:, 0] = torch.arange(V, device="cuda") % 251
+    table[:, C - 1] = torch.arange(V, device="cuda") // 1000
+    ids = torch.arange(V - 1, -1, -1, dtype=torch.int32, device="cuda")
+    out = nt.nt_token_embedding(table, ids)
+    for row in (0, 1, 70000, V - 1):
+        np.testing.assert_array_equal(bits(out[row], torch), bits(table[V - 1 - row], torch))
+    assert bool((out[:, 0] == table[:, 0].flip(0)).all())
+    assert bool((out[:, C - 1] == table[:, C - 1].flip(0)).all())
+    g = nt.nt_token_embedding_backward(ids, out, V)
+    assert bool((g[:, 0] == table[:, 0].float()).all())
+    assert bool((g[:, C - 1] == table[:, C - 1].float()).all())
+    assert bool((g[V - 3:] == table[V - 3:].float()).all())
+
+
 def test_embedding_rows_behind_stay(nt):
     """Rows behind the last token, and behind the table, are left as they were."""
     big = torch.full((12, 40), 7.0, device="cuda")
@@ -284,6 +303,26 @@ def test_residual_norm_many_rows(nt):
     assert g.shape == (0, 40) and bool((g_w == 0).all())
 
 
+def test_residual_norm_far_rows(nt):
+    """Rows past 4 GiB: the last ones are as those alone."""
+    announce("norm of 4.6 GB")
+    T, C, some = 140000, 16384, 5
+    rng = np.random.default_rng(4)
+    last, _ = _dev(rng.normal(size=(some, C)), "bf16")
+    w, _ = _dev(1.0 + 0.2 * rng.normal(size=C))
+    x = torch.zeros((T, C), dtype=torch.bfloat16, device="cuda")
+    x[T - some:] = last
+    y, h = nt.nt_residual_norm(x, w, residual=x)
+    y1, h1 = nt.nt_residual_norm(last, w, residual=last)
+    codes, scales, _ = nt.nt_residual_norm_8bit(h, w)
+    c1, s1, _ = nt.nt_residual_norm_8bit(h1, w)
+    g, _ = nt.nt_residual_norm_backward(h, x, w)
+    g1, _ = nt.nt_residual_norm_backward(h1, last, w)
+    for a, b in ((y, y1), (h, h1), (codes.view(torch.uint8), c1.view(torch.uint8)), (scales, s1),
+                 (g, g1)):
+        assert bool((a[T - some:] == b).all()) and bool((a[:T - some] == 0).all())
+
+
 # ---------------------------------------------------------------------- loss
 def _loss_inputs(rng, T, V, C, dtype, absent=0.2, spread=2.0):
     x, x64 = _dev(rng.normal(size=(T, C)), dtype)
@@ -323,6 +362,88 @@ def test_token_loss_many_tiles(nt):
     rng = np.random.default_rng(1)
     x, x64, W, W64, ids = _loss_inputs(rng, 3900, 4300, 72, "bf16", absent=0.01)
     _check_loss(nt, x, x64, W, W64, ids, 1.0, "bf16")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,V,C", [(3, 130, 4104), (16, 1000, 2056), (31, 200, 2056), (20, 66000, 520)])
+def test_token_loss_few_tokens(nt, T, V, C, dtype):
+    """Rows of x that LDS holds in stretches only, and more rows of W than the launched
+    waves take at a time."""
+    announce(f"loss T={T} V={V} C={C} {dtype}")
+    rng = np.random.default_rng(T + V + C)
+    x, x64, W, W64, ids = _loss_inputs(rng, T, V, C, dtype)
+    _check_loss(nt, x, x64, W, W64, ids, 1.0, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_token_loss_passes(nt, dtype):
+    """More tokens than a pass takes, forward and back; the last pass has no target at
+    all in its first half."""
+    announce(f"loss T=140000 {dtype}")
+    rng = np.random.default_rng(8)
+    x, x64, W, W64, ids = _loss_inputs(rng, 140000, 24, 16, dtype, absent=0.5)
+    ids[131072:135000] = -1
+    lse = _check_loss(nt, x, x64, W, W64, ids, 1.0, dtype)
+    _check_backward(nt, x, x64, W, W64, ids, lse, dtype, 1.0, rng, True, True)
+
+
+@pytest.mark.parametrize("T,V,C,absent,what", [
+    (6140, 6130, 8, 0.01, "the logits"),
+    (36860, 16, 1024, 0.97, "g_x"),
+    (40, 36860, 1024, 0.0, "g_W")])
+def test_token_loss_wide_tiles_f32(nt, T, V, C, absent, what):
+    announce(f"loss T={T} V={V} C={C} f32: wide tiles of {what}")
+    rng = np.random.default_rng(12)
+    x, x64, W, W64, ids = _loss_inputs(rng, T, V, C, "f32", absent=absent)
+    lse = _check_loss(nt, x, x64, W, W64, ids, 1.0, "f32")
+    _check_backward(nt, x, x64, W, W64, ids, lse, "f32", 1.0, rng, False, False)
+
+
+@pytest.mark.parametrize("T", [5, 40])
+def test_token_loss_far_rows(nt, T):
+    """Rows of W past 4 GiB: all are zeros but the last ones, so that the logits of the
+    others are 0 and the gradient of the others is p0 x, p0 = exp(-lse)."""
+    V, C, some = 140000, 16384, 300
+    announce(f"loss T={T} V={V} C={C}")
+    rng = np.random.default_rng(T)
+    x, x64 = _dev(rng.normal(size=(T, C)), "bf16")
+    last, last64 = _dev(rng.normal(size=(some, C)) * 4 / math.sqrt(C), "bf16")
+    W = torch.zeros((V, C), dtype=torch.bfloat16, device="cuda")
+    W[V - some:] = last
+    ids = rng.integers(V - some, V, size=T)
+    ids[1] = -1
+    ids[2] = 7
+    nll, lse = nt.nt_token_loss(x, W, _ids(ids))
+    # the last rows and a zero one, which counts for all the others
+    few = np.concatenate([np.zeros((1, C)), last64])
+    z = x64 @ few.T
+    top = z.max(1, keepdims=True)
+    count = np.r_[V - some, np.ones(some)]
+    want = (top[:, 0] + np.log((np.exp(z - top) * count).sum(1))) * (ids >= 0)
+    at = np.where(ids >= V - some, ids - (V - some) + 1, 0)
+    err = tb._logit_error(x64, few, 1.0, want)
+    p = np.exp(z - want[:, None]) * count
+    # as in token_bounds.loss_bound, with a weight for each row
+    bl = ((p * err).sum(1) + (V + 8) * tb.U + 8 * tb.U * (1 + np.abs(want))) * (ids >= 0)
+    _within("lse", lse, want, bl)
+    _within("nll", nll, np.where(ids >= 0, want - z[np.arange(T), at], 0.0),
+            bl + err[np.arange(T), at] * (ids >= 0))
+    if T > 5:
+        return
+    g = torch.ones(T, device="cuda")
+    g_x, g_W = nt.nt_token_loss_backward(x, W, _ids(ids), lse, g)
+    l64 = f64(lse, torch)
+    local = np.where(ids < 0, -1, at)
+    # one zero row as the vocabulary has it: its gradient is that of every zero row but
+    # the seventh, which is a target
+    rx, rW = oracle.token_loss_backward(x64, few, local, l64, np.ones(T))
+    bx, bW = tb.loss_backward_bound(x64, few, local, l64, np.ones(T), None, 1.0, None, rx, "bf16")
+    # the zero rows add nothing to g_x, the longer sum of the product nothing but zeros
+    _within("g_x", g_x, rx, bx)
+    _within("g_W", g_W[V - some:], rW[1:], bW[1:])
+    _within("g_W[7]", g_W[7:8], rW[:1], bW[:1])
+    rest = np.exp(-l64) * (ids >= 0) @ x64
+    _within("g_W[V - some - 1]", g_W[V - some - 1:V - some], rest[None], bW[:1])
 
 
 @pytest.mark.parametrize("T", [20, 200])
@@ -435,7 +556,7 @@ def test_token_loss_backward(nt, T, V, C, dtype):
 
 @pytest.mark.parametrize("T,V,C,absent,what", [
     (3900, 4300, 64, 0.01, "wide tiles of the logits"),
-    (8100, 40, 2056, 0.9, "wide tiles of g_x"),
+    (7100, 40, 2056, 0.9, "wide tiles of g_x"),
     (60, 8100, 2056, 0.0, "wide tiles of g_W"),
     (131000, 1100, 64, 0.998, "pieces of the vocabulary")])
 def test_token_loss_backward_large(nt, T, V, C, absent, what):
