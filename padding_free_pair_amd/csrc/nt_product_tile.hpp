@@ -3,8 +3,8 @@
 //
 // An operand lies along k (a row of k's for each m or n) or across it (a row of m's
 // or n's for each k). A tile of BK values of k, 128 bytes of every row along k, is
-// loaded straight to LDS as it lies; the chunks of a row are turned as those of the
-// attention's tiles (AtTileMap), so that fragments of either kind are read without
+// loaded straight to LDS as it lies; the chunks of a row are turned (across k as those
+// of the attention's tiles, AtTileMap), so that fragments along k are read without
 // conflicts. Fragments across k take the transposing LDS read, which moves 8 bytes a
 // lane where the plain one moves 16: a product with both operands across k reached 1,120
 // TFLOP/s, so at least one of them is better transposed in memory once.
@@ -80,18 +80,28 @@ template <typename V> __device__ __forceinline__ V pt_lds(uint32_t at) {
 // Tiles of an operand that lies along k: ROWS rows of 128 bytes, the loads of a
 // thread, and the fragments.
 template <typename T, int ROWS, int THREADS> struct PtRows {
-  typedef AtTile<T, 128 / (int)sizeof(T)> L;
+  static constexpr int vec = 16 / (int)sizeof(T);  // elements of a chunk, 8 chunks a row
   static constexpr int pieces = ROWS * 8 / THREADS;
   static_assert(ROWS * 8 % THREADS == 0, "whole pieces");
   static constexpr bool S32 = sizeof(T) == 4;
+  // A row's chunks are turned (XOR) by its place in 16 rows. Two rows are a line of the 64
+  // banks, so rows 2 r and 2 r + 1 share a turn and the 8 of them differ. The 16 lanes that
+  // are served together hold rows 0 .. 3 and 12 .. 15 of one quarter and 4 .. 11 of the next
+  // one, whose chunk differs in bit 0 (fp32: 1): that bit is the row's bit 1, which takes
+  // either value in both groups. (With its bit 2 there half of the reads' cycles were
+  // conflicts, and a loss of 8,007 tokens over 65,537 words took 8.6e8 cycles of the compute
+  // units where it takes 8.2e8, LDS busy for 48 % of them where it is for 25.)
+  static __device__ __forceinline__ int turn(int r) {
+    return S32 ? (r >> 3 & 1) << 2 | (r >> 1 & 1) << 1 | (r >> 2 & 1) : r >> 1 & 7;
+  }
   static __device__ __forceinline__ int row(int thread, int u) { return (thread + u * THREADS) / 8; }
   static __device__ __forceinline__ int col(int thread, int u) {
-    return ((thread + u * THREADS) % 8 ^ L::turn(row(thread, u))) * L::vec;
+    return ((thread + u * THREADS) % 8 ^ turn(row(thread, u))) * vec;
   }
   // The lane's bytes in a tile: row r + l % 16, values 8 g ..; r is a multiple of 16.
   static __device__ __forceinline__ uint32_t lane(int r) {
     const int l = threadIdx.x & 63;
-    return (uint32_t)(L::at(r + (l & 15), 8 * (l >> 4)) * (int)sizeof(T));
+    return (uint32_t)((r + (l & 15)) * 128 + (8 * (l >> 4) / vec ^ turn(l & 15)) * 16);
   }
   // Block i (16 rows on), values 32 s + 8 g .., at the LDS address of lane(r). The turn
   // of a row's chunks goes by its place in 16 rows; steps and halves are bits of the chunk.
@@ -128,7 +138,7 @@ template <typename T, int ROWS, int THREADS> struct PtAlong : PtRows<T, ROWS, TH
                                         int64_t plane = 0) const {
     const uint32_t to = tile + (threadIdx.x & ~63) * 16;
     const char* from = reinterpret_cast<const char*>(base + plane + k0);
-    if (k0 + Base::L::pitch <= K) {
+    if (k0 + 8 * Base::vec <= K) {
 #pragma unroll
       for (int u = 0; u < pieces; ++u) at_load_lds16(from, off[u], to + u * THREADS * 16);
     } else {
