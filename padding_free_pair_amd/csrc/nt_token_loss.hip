@@ -595,7 +595,7 @@ template <typename S> struct TlTurn {
 // W, lo. (The order that both products would read along k, [t][v] of hi for the
 // gradient of x, costs more to store than its product gains from it: workgroups come to
 // their stores at the same time, so every byte is paid.) 8,007 tokens x 16,128 rows of
-// 2,048, bf16: 560 us, cores busy for 48 % of the cycles, 1.1 TB/s of d to memory in bursts.
+// 2,048, bf16: 560 us, cores busy for 48 % of the cycles, 0.9 TB/s of d to memory in bursts.
 template <typename S>
 __global__ __launch_bounds__(S::threads) void k_tl_logit_grad(TlGrad<typename S::type> p) {
   typedef typename S::type T;
@@ -910,8 +910,8 @@ struct Cut {
 // whole rounds of all units (in fp32 and half a one: tokens without a target leave the last
 // one fuller or emptier, and the small tile costs little more), 4 for a large tile and 1.3
 // for a small one (measured in bf16: 1,430 and 1,115 TFLOP/s where the rounds are full;
-// fp32: 129 and 122, 1.07), a tile's beginning and end as 300 steps more (fp32: 40), and the results' way through memory, `bytes` each
-// and 8 more for each part where there are several, at 4 TB/s. fp32, 1,866 tokens, half of
+// fp32: 129 and 122, 1.07), a tile's beginning and end as 300 steps more (fp32: 40), and the
+// results' way through memory, `bytes` each and 8 more for each part where there are several, at 4 TB/s. fp32, 1,866 tokens, half of
 // them without a target, over 4,099 words of 384, gradient: 140 us by this rule, 196 in
 // large tiles.
 Cut cut_of(int64_t m, int64_t n, int64_t k, double bytes, bool narrow, bool split) {
