@@ -909,9 +909,9 @@ nt_status nt_token_loss_backward_workspace_bytes(int64_t T, int64_t V, int32_t C
  *   d[t, v] = (g_nll[t] + g_lse[t]) exp(z[t, v] - lse[t]) - g_nll[t] [v = target_t],
  *   g_x = scale d W,   g_W (+)= scale d^T x.
  * g_x: [T, C] of `dtype`, zero for tokens without a target; g_W: fp32 [V, C].
- * Either may be NULL. With NT_BF16 g_x takes d rounded to bf16 (at the target
- * unrounded) and g_W takes it as a pair of bf16, hi + lo (to 2^-17). A target of V or
- * more makes its gradients NaN. workspace: device, 16-byte aligned, of one call at a time.
+ * Either may be NULL. With NT_BF16 both take d as a pair of bf16, hi + lo (to 2^-17);
+ * the exponents take lse as it is given, in fp32, which leaves 2^-24 |lse| of each power.
+ * A target of V or more makes its gradients NaN. workspace: device, 16-byte aligned, of one call at a time.
  */
 nt_status nt_token_loss_backward(const void* x, const void* W, const int32_t* targets,
                                  const float* lse, const float* g_nll, const float* g_lse,

@@ -176,10 +176,10 @@ template <typename T, int COLS, int THREADS> struct PtAcross {
       asm volatile("" : "+v"(off[u]));
     }
   }
-  // Rows k0 .. to LDS address `tile`.
-  __device__ __forceinline__ void start(int64_t k0, uint32_t tile) const {
+  // Rows k0 .. to LDS address `tile`, of the array that lies `plane` elements on.
+  __device__ __forceinline__ void start(int64_t k0, uint32_t tile, int64_t plane = 0) const {
     const uint32_t to = tile + (threadIdx.x & ~63) * 16;
-    const char* from = reinterpret_cast<const char*>(base + k0 * ld);
+    const char* from = reinterpret_cast<const char*>(base + plane + k0 * ld);
 #pragma unroll
     for (int u = 0; u < pieces; ++u) at_load_lds16(from, off[u], to + u * THREADS * 16);
   }

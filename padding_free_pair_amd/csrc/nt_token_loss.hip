@@ -7,9 +7,9 @@
 // a second kernel joins them. Backward: pieces of the vocabulary; for each,
 // d = (g_nll + g_lse) exp(z - lse) - g_nll [v = target] goes to the workspace in
 // the operands' type, then g_x += scale d W and g_W = scale d^T x are products
-// over it. The weights' gradient is fp32, which one bf16 of d (2^-9 of each
-// value) would not fill: it takes d as a pair of bf16, hi + lo (2^-17), in two
-// products; g_x is rounded to bf16 itself and takes hi alone.
+// over it. In bf16 one rounding of d (2^-9 of each value) would be seen in both: g_W is
+// fp32, and g_x, which is rounded once itself, would be off by up to its own half step
+// again where terms cancel. Both take d as a pair of bf16, hi + lo (2^-17), in two products.
 //
 // Tokens without a target take no part: the others' rows are listed first, the
 // forward reads x through the list, the backward copies the listed rows (with
@@ -535,7 +535,6 @@ template <typename T> struct TlGrad {
   float* out;     // g_W
   int64_t tokens; // of the copies, a multiple of 256
   int64_t x_budget;  // numbers in the sums of g_x
-  float* rest;       // [tokens] what rounding took from d at the target (bf16)
   int C, w_most, accumulate;
   float scale, scale2;
   uint32_t tiles_m, tiles_n;
@@ -591,10 +590,10 @@ template <typename S> struct TlTurn {
   }
 };
 
-// d of a tile, rows of W (m) x tokens (n), to d[v][t], in bf16 hi and, for the gradient of
-// W, lo. (The order that both products would read along k, [t][v] of hi for the
-// gradient of x, costs more to store than its product gains from it: workgroups come to
-// their stores at the same time, so every byte is paid.) 8,007 tokens x 16,128 rows of
+// d of a tile, rows of W (m) x tokens (n), to d[v][t], in bf16 hi and lo. (The order that
+// both products would read along k, [t][v] for the gradient of x, costs more to store
+// than its product gains from it: workgroups come to their stores at the same time, so
+// every byte is paid.) 8,007 tokens x 16,128 rows of
 // 2,048, bf16: 560 us, cores busy for 48 % of the cycles, 0.9 TB/s of d to memory in bursts.
 template <typename S>
 __global__ __launch_bounds__(S::threads) void k_tl_logit_grad(TlGrad<typename S::type> p) {
@@ -639,15 +638,10 @@ __global__ __launch_bounds__(S::threads) void k_tl_logit_grad(TlGrad<typename S:
             both * __builtin_amdgcn_exp2f(__builtin_fmaf(z.d[i][j][e], p.scale2, -base));
     if (__ballot(target >= 0)) {
       at_rare();
-      float found = 0.0f;
 #pragma unroll
       for (int i = 0; i < S::mt; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          z.d[i][j][e] -= 16 * i + e == target ? one : 0.0f;
-          found = 16 * i + e == target ? z.d[i][j][e] : found;
-        }
-      if (sizeof(T) == 2 && target >= 0) p.rest[t] = found - (float)(T)found;
+        for (int e = 0; e < 4; ++e) z.d[i][j][e] -= 16 * i + e == target ? one : 0.0f;
     }
     if (v0 + S::m > p.V || t0 + S::n > live) {
       // zeros for rows of W that are not there and for tokens behind the last one
@@ -667,7 +661,6 @@ __global__ __launch_bounds__(S::threads) void k_tl_logit_grad(TlGrad<typename S:
   T* to = p.d + (c0 + m0) * p.ldt + t0 + n0;
   TlTurn<S>::store(tile, to, p.ldt);
   if constexpr (sizeof(T) == 2) {
-    if (!p.out) return;
 #pragma unroll
     for (int j = 0; j < S::nt; ++j)
 #pragma unroll
@@ -740,7 +733,8 @@ __device__ __forceinline__ void tl_store(const PtSums<S>& acc, float* to, int64_
 // for hi and lo) at 8,007 tokens of 2,048 in bf16, the matrix cores busy for 59 and 61 %.
 //
 // The product of g_x, sums[split][t][c] (+)= sum over the split's rows v of the piece of
-// d[t, v] W[v, c], and that of g_W: both sides of a launch and of its join count alike.
+// d[t, v] W[v, c], d as hi and lo in turn, and that of g_W: both sides of a launch and of its
+// join count alike.
 template <int TILE> __device__ __forceinline__ int64_t tl_tokens(int64_t live) {
   return (live + TILE - 1) / TILE;
 }
@@ -754,11 +748,12 @@ __global__ __launch_bounds__(S::threads) void k_tl_x_grad(TlGrad<typename S::typ
   const int64_t live = *p.live;
   const int64_t K = p.V - p.v_first < p.piece ? p.V - p.v_first : p.piece;
   TlPart part;
+  constexpr int kPlanes = sizeof(T) == 2 ? 2 : 1;
   // parts of the first piece, which may be cut finer than a shorter last one could
-  if (!part.take(p.tiles_m, (uint32_t)tl_tokens<S::n>(live), p.piece / S::bk,
+  if (!part.take(p.tiles_m, (uint32_t)tl_tokens<S::n>(live), kPlanes * (p.piece / S::bk),
                  tl_most(p.x_budget, live, p.C)))
     return;
-  const int64_t steps = (K + S::bk - 1) / S::bk;
+  const int64_t one = (K + S::bk - 1) / S::bk, steps = kPlanes * one;
   const int64_t count = part.begin + part.count < steps ? part.count : steps - part.begin;
   const int64_t c0 = (int64_t)part.m * S::m, t0 = (int64_t)part.n * S::n;
   const A la(p.WT + c0 * p.ldv, p.ldv, [&](int r) { return c0 + r < p.C ? r : p.C - 1 - c0; });
@@ -766,8 +761,14 @@ __global__ __launch_bounds__(S::threads) void k_tl_x_grad(TlGrad<typename S::typ
   PtSums<S> acc;
   pt_product<false, S, A, B>(
       acc, smem, count,
-      [&](int64_t j, uint32_t to) { la.start((part.begin + j) * S::bk, p.piece, to); },
-      [&](int64_t j, uint32_t to) { lb.start((part.begin + j) * S::bk, to); });
+      [&](int64_t j, uint32_t to) {
+        const int64_t k = part.begin + j;
+        la.start((k < one ? k : k - one) * S::bk, p.piece, to);
+      },
+      [&](int64_t j, uint32_t to) {
+        const int64_t k = part.begin + j;
+        lb.start((k < one ? k : k - one) * S::bk, to, k < one ? 0 : p.plane);
+      });
   tl_store(acc, p.sums + part.split * live * p.C, p.C, t0, live, c0, p.C, p.accumulate);
 }
 
@@ -811,39 +812,25 @@ struct TlCut {
 };
 
 // The splits of g_x joined and rounded, each listed row at its token's place, zeros at the
-// others. In bf16 d's largest value in most rows, p - 1 at the target, is made good for its
-// rounding with the target's row of W, which leaves g_x as exact as its own rounding does
-// (without it 1.7 times as far off).
+// others.
 template <typename T>
 __global__ __launch_bounds__(256) void k_tl_x_join(const float* sums, const int32_t* targets,
                                                    const int32_t* rows, const int64_t* live,
-                                                   const float* rest, const T* W, T* g_x,
-                                                   int64_t tokens, int64_t piece, int64_t V,
+                                                   T* g_x, int64_t tokens, int64_t piece,
                                                    int64_t budget, int C, TlCut cut) {
   const int64_t n = *live;
   const int64_t tiles = (int64_t)((C + cut.tile_m - 1) / cut.tile_m) *
                         ((n + cut.tile_n - 1) / cut.tile_n);
-  const int splits = n ? tl_splits(tiles, piece / cut.bk, cut.launched, tl_most(budget, n, C)) : 1;
+  const int64_t steps = cut.planes * (piece / cut.bk);
+  const int splits = n ? tl_splits(tiles, steps, cut.launched, tl_most(budget, n, C)) : 1;
   for (int64_t r = blockIdx.x; r < tokens; r += gridDim.x) {
-    const int64_t row = r < n ? rows[r] : 0;
-    T* to = g_x + row * C;
+    T* to = g_x + (int64_t)(r < n ? rows[r] : 0) * C;
     const bool absent = targets[r] < 0;
-    const int64_t target = targets[row];
-    const bool good = sizeof(T) == 2 && r < n && target < V;
-    const T* w = W + (good ? target : 0) * C;
-    const float left = good ? rest[r] : 0.0f;
     for (int c = 4 * threadIdx.x; c < C; c += 4 * 256) {
       if (r < n) {
         f32x4 f = *reinterpret_cast<const f32x4*>(sums + r * C + c);
         for (int s = 1; s < splits; ++s)
           f += *reinterpret_cast<const f32x4*>(sums + (s * n + r) * C + c);
-        if constexpr (sizeof(T) == 2) {
-          if (good) {
-            const at_bf16x4 x = *reinterpret_cast<const at_bf16x4*>(w + c);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) f[e] += left * (float)x[e];
-          }
-        }
         at_store4(to + c, f[0], f[1], f[2], f[3]);
       }
       if (absent) at_store4(g_x + r * C + c, 0.0f, 0.0f, 0.0f, 0.0f);
@@ -940,7 +927,7 @@ struct Plan {
   int w_most;
   Cut logits, singles, weights;
   // the workspace
-  size_t rows, live, part, at, rest, x, xT, WT, d, x_sums, w_sums, total;
+  size_t rows, live, part, at, x, xT, WT, d, x_sums, w_sums, total;
 };
 
 // Tokens of a pass: an array of them spans 4 GiB at most, and the statistics of 128
@@ -986,7 +973,7 @@ Plan backward_plan(int64_t T, int64_t V, int64_t C, nt_dtype dtype) {
   for (int64_t pieces = tiles_of(V, most), last = pieces + 8; pieces < last; ++pieces) {
     const int64_t piece = up(tiles_of(V, pieces), 256), n = std::min(piece, V);
     const Cut l = cut_of(n, p.tokens, C, (double)(es * p.planes), narrow, false);
-    const Cut x = cut_of(C, p.tokens, n, 8.0, narrow, true);
+    const Cut x = cut_of(C, p.tokens, p.planes * n, 8.0, narrow, true);
     const Cut w = cut_of(C, n, p.planes * p.tokens, 4.0, narrow, true);
     const double cost = (double)tiles_of(V, piece) * (l.cost + x.cost + w.cost);
     if (!p.piece || cost < best) {
@@ -1014,7 +1001,6 @@ Plan backward_plan(int64_t T, int64_t V, int64_t C, nt_dtype dtype) {
   size_t at = 0;
   p.rows = at; at = align256(at + sizeof(int32_t) * p.tokens);
   p.live = at; at = align256(at + sizeof(int64_t));
-  p.rest = at; at = align256(at + sizeof(float) * p.tokens);
   p.x = at; at = align256(at + es * p.padded * C);
   p.xT = at; at = align256(at + es * p.ldt * C);
   p.WT = at; at = align256(at + es * p.ldv * C);
@@ -1136,8 +1122,7 @@ hipError_t backward(const Plan& p, const T* x, const T* W, const int32_t* target
   if (e != hipSuccess) return e;
   TlGrad<T> a = {xs, xT, W, WT, targets, rows, live, lse, g_nll, g_lse,
                  reinterpret_cast<T*>(ws + p.d), p.ldt * p.piece, p.piece, p.ldv, p.ldt, 0, V,
-                 nullptr, g_W, p.padded, p.x_budget, reinterpret_cast<float*>(ws + p.rest), C,
-                 p.w_most, 0, scale, scale * kLog2e, 0, 0};
+                 nullptr, g_W, p.padded, p.x_budget, C, p.w_most, 0, scale, scale * kLog2e, 0, 0};
   float* x_sums = reinterpret_cast<float*>(ws + p.x_sums);
   float* w_sums = reinterpret_cast<float*>(ws + p.w_sums);
   const int bk = 128 / (int)sizeof(T);
@@ -1176,7 +1161,7 @@ hipError_t backward(const Plan& p, const T* x, const T* W, const int32_t* target
   const int t = p.singles.tile;
   const int64_t launched = std::max(p.singles.launched, up(tiles_of(C, t) * tiles_of(tokens, t), 8));
   k_tl_x_join<T><<<blocks_of(tokens, 1), 256, 0, s>>>(
-      x_sums, targets, rows, live, a.rest, W, g_x, tokens, p.piece, V, p.x_budget, C,
+      x_sums, targets, rows, live, g_x, tokens, p.piece, p.x_budget, C,
       TlCut{t, t, bk, (int)p.planes, launched});
   return hipGetLastError();
 }

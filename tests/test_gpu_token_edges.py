@@ -1,0 +1,78 @@
+"""GPU tests of the operators between tokens and singles where they can go wrong:
+precision next to a rounding, the smallest numbers, the pieces and tiles that a
+batch's sizes lead to, paths that keep state in a workspace."""
+import math
+
+import numpy as np
+import pytest
+
+import oracle
+import token_bounds as tb
+from gpu_util import announce, bits, f64
+from test_gpu_token import _check_loss, _dev, _ids, _loss_inputs, _within, nt  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+
+# ----------------------------------------------------------- loss's gradient
+def _pair_bound(x, W, ids, lse, g_nll, g_lse, scale, old, g_x, dtype):
+    """(bound of g_x, bound of g_W) where both products take d as a pair of bf16: hi
+    leaves at most 2^-8 of d and lo 2^-8 of that. As token_bounds.loss_backward_bound
+    for the logits and sums (each product twice as many terms); beside them g_x has the
+    one rounding of its storage."""
+    live, d, p = oracle.logit_grad(x, W, ids, lse, g_nll, g_lse, scale)
+    both = np.abs(g_nll[live]) + (0.0 if g_lse is None else np.abs(g_lse[live]))
+    de = both[:, None] * p * (tb._logit_error(x[live], W, scale, lse[live]) + 8 * tb.U)
+    de = de + 4 * tb.U * np.abs(d)
+    for i, t in enumerate(live):
+        de[i, ids[t]] += 4 * tb.U * (both[i] * p[i, ids[t]] + np.abs(g_nll[t]))
+    pair = 2.0 ** -16 if dtype == "bf16" else 0.0
+    bx = np.zeros(x.shape)
+    bx[live] = abs(scale) * ((de + (pair + (2 * len(W) + 40) * tb.U) * np.abs(d)) @ np.abs(W))
+    bx = (1 + 2.0 ** -8) * bx + tb.HALF[dtype] * np.abs(g_x) + 1e-30
+    bW = abs(scale) * ((de + (pair + (2 * len(live) + 40) * tb.U) * np.abs(d)).T
+                       @ np.abs(x[live])) + 1e-30
+    return bx, bW if old is None else bW + 2 * tb.U * np.abs(old)
+
+
+def _check_gradients(nt, x, x64, W, W64, ids, lse, dtype, rng, scale=1.0, both=False,
+                     accumulate=False):
+    T = len(ids)
+    g_nll, gn64 = _dev(rng.normal(size=T) / T)
+    g_lse, gl64 = _dev(rng.normal(size=T) / T) if both else (None, None)
+    old, old64 = _dev(rng.normal(size=W64.shape) * 1e-2) if accumulate else (None, None)
+    g_x, g_W = nt.nt_token_loss_backward(x, W, _ids(ids), lse, g_nll, g_lse=g_lse, scale=scale,
+                                         g_W=old, accumulate=accumulate)
+    s, l64 = np.float64(np.float32(scale)), f64(lse, torch)
+    rx, rW = oracle.token_loss_backward(x64, W64, ids, l64, gn64, gl64, s, old64)
+    bx, bW = _pair_bound(x64, W64, ids, l64, gn64, gl64, s, old64, rx, dtype)
+    _within("g_x", g_x, rx, bx)
+    _within("g_W", g_W, rW, bW)
+    return g_nll, g_lse, g_x, g_W
+
+
+@pytest.mark.parametrize("T,V,C", [(1, 300, 64), (33, 33, 8), (40, 2000, 64), (130, 300, 200),
+                                   (257, 128, 1032), (300, 1301, 128)])
+def test_loss_gradient_beside_one_rounding(nt, T, V, C):
+    """In bf16 g_x is off by its own rounding and next to nothing else: where the terms of
+    its sum cancel, one rounding of them would be seen."""
+    announce(f"loss backward, pair, T={T} V={V} C={C}")
+    rng = np.random.default_rng(T + V)
+    x, x64, W, W64, ids = _loss_inputs(rng, T, V, C, "bf16")
+    for scale, both in ((1.0, False), (-0.3, True)):
+        lse = nt.nt_token_loss(x, W, _ids(ids), scale=scale)[1]
+        _check_gradients(nt, x, x64, W, W64, ids, lse, "bf16", rng, scale, both, both)
+
+
+def test_loss_gradient_at_the_target(nt):
+    """d at the target dominates: hardly any probability elsewhere, the target's row of W
+    large, and d there (p - 1) g with a g that bf16 does not hold."""
+    T, V, C = 60, 200, 64
+    announce("loss backward, d at the target")
+    rng = np.random.default_rng(1)
+    x, x64 = _dev(rng.normal(size=(T, C)) * 1e-3, "bf16")
+    W, W64 = _dev(rng.normal(size=(V, C)) * 100, "bf16")
+    ids = rng.integers(0, V, size=T)
+    lse = nt.nt_token_loss(x, W, _ids(ids))[1]
+    _check_gradients(nt, x, x64, W, W64, ids, lse, "bf16", rng)
