@@ -855,7 +855,8 @@ nt_status nt_residual_norm(const void* x, const void* residual, const float* w, 
  * largest) in units of scales, fp32 [rows] for group 0 (a row shares one) or
  * [rows, C / group] (group: a power of two from 8 to 512 that divides C). A
  * scale is the largest finite magnitude of its values times the fp32 number next
- * to 1/448; values that are not finite are NaN codes.
+ * to 1/448, and a quotient past 448, which the rounding of a subnormal scale can leave,
+ * is 448; values that are not finite are NaN codes.
  */
 nt_status nt_residual_norm_8bit(const void* x, const void* residual, const float* w, void* h,
                                 uint8_t* codes, float* scales, int64_t rows, int32_t C,

@@ -199,8 +199,14 @@ __device__ __forceinline__ void rn_forward(const RnForward<T>& p, int64_t row, f
       float q[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) q[e] = f[u][e] * lift * inverse;
-      // nothing passes 448 by more than the inverse's rounding; NaN and infinities become
-      // the NaN code
+      // A normal scale leaves nothing past 448 but roundings. A subnormal one may be rounded to
+      // far less than the largest value's 448th, and the conversion makes NaN of what is past
+      // its range. NaN and infinities do become the NaN code.
+      if (scale < 0x1p-126f) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (isfinite(q[e])) q[e] = fminf(fmaxf(q[e], -448.0f), 448.0f);
+      }
       uint32_t a = 0, b = 0;
       a = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], a, false);
       a = __builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], a, true);

@@ -76,3 +76,35 @@ def test_loss_gradient_at_the_target(nt):
     ids = rng.integers(0, V, size=T)
     lse = nt.nt_token_loss(x, W, _ids(ids))[1]
     _check_gradients(nt, x, x64, W, W64, ids, lse, "bf16", rng)
+
+
+# ---------------------------------------------------------------------- norm
+@pytest.mark.parametrize("group", [0, 64])
+def test_residual_norm_8bit_smallest_scales(nt, group):
+    """Finite values have finite codes where the scale is a few of fp32's smallest steps and
+    its rounding leaves quotients past 448: those are 448."""
+    step, C = 2.0 ** -149, 128
+    tops = [1, 100, 224, 225, 464, 465, 500, 650, 671, 672, 1100, 2000, 5900, 6100, 7000, 10 ** 5]
+    rng = np.random.default_rng(6)
+    units = np.stack([np.r_[t, -t, 0, rng.integers(-t, t + 1, size=C - 3)] for t in tops])
+    units[:, 64:66] = units[:, :2]  # the largest one in every group
+    y = (units * step).astype(np.float32)
+    assert (y.astype(np.float64) == units * step).all()
+    x = torch.from_numpy(y).cuda()
+    # the squares are zeros in fp32, so eps = 1 leaves x as it is
+    codes, scales, _ = nt.nt_residual_norm_8bit(x, eps=1.0, group=group)
+    want = (np.abs(y).max(1) * np.float32(1.0 / 448.0))[:, None]
+    s = scales.cpu().numpy()
+    np.testing.assert_array_equal(s, np.broadcast_to(want, s.shape))
+    got = codes.float().cpu().numpy().astype(np.float64)
+    assert np.isfinite(got).all()
+    s = s[:, :1].astype(np.float64)
+    off = np.abs(got * s - y)
+    bound = np.maximum(tb.E4M3_HALF * np.abs(y), tb.E4M3_LEAST_HALF * s)
+    # the quotient is off by 2^-22 of it at most, and what is past 448 is lost
+    bound = bound + 2.0 ** -22 * np.abs(y) + np.maximum(np.abs(y) - 448 * s, 0.0)
+    assert (off <= bound).all()
+    x[3, 5], x[8, 70] = math.nan, math.inf
+    codes = nt.nt_residual_norm_8bit(x, eps=1.0, group=group)[0].float()
+    assert bool(torch.isnan(codes[3]).all())  # the row's mean of squares
+    assert bool(torch.isnan(codes[8, 70])) and bool((codes[8, :70] == 0).all())
