@@ -898,8 +898,9 @@ nt_status nt_token_loss(const void* x, const void* W, const int32_t* targets, fl
                         void* workspace, size_t workspace_bytes, void* stream);
 
 /* Workspace bytes nt_token_loss_backward needs: the gradients of the logits of
- * a piece of the vocabulary (at most 512 MiB, or of 256 rows), sums of g_x, two copies of
- * x and one of the piece's rows of W, for at most 65,536 tokens. */
+ * a piece of the vocabulary and a copy of the piece's rows of W (each at most 512 MiB, or of
+ * 256 rows), the parts of g_x and of the piece's g_W (each at most 256 MiB, or one part of
+ * g_x), and two copies of x, for at most 65,536 tokens. */
 nt_status nt_token_loss_backward_workspace_bytes(int64_t T, int64_t V, int32_t C, nt_dtype dtype,
                                                  size_t* bytes);
 

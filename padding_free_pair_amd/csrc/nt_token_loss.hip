@@ -881,7 +881,7 @@ template <> struct Tiles<float> {
 };
 
 constexpr int64_t kCus = 256;
-constexpr int64_t kPieceBytes = int64_t(512) << 20;  // of d
+constexpr int64_t kPieceBytes = int64_t(512) << 20;  // of d, and of the copy of the piece's rows of W
 constexpr int64_t kSumsBytes = int64_t(256) << 20;   // of the parts of g_x or g_W, where there are
 
 // How a product of m x n results over k is cut: its tile, and the workgroups launched,
@@ -966,8 +966,13 @@ Plan backward_plan(int64_t T, int64_t V, int64_t C, nt_dtype dtype) {
   p.tokens = pass_of(T, V);
   p.padded = up(p.tokens, 256);
   p.planes = narrow ? 2 : 1;  // of d
-  const int64_t most =
-      std::max<int64_t>(256, kPieceBytes / (p.padded * es * p.planes) / 256 * 256);
+  // Rows of a power of two of bytes would put the same values of k of all rows in one
+  // channel of the cache: a line more
+  const int64_t line = 128 / es;
+  p.ldt = p.padded + line;
+  // rows that both the piece's arrays hold: many tokens make d the larger one, few the copy of W
+  const int64_t rows = std::min(kPieceBytes / (p.ldt * es * p.planes), kPieceBytes / (C * es) - line);
+  const int64_t most = std::max<int64_t>(256, rows / 256 * 256);
   // the number of pieces, from the least one on, that fills whole rounds best
   double best = 0.0;
   for (int64_t pieces = tiles_of(V, most), last = pieces + 8; pieces < last; ++pieces) {
@@ -984,10 +989,7 @@ Plan backward_plan(int64_t T, int64_t V, int64_t C, nt_dtype dtype) {
       p.weights = w;
     }
   }
-  // Rows of a power of two of bytes would put the same values of k of all rows in one
-  // channel of the cache: a line more
-  p.ldv = p.piece + 128 / es;
-  p.ldt = p.padded + 128 / es;
+  p.ldv = p.piece + line;
   const int64_t numbers = kSumsBytes / (int64_t)sizeof(float);
   // room for all parts that the workgroups allow, or for 256 MiB of them (fewer tokens with
   // a target allow more parts of fewer rows, which take no more room)

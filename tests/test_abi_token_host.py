@@ -176,6 +176,25 @@ def test_workspace_sizes(lib):
     assert lib.nt_token_loss_workspace_bytes(5, 9, 16, 9, ctypes.byref(b)) == E.NT_ERR_DTYPE
 
 
+@pytest.mark.parametrize("dtype", [0, 1])
+@pytest.mark.parametrize("T", [1, 16, 256, 257, 3000, 65536])
+def test_workspace_of_few_tokens(lib, T, dtype):
+    """No array of the loss's gradient grows with the vocabulary: neither the logits'
+    gradients, of which few tokens have many rows, nor the copy of W's rows beside them."""
+    b = ctypes.c_size_t()
+    es, planes = (2, 2) if dtype else (4, 1)
+    line, rows, mib = 128 // es, (T + 255) // 256 * 256, 1 << 20
+    for C in (8, 384, 4096, 8192, 16384):
+        d = max(512 * mib, 256 * (rows + line) * es * planes)
+        w = max(512 * mib, (256 + line) * C * es)
+        x = (2 * rows + line) * C * es
+        sums = max(4 * rows * C, 256 * mib) + 256 * mib
+        for V in (33, 32003, 131072, 524288, 2 ** 26):
+            assert lib.nt_token_loss_backward_workspace_bytes(T, V, C, dtype,
+                                                              ctypes.byref(b)) == E.NT_OK
+            assert b.value <= d + w + x + sums + mib, (V, C, b.value)
+
+
 def test_nothing_to_do(lib):
     """Calls without rows that write nothing return at once."""
     assert embedding(lib, T=0, tokens=None, out=None) == E.NT_OK
