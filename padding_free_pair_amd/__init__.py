@@ -358,7 +358,7 @@ def nt_pair_reduce(p: Partition, z, m=None, stream=None):
 
 def nt_block_workspace_bytes(p: Partition, c_s: int, c_z: int, hidden: int, dtype) -> int:
     n = ctypes.c_size_t()
-    code = dtype if isinstance(dtype, int) else (NT_BF16 if "bfloat16" in str(dtype) else NT_F32)
+    code = _code(dtype)
     _check(_native.lib().nt_block_workspace_bytes(ctypes.byref(p.struct), c_s, c_z, hidden, code,
                                                   ctypes.byref(n)))
     return n.value
@@ -426,7 +426,7 @@ def nt_pair_block_noalloc(p: Partition, s_in, weights, s_out=None, z_out=None, s
 def nt_chain_workspace_bytes(p: Partition, nblocks: int, c_s: int, c_z: int, hidden: int,
                              dtype) -> int:
     n = ctypes.c_size_t()
-    code = dtype if isinstance(dtype, int) else (NT_BF16 if "bfloat16" in str(dtype) else NT_F32)
+    code = _code(dtype)
     _check(_native.lib().nt_chain_workspace_bytes(ctypes.byref(p.struct), nblocks, c_s, c_z,
                                                   hidden, code, ctypes.byref(n)))
     return n.value
@@ -510,8 +510,18 @@ def nt_pair_block_rect(p: Partition, s_rows, s_cols, weights, s_out=None, z_out=
 _WEIGHT_NAMES = ("Wa", "Wb", "W1", "W2", "Wo")
 
 
+_CODES = {"bfloat16": NT_BF16, "bf16": NT_BF16, "float32": NT_F32, "float": NT_F32,
+          "fp32": NT_F32, "f32": NT_F32}
+
+
 def _code(dtype) -> int:
-    return dtype if isinstance(dtype, int) else (NT_BF16 if "bfloat16" in str(dtype) else NT_F32)
+    """The code of a dtype, of its name, or the code itself."""
+    if isinstance(dtype, int):
+        return dtype
+    code = _CODES.get(str(dtype).rpartition(".")[2].rstrip("'>"))  # torch's and numpy's prefixes
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype}; use torch.bfloat16 or torch.float32")
+    return code
 
 
 def nt_loss_workspace_bytes(p: Partition) -> int:
