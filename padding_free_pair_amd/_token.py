@@ -256,11 +256,12 @@ def nt_token_loss(x, W, targets, scale: float = 1.0, nll=None, lse=None, workspa
 
 def nt_token_loss_backward(x, W, targets, lse, g_nll, g_lse=None, scale: float = 1.0, g_x=None,
                            g_W=None, accumulate: bool = False, weight_grad: bool = True,
-                           workspace=None, stream=None):
+                           workspace=None, stream=None, x_grad: bool = True):
     """Gradients of nt_token_loss for g_nll = dL/dnll and, optionally, g_lse =
     dL/dlse (float32 [tokens]) from its inputs and lse; returns (g_x, g_W), g_x in
     x's dtype, g_W float32 [vocabulary, width], added to the given one with
-    accumulate (None with weight_grad False)."""
+    accumulate. With x_grad (x is nobody's output) or weight_grad (W is kept) False
+    that one is None and not computed."""
     torch, lib = _load()
     code, dev, f32 = _dtype_code(x), x.device, torch.float32
     T, V, C = _loss_inputs(torch, dev, x, W, targets)
@@ -270,12 +271,16 @@ def nt_token_loss_backward(x, W, targets, lse, g_nll, g_lse=None, scale: float =
         raise ValueError("accumulate needs g_W")
     if g_W is not None and not weight_grad:
         raise ValueError("g_W without weight_grad")
+    if g_x is not None and not x_grad:
+        raise ValueError("g_x without x_grad")
+    if not (x_grad or weight_grad):
+        raise ValueError("neither x_grad nor weight_grad: nothing to compute")
     with _on(torch, dev, stream) as s:
         need = _bytes("nt_token_loss_backward_workspace_bytes", T, V, C, code)
-        if g_x is None:
-            g_x = torch.empty_like(x)
-        else:
+        if g_x is not None:
             _expect(dev, "g_x", g_x, (T, C), x.dtype)
+        elif x_grad:
+            g_x = torch.empty_like(x)
         if g_W is not None:
             _expect(dev, "g_W", g_W, (V, C), f32)
         elif weight_grad:

@@ -78,6 +78,28 @@ def test_loss_gradient_at_the_target(nt):
     _check_gradients(nt, x, x64, W, W64, ids, lse, "bf16", rng)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,V,C", [(1, 300, 64), (33, 130, 8), (257, 128, 1032), (90, 3000, 64)])
+def test_loss_gradient_of_the_weights_alone(nt, T, V, C, dtype):
+    """Without g_x the weights' gradient has the same bits, added or not."""
+    announce(f"loss backward without g_x T={T} V={V} C={C} {dtype}")
+    rng = np.random.default_rng(T)
+    x, x64, W, W64, ids = _loss_inputs(rng, T, V, C, dtype)
+    lse = nt.nt_token_loss(x, W, _ids(ids))[1]
+    g = torch.randn(T, device="cuda")
+    for old in (None, torch.randn((V, C), device="cuda")):
+        a, b = (None, None) if old is None else (old.clone(), old.clone())
+        more = old is not None
+        _, want = nt.nt_token_loss_backward(x, W, _ids(ids), lse, g, g_W=a, accumulate=more)
+        none, got = nt.nt_token_loss_backward(x, W, _ids(ids), lse, g, g_W=b, accumulate=more,
+                                              x_grad=False)
+        assert none is None
+        np.testing.assert_array_equal(bits(got, torch), bits(want, torch))
+    for refused in (dict(x_grad=False, weight_grad=False), dict(x_grad=False, g_x=torch.empty_like(x))):
+        with pytest.raises(ValueError):
+            nt.nt_token_loss_backward(x, W, _ids(ids), lse, g, **refused)
+
+
 # ---------------------------------------------------------------------- norm
 @pytest.mark.parametrize("group", [0, 64])
 def test_residual_norm_8bit_smallest_scales(nt, group):
