@@ -17,6 +17,7 @@
 // Nothing is added with atomics; sums have one order.
 #include "nt_internal.hpp"
 #include "nt_product_tile.hpp"
+#include "nt_token_loss_plan.hpp"
 
 #include <math.h>
 
@@ -25,7 +26,8 @@
 namespace nt {
 namespace {
 
-constexpr int kMostSplits = 16;
+using namespace token_loss;
+
 constexpr int kTlListThreads = 1024;
 constexpr int64_t kTlListChunk = 4 * kTlListThreads;  // targets of a workgroup of the list
 
@@ -287,9 +289,6 @@ __global__ __launch_bounds__(256) void k_tl_join(const float2* part, const float
 // Where it ends: 32 tokens here and 33 in tiles take 36 and 53 us over 32,000 words of
 // 2,048, 13.5 and 17.5 over 4,099 of 384, 228 and 231 over 131,072 of 4,096; in fp32 72 and
 // 99, 13.6 and 19.7, 475 and 626.
-constexpr int kThinTokens = 32;
-constexpr int kThinWaves = 4;
-constexpr int kThinBlocks = 1024;  // of a launch, four for each compute unit
 
 // Of the calling wave's lanes, whether the lane's token has a target, and its place among those.
 struct TlFew {
@@ -861,8 +860,6 @@ __global__ void k_tl_fill(float* p, int64_t n) {
     p[i] = 0.0f;
 }
 
-int64_t up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
-int64_t tiles_of(int64_t x, int64_t tile) { return (x + tile - 1) / tile; }
 // Workgroups of a kernel that walks on with its grid.
 uint32_t blocks_of(int64_t x, int64_t each) {
   return (uint32_t)std::min<int64_t>(tiles_of(x, each), 1 << 16);
@@ -879,140 +876,6 @@ template <> struct Tiles<float> {
   typedef PtShape<float, 4, 4, 2, 2> Large;  // 128 x 128, 4 waves, two of them
   typedef PtShape<float, 2, 2, 2, 2> Small;  // 64 x 64, 4 waves, four of them
 };
-
-constexpr int64_t kCus = 256;
-constexpr int64_t kPieceBytes = int64_t(512) << 20;  // of d, and of the copy of the piece's rows of W
-constexpr int64_t kSumsBytes = int64_t(256) << 20;   // of the parts of g_x or g_W, where there are
-
-// How a product of m x n results over k is cut: its tile, and the workgroups launched,
-// which cut k into parts where there are more of them than tiles.
-struct Cut {
-  bool large;
-  int tile;
-  int64_t launched;
-  double cost;
-};
-
-// The cheaper tile, counted in steps of k that a compute unit spends on a small tile:
-// whole rounds of all units (in fp32 and half a one: tokens without a target leave the last
-// one fuller or emptier, and the small tile costs little more), 4 for a large tile and 1.3
-// for a small one (measured in bf16: 1,430 and 1,115 TFLOP/s where the rounds are full;
-// fp32: 129 and 122, 1.07), a tile's beginning and end as 300 steps more (fp32: 40), and the
-// results' way through memory, `bytes` each and 8 more for each part where there are several, at 4 TB/s. fp32, 1,866 tokens, half of
-// them without a target, over 4,099 words of 384, gradient: 140 us by this rule, 196 in
-// large tiles.
-Cut cut_of(int64_t m, int64_t n, int64_t k, double bytes, bool narrow, bool split) {
-  Cut best = {};
-  const double step = narrow ? 5.9e-9 : 1.4e-8;  // seconds
-  const int64_t bk = narrow ? 64 : 32;
-  for (int large = 0; large < 2; ++large) {
-    const int64_t tile = (narrow ? 128 : 64) << large;
-    const int64_t tiles = tiles_of(m, tile) * tiles_of(n, tile);
-    // as many workgroups as there is room for at a time
-    const int64_t room = kCus * (large ? (narrow ? 1 : 2) : (narrow ? 2 : 4));
-    const int64_t launched = split ? std::max(up(tiles, 8), room) : up(tiles, 8);
-    int64_t s = std::min<int64_t>(launched / up(tiles, 8), std::min<int64_t>(kMostSplits, k / (8 * bk)));
-    if (s < 1) s = 1;
-    const double cost = ((double)tiles_of(tiles * s, kCus) + (narrow ? 0.0 : 0.5)) *
-                            (large ? 4.0 : narrow ? 1.3 : 1.07) *
-                            ((double)tiles_of(k, s) + (narrow ? 300.0 : 40.0)) +
-                        (double)m * (double)n * ((s > 1 ? (double)s * 8.0 : 0.0) + bytes) / 4e12 / step;
-    if (!large || cost < best.cost) best = {large != 0, (int)tile, launched, cost};
-  }
-  return best;
-}
-
-struct Plan {
-  int64_t tokens, padded, piece, planes, ldv, ldt, x_budget;
-  int w_most;
-  Cut logits, singles, weights;
-  // the workspace
-  size_t rows, live, part, at, x, xT, WT, d, x_sums, w_sums, total;
-};
-
-// Tokens of a pass: an array of them spans 4 GiB at most, and the statistics of 128
-// rows of the vocabulary each 512 MiB (or those of 256 tokens).
-int64_t pass_of(int64_t T, int64_t V) {
-  const int64_t most = (int64_t(1) << 26) / tiles_of(V, 128) / 256 * 256;
-  return std::min(T, std::max<int64_t>(256, std::min<int64_t>(most, 1 << 16)));
-}
-
-bool thin(int64_t T) { return T <= kThinTokens; }
-int thin_blocks(int64_t V) { return (int)std::min<int64_t>(tiles_of(V, 16 * kThinWaves), kThinBlocks); }
-
-Plan forward_plan(int64_t T, int64_t V, int64_t C, nt_dtype dtype) {
-  Plan p = {};
-  p.tokens = pass_of(T, V);
-  p.logits = cut_of(V, p.tokens, C, 0.0, dtype == NT_BF16, false);
-  size_t at = 0;
-  if (thin(T)) {
-    p.at = at; at = align256(at + sizeof(float) * T);
-    p.part = at; at = align256(at + sizeof(float2) * T * thin_blocks(V));
-    p.total = at;
-    return p;
-  }
-  p.rows = at; at = align256(at + sizeof(int32_t) * p.tokens);
-  p.live = at; at = align256(at + sizeof(int64_t));
-  p.at = at; at = align256(at + sizeof(float) * p.tokens);
-  p.part = at; at = align256(at + sizeof(float2) * p.tokens * tiles_of(V, p.logits.tile));
-  p.total = at;
-  return p;
-}
-
-Plan backward_plan(int64_t T, int64_t V, int64_t C, nt_dtype dtype) {
-  Plan p = {};
-  const bool narrow = dtype == NT_BF16;
-  const int64_t es = narrow ? 2 : 4;
-  p.tokens = pass_of(T, V);
-  p.padded = up(p.tokens, 256);
-  p.planes = narrow ? 2 : 1;  // of d
-  // Rows of a power of two of bytes would put the same values of k of all rows in one
-  // channel of the cache: a line more
-  const int64_t line = 128 / es;
-  p.ldt = p.padded + line;
-  // rows that both the piece's arrays hold: many tokens make d the larger one, few the copy of W
-  const int64_t rows = std::min(kPieceBytes / (p.ldt * es * p.planes), kPieceBytes / (C * es) - line);
-  const int64_t most = std::max<int64_t>(256, rows / 256 * 256);
-  // the number of pieces, from the least one on, that fills whole rounds best
-  double best = 0.0;
-  for (int64_t pieces = tiles_of(V, most), last = pieces + 8; pieces < last; ++pieces) {
-    const int64_t piece = up(tiles_of(V, pieces), 256), n = std::min(piece, V);
-    const Cut l = cut_of(n, p.tokens, C, (double)(es * p.planes), narrow, false);
-    const Cut x = cut_of(C, p.tokens, p.planes * n, 8.0, narrow, true);
-    const Cut w = cut_of(C, n, p.planes * p.tokens, 4.0, narrow, true);
-    const double cost = (double)tiles_of(V, piece) * (l.cost + x.cost + w.cost);
-    if (!p.piece || cost < best) {
-      best = cost;
-      p.piece = piece;
-      p.logits = l;
-      p.singles = x;
-      p.weights = w;
-    }
-  }
-  p.ldv = p.piece + line;
-  const int64_t numbers = kSumsBytes / (int64_t)sizeof(float);
-  // room for all parts that the workgroups allow, or for 256 MiB of them (fewer tokens with
-  // a target allow more parts of fewer rows, which take no more room)
-  const int64_t x_tiles = tiles_of(C, p.singles.tile) * tiles_of(p.tokens, p.singles.tile);
-  const int64_t x_parts = std::min<int64_t>(kMostSplits, p.singles.launched / up(x_tiles, 8));
-  p.x_budget = std::max(p.padded * C, std::min(x_parts * p.padded * C, numbers));
-  const int64_t w_tiles = tiles_of(C, p.weights.tile) * tiles_of(std::min(p.piece, V), p.weights.tile);
-  const int64_t w_rows = std::min(p.piece, V) * C;
-  p.w_most = (int)std::max<int64_t>(
-      1, std::min(std::min<int64_t>(kMostSplits, p.weights.launched / up(w_tiles, 8)), numbers / w_rows));
-  size_t at = 0;
-  p.rows = at; at = align256(at + sizeof(int32_t) * p.tokens);
-  p.live = at; at = align256(at + sizeof(int64_t));
-  p.x = at; at = align256(at + es * p.padded * C);
-  p.xT = at; at = align256(at + es * p.ldt * C);
-  p.WT = at; at = align256(at + es * p.ldv * C);
-  p.d = at; at = align256(at + es * p.planes * p.ldt * p.piece);
-  p.x_sums = at; at = align256(at + sizeof(float) * p.x_budget);
-  p.w_sums = at;
-  if (p.w_most > 1) at = align256(at + sizeof(float) * p.w_most * w_rows);
-  p.total = at;
-  return p;
-}
 
 hipError_t list(const int32_t* targets, int64_t tokens, int32_t* rows, int64_t* live, float* nll,
                 float* lse, hipStream_t s) {
@@ -1055,7 +918,7 @@ template <typename T>
 hipError_t forward(const T* x, const T* W, const int32_t* targets, float* nll, float* lse,
                    int64_t T_, int64_t V, int C, float scale, char* ws, nt_dtype dtype,
                    hipStream_t s) {
-  const Plan p = forward_plan(T_, V, C, dtype);
+  const Plan p = forward_plan(T_, V, C, dtype == NT_BF16);
   if (thin(T_)) return forward_thin(x, W, targets, nll, lse, (int)T_, V, C, scale, ws, p, s);
   int32_t* rows = reinterpret_cast<int32_t*>(ws + p.rows);
   int64_t* live = reinterpret_cast<int64_t*>(ws + p.live);
@@ -1173,7 +1036,7 @@ hipError_t backward(const void* x, const void* W, const int32_t* targets, const 
                     const float* g_nll, const float* g_lse, void* g_x, float* g_W, int64_t tokens,
                     int64_t V, int C, float scale, bool accumulate, void* ws, nt_dtype dtype,
                     hipStream_t s) {
-  const Plan p = backward_plan(tokens, V, C, dtype);
+  const Plan p = backward_plan(tokens, V, C, dtype == NT_BF16);
   for (int64_t t = 0; t < tokens; t += p.tokens) {
     const hipError_t e = backward<T>(
         p, static_cast<const T*>(x) + t * C, static_cast<const T*>(W), targets + t, lse + t,
@@ -1187,11 +1050,11 @@ hipError_t backward(const void* x, const void* W, const int32_t* targets, const 
 }  // namespace
 
 size_t token_loss_ws_bytes(int64_t tokens, int64_t V, int C, nt_dtype dtype) {
-  return tokens ? forward_plan(tokens, V, C, dtype).total : 0;
+  return tokens ? forward_plan(tokens, V, C, dtype == NT_BF16).total : 0;
 }
 
 size_t token_loss_backward_ws_bytes(int64_t tokens, int64_t V, int C, nt_dtype dtype) {
-  return tokens ? backward_plan(tokens, V, C, dtype).total : 0;
+  return tokens ? backward_plan(tokens, V, C, dtype == NT_BF16).total : 0;
 }
 
 hipError_t launch_token_loss(const void* x, const void* W, const int32_t* targets, float* nll,

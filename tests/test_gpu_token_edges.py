@@ -9,6 +9,7 @@ import pytest
 import oracle
 import token_bounds as tb
 from gpu_util import announce, bits, f64
+from token_cases import LOSS_PLANS
 from test_gpu_token import _check_loss, _dev, _ids, _loss_inputs, _within, nt  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -76,6 +77,30 @@ def test_loss_gradient_at_the_target(nt):
     ids = rng.integers(0, V, size=T)
     lse = nt.nt_token_loss(x, W, _ids(ids))[1]
     _check_gradients(nt, x, x64, W, W64, ids, lse, "bf16", rng)
+
+
+@pytest.mark.parametrize("name", LOSS_PLANS)
+def test_loss_of_many(nt, name):
+    """Large tiles with partial ones at both ends, pieces of the vocabulary with a short last
+    one (parts of whose rows are empty), passes over the tokens: forward and both gradients,
+    with targets in every piece, added to an old one."""
+    T, V, C, dtype, absent, said = LOSS_PLANS[name]
+    announce(f"loss of many, {name}: T={T} V={V} C={C} {dtype}")
+    rng = np.random.default_rng(T + V)
+    x, x64, W, W64, ids = _loss_inputs(rng, T, V, C, dtype, absent=absent)
+    piece, pieces = said.get("piece", 1024), said.get("pieces", 1)
+    if pieces > 1:  # the first and the last word of every piece
+        edges = np.r_[np.arange(pieces) * piece, np.arange(1, pieces) * piece - 1, V - 1]
+        ids[rng.choice(60000, size=len(edges), replace=False)] = edges
+        ids[T - 1] = V - 2
+    lse = _check_loss(nt, x, x64, W, W64, ids, 1.0, dtype)
+    g_nll, _, g_x, g_W = _check_gradients(nt, x, x64, W, W64, ids, lse, dtype, rng, both=True,
+                                          accumulate=True)
+    a = nt.nt_token_loss_backward(x, W, _ids(ids), lse, g_nll)
+    alone = (nt.nt_token_loss_backward(x, W, _ids(ids), lse, g_nll, weight_grad=False)[0],
+             nt.nt_token_loss_backward(x, W, _ids(ids), lse, g_nll, x_grad=False)[1])
+    for p, q in zip(a, alone):
+        np.testing.assert_array_equal(bits(p, torch), bits(q, torch))
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
