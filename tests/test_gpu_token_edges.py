@@ -155,3 +155,140 @@ def test_residual_norm_8bit_smallest_scales(nt, group):
     codes = nt.nt_residual_norm_8bit(x, eps=1.0, group=group)[0].float()
     assert bool(torch.isnan(codes[3]).all())  # the row's mean of squares
     assert bool(torch.isnan(codes[8, 70])) and bool((codes[8, :70] == 0).all())
+
+
+# ------------------------------------------------- workspaces, graphs, streams
+def _sorted_step(nt, table, tokens, few, w, out, workspaces=(None, None, None)):
+    """The operators in the forms that keep state in a workspace: the embedding's gradient by
+    sorted tokens, the loss of few tokens, the norm's weights."""
+    T, (V, C) = tokens.shape[0], table.shape
+    assert nt.nt_token_embedding_backward_workspace_bytes(T, V, C) > 0  # sorted, not direct
+    assert few.shape[0] <= 32
+    s0 = nt.nt_token_embedding(table, tokens.clamp(max=V - 1), scale=2.0)
+    y, h = nt.nt_residual_norm(s0, w, residual=s0)
+    nll, lse = nt.nt_token_loss(y[:few.shape[0]], table, few, workspace=workspaces[0])
+    g, g_w = nt.nt_residual_norm_backward(h, y, w, workspace=workspaces[1])
+    g_table = nt.nt_token_embedding_backward(tokens, g, V, g_table=out, workspace=workspaces[2])
+    more = nt.nt_token_embedding_backward(tokens, y, V, g_table=g_table.clone(), accumulate=True,
+                                          workspace=workspaces[2])
+    return nll, lse, g_w, g_table, more
+
+
+def _sorted_inputs(dtype, V, C, T, n):
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    table = (torch.randn((V, C), device="cuda") * 0.3).to(dt)
+    w = torch.ones(C, device="cuda")
+    return table, w, _tokens_of(V, T), torch.randint(-1, V, (n,), device="cuda", dtype=torch.int32)
+
+
+def _tokens_of(V, T):
+    """Frequent, rare and absent tokens, and some that the table does not hold."""
+    ids = torch.randint(-3, V, (T,), device="cuda", dtype=torch.int32)
+    ids[::3] = V // 2
+    ids[1::7] = V + 5
+    return ids
+
+
+def _same_bits(got, want):
+    for a, b in zip(got, want):
+        np.testing.assert_array_equal(bits(a, torch), bits(b, torch))
+
+
+SORTED = [(6000, 136, 700, 20), (9, 64, 5000, 16), (70001, 24, 4500, 32)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V,C,T,n", SORTED)
+def test_sorted_and_few_captured_and_replayed(nt, V, C, T, n, dtype):
+    """Replays on new inputs, with eager calls and synchronizations between, as eager calls."""
+    announce(f"captured V={V} C={C} T={T} {dtype}")
+    torch.manual_seed(V)
+    table, w, tokens, few = _sorted_inputs(dtype, V, C, T, n)
+    out = torch.empty((V, C), device="cuda")
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        for _ in range(2):
+            _sorted_step(nt, table, tokens, few, w, out)
+    torch.cuda.current_stream().wait_stream(stream)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = _sorted_step(nt, table, tokens, few, w, out)
+    for k in range(4):
+        tokens.copy_(_tokens_of(V, T) if k % 2 else torch.full_like(tokens, k - 2))
+        few.copy_(torch.randint(-1, V, (n,), device="cuda", dtype=torch.int32))
+        table.copy_(torch.randn((V, C), device="cuda") * 0.3)
+        graph.replay()
+        torch.cuda.synchronize()
+        held = [t.clone() for t in got]
+        _same_bits(held, _sorted_step(nt, table, tokens, few, w, torch.empty_like(out)))
+
+
+def test_sorted_and_few_on_two_streams(nt):
+    """Two streams at once, each call with a workspace of its own."""
+    torch.manual_seed(3)
+    V, C, T, n = 6000, 136, 3000, 32
+    table, w, _, _ = _sorted_inputs("bf16", V, C, T, n)
+    batches = [_sorted_inputs("bf16", V, C, T, n)[2:] for _ in range(2)]
+    want = [_sorted_step(nt, table, *b, w, None) for b in batches]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in batches], []
+    for b, s in zip(batches, streams):
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            got.append([_sorted_step(nt, table, *b, w, None) for _ in range(5)][-1])
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        _same_bits(a, b)
+
+
+def test_workspaces_shared_by_graphs_and_sizes(nt):
+    """One workspace for calls of different sizes in turn, eager ones and two graphs that hold
+    it, on one stream: nothing that another call left in it is taken for its own."""
+    torch.manual_seed(4)
+    cases = [_sorted_inputs("bf16", 6000, 136, 3000, 32), _sorted_inputs("f32", 9, 64, 5000, 7)]
+    # torch's allocations are 512 bytes apart, so any size is aligned
+    ws = [torch.empty(1 << 24, dtype=torch.uint8, device="cuda").fill_(255) for _ in range(3)]
+    step = lambda c: _sorted_step(nt, c[0], c[2], c[3], c[1], None, ws)  # noqa: E731
+    want = [[t.clone() for t in _sorted_step(nt, c[0], c[2], c[3], c[1], None)] for c in cases]
+    graphs = []
+    for c in cases:
+        stream = torch.cuda.Stream()
+        stream.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(stream):
+            step(c)
+        torch.cuda.current_stream().wait_stream(stream)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = step(c)
+        graphs.append((graph, got))
+    for k in range(4):
+        for c, (graph, got), ref in zip(cases, graphs, want):
+            graph.replay()
+            held = [t.clone() for t in got]
+            torch.cuda.synchronize()
+            _same_bits(held, ref)
+            if k % 2:
+                _same_bits(step(c), ref)
+            if k == 2:
+                for t in ws:
+                    t.fill_(255)
+
+
+def test_loss_workspace_of_sizes_in_turn(nt):
+    """The loss and its gradient in one workspace after larger and smaller calls, and after
+    NaN in all of it."""
+    rng = np.random.default_rng(2)
+    sizes = [(700, 1301, 128, "bf16"), (33, 300, 64, "bf16"), (20, 1000, 64, "f32"),
+             (257, 128, 72, "f32"), (300, 900, 200, "bf16")]
+    need = max(nt.nt_token_loss_backward_workspace_bytes(*s) for s in sizes)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    ws.fill_(255)
+    for T, V, C, dtype in sizes * 2:
+        x, _, W, _, ids = _loss_inputs(rng, T, V, C, dtype)
+        g = torch.randn(T, device="cuda")
+        a = nt.nt_token_loss(x, W, _ids(ids))
+        b = nt.nt_token_loss(x, W, _ids(ids), workspace=ws)
+        _same_bits(b, a)
+        _same_bits(nt.nt_token_loss_backward(x, W, _ids(ids), a[1], g, workspace=ws),
+                   nt.nt_token_loss_backward(x, W, _ids(ids), a[1], g))
