@@ -39,8 +39,19 @@ struct Cut {
 // for a small one (measured in bf16: 1,430 and 1,115 TFLOP/s where the rounds are full;
 // fp32: 129 and 122, 1.07), a tile's beginning and end as 300 steps more (fp32: 40), and the
 // results' way through memory, `bytes` each and 8 more for each part where there are
-// several, at 4 TB/s. fp32, 1,866 tokens, half of them without a target, over 4,099 words
-// of 384, gradient: 140 us by this rule, 196 in large tiles.
+// several, at 4 TB/s. Measured at 13 sizes in fp32 and 18 in bf16 (256 to 8,007 tokens, all of
+// them or half with a target, 1,000 to 32,000 words of 256 to 2,048), forward and gradient, by
+// this rule, in large tiles and in small ones, in us:
+//   fp32, 1,866 (half) over 4,099 of 384: gradient 139, 188, 137; forward 44, 66, 44
+//   fp32, 500 over 32,000 of 1,024:       gradient 915, 925, 933; forward 294, 273, 294
+//   fp32, 4,000 over 16,000 of 256:       gradient 980, 946, 913; forward 306, 307, 311
+//   bf16, 1,000 over 16,000 of 384:       gradient 139, 155, 142; forward 28, 27, 36
+//   bf16, 4,096 over 8,000 of 2,048:      gradient 592, 580, 787; forward 114, 115, 165
+//   bf16, 2,272 (half) over 8,000 of 2,048: gradient 248, 235, 313; forward 80, 55, 80
+// The last one is the rule's worst; elsewhere it is within 15 % of the better tile in bf16
+// and 8 % in fp32. The half round is fp32's alone: without it the forward of the first size
+// takes 66, and with it in bf16 gradients take up to 27 % longer (4,096 over 8,000: 750) and
+// forwards up to 38 %, as large tiles gain a third there and next to nothing in fp32.
 inline Cut cut_of(int64_t m, int64_t n, int64_t k, double bytes, bool narrow, bool split) {
   Cut best = {};
   const double step = narrow ? 5.9e-9 : 1.4e-8;  // seconds
