@@ -843,9 +843,10 @@ nt_status nt_token_embedding_backward(const int32_t* tokens, const void* g_out, 
 
 /*
  * h = x + residual, rounded to `dtype`, and y = h / sqrt(mean_c h^2 + eps) * w of
- * the rounded h, with fp32 statistics, rounded once. x, residual, h, y: [rows,
- * C]; w: fp32 [C]. residual NULL: h is x (its pointer is not read); w NULL: no
- * weight. h may be x or residual, y may be x or residual where h is not.
+ * the rounded h, with fp32 statistics, rounded once: the sum of a row's squares has
+ * to stay within fp32 (values up to 10^17 do; past its range y and the gradient are zero).
+ * x, residual, h, y: [rows, C]; w: fp32 [C]. residual NULL: h is x (its pointer is not
+ * read); w NULL: no weight. h may be x or residual, y may be x or residual where h is not.
  */
 nt_status nt_residual_norm(const void* x, const void* residual, const float* w, void* h, void* y,
                            int64_t rows, int32_t C, float eps, nt_dtype dtype, void* stream);

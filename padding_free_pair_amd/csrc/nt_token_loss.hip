@@ -728,8 +728,8 @@ __device__ __forceinline__ void tl_store(const PtSums<S>& acc, float* to, int64_
   }
 }
 
-// The products reach 1,220 (g_x, 430 us a piece of 16,128 rows) and 1,250 TFLOP/s (g_W, 850 us
-// for hi and lo) at 8,007 tokens of 2,048 in bf16, the matrix cores busy for 59 and 61 %.
+// Either product reaches 1,250 TFLOP/s (840 us a piece of 16,128 rows, for hi and lo) at 8,007
+// tokens of 2,048 in bf16, the matrix cores busy for 59 to 60 % of the cycles.
 //
 // The product of g_x, sums[split][t][c] (+)= sum over the split's rows v of the piece of
 // d[t, v] W[v, c], d as hi and lo in turn, and that of g_W: both sides of a launch and of its
