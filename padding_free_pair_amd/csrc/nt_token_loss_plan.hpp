@@ -52,9 +52,10 @@ struct Cut {
 // and 8 % in fp32. The half round is fp32's alone: without it the forward of the first size
 // takes 66, and with it in bf16 gradients take up to 27 % longer (4,096 over 8,000: 750) and
 // forwards up to 38 %, as large tiles gain a third there and next to nothing in fp32.
+inline double step_of(bool narrow) { return narrow ? 5.9e-9 : 1.4e-8; }  // seconds
 inline Cut cut_of(int64_t m, int64_t n, int64_t k, double bytes, bool narrow, bool split) {
   Cut best = {};
-  const double step = narrow ? 5.9e-9 : 1.4e-8;  // seconds
+  const double step = step_of(narrow);
   const int64_t bk = narrow ? 64 : 32;
   for (int large = 0; large < 2; ++large) {
     const int64_t tile = (narrow ? 128 : 64) << large;
@@ -123,14 +124,17 @@ inline Plan backward_plan(int64_t T, int64_t V, int64_t C, bool narrow) {
   // rows that both the piece's arrays hold: many tokens make d the larger one, few the copy of W
   const int64_t rows = std::min(kPieceBytes / (p.ldt * es * p.planes), kPieceBytes / (C * es) - line);
   const int64_t most = std::max<int64_t>(256, rows / 256 * 256);
-  // the number of pieces, from the least one on, that fills whole rounds best
+  // the number of pieces, from the least one on, that fills whole rounds best; each is some
+  // launches more, 20 us where the card is not filled (256 tokens over 131,072 words of 8,192 in
+  // bf16: five pieces by this take 4.6 ms, eight without it 5.1)
+  const double launches = 2e-5 / step_of(narrow);
   double best = 0.0;
   for (int64_t pieces = tiles_of(V, most), last = pieces + 8; pieces < last; ++pieces) {
     const int64_t piece = up(tiles_of(V, pieces), 256), n = std::min(piece, V);
     const Cut l = cut_of(n, p.tokens, C, (double)(es * p.planes), narrow, false);
     const Cut x = cut_of(C, p.tokens, p.planes * n, 8.0, narrow, true);
     const Cut w = cut_of(C, n, p.planes * p.tokens, 4.0, narrow, true);
-    const double cost = (double)tiles_of(V, piece) * (l.cost + x.cost + w.cost);
+    const double cost = (double)tiles_of(V, piece) * (l.cost + x.cost + w.cost + launches);
     if (!p.piece || cost < best) {
       best = cost;
       p.piece = piece;
