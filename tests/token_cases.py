@@ -15,8 +15,8 @@ LOSS_PLANS = {
     "pieces and passes": (66100, 5393, 200, "bf16", 0.998,
                           {"tokens": 65536, "logits": 256, "pieces": 6, "last": 273}),
     "pieces f32": (65536, 5393, 64, "f32", 0.998,
-                   {"forward": 128, "logits": 128, "singles": 64, "weights": 64, "pieces": 6,
-                    "piece": 1024, "last": 273}),
+                   {"forward": 128, "logits": 128, "singles": 64, "weights": 64, "pieces": 4,
+                    "piece": 1536, "last": 785}),
     "wide logits f32": (6140, 6130, 8, "f32", 0.01, {"forward": 128, "logits": 128}),
     "wide g_x f32": (36860, 16, 1024, "f32", 0.97, {"singles": 128}),
     "wide g_W f32": (40, 36860, 1024, "f32", 0.0, {"weights": 128}),
