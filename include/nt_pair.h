@@ -844,7 +844,7 @@ nt_status nt_token_embedding_backward(const int32_t* tokens, const void* g_out, 
 /*
  * h = x + residual, rounded to `dtype`, and y = h / sqrt(mean_c h^2 + eps) * w of
  * the rounded h, with fp32 statistics, rounded once: the sum of a row's squares has
- * to stay within fp32 (values up to 10^17 do; past its range y and the gradient are zero).
+ * to stay within fp32 (values up to 10^17 do), here and in the gradient.
  * x, residual, h, y: [rows, C]; w: fp32 [C]. residual NULL: h is x (its pointer is not
  * read); w NULL: no weight. h may be x or residual, y may be x or residual where h is not.
  */
